@@ -15,14 +15,13 @@
 #include <mutex>
 #include <string>
 
-#include "launch.hpp"
-#include "mlp.h"
+#include "host_api.hpp"
 
 using namespace gmlp;
 
-namespace {
+namespace gmlp {
 
-thread_local std::string g_last_error;
+static thread_local std::string g_last_error;
 
 mlp_status fail(mlp_status st, const char* fmt, ...) {
   char buf[512];
@@ -33,6 +32,10 @@ mlp_status fail(mlp_status st, const char* fmt, ...) {
   g_last_error = buf;
   return st;
 }
+
+}  // namespace gmlp
+
+namespace {
 
 // ---- one-shot stage timing (mlp_time_stage_once) ----------------------------------------------
 
@@ -57,40 +60,14 @@ struct StageScope {
   }
 };
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
-
-constexpr size_t kAlign = 256;
-size_t round_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
-
-int esize(int dtype) { return dtype == MLP_F32 ? 4 : 2; }
-
-bool is_gated(int act) {
-  return act == MLP_ACT_SWIGLU || act == MLP_ACT_GEGLU || act == MLP_ACT_REGLU || act == MLP_ACT_GLU;
-}
-
-// The epilogues' function of an mlp_act: the gate function of a gated one, else f itself.
-int act_fn_of(int act) {
-  switch (act) {
-    case MLP_ACT_SWIGLU: return FN_SILU;
-    case MLP_ACT_GEGLU: case MLP_ACT_GELU_TANH: return FN_GELU_TANH;
-    case MLP_ACT_REGLU: case MLP_ACT_RELU: return FN_RELU;
-    case MLP_ACT_GLU: return FN_SIGMOID;
-    default: return FN_RELU_SQ;
-  }
-}
-DType dtype_of(int dtype) { return dtype == MLP_BF16 ? DT_BF16 : dtype == MLP_F16 ? DT_F16 : DT_F32; }
 DType io_of(const mlp_desc* d) { return dtype_of(d->dtype); }
 
 // ---- GEMM planning -------------------------------------------------------------------------
 
-struct Plan {
-  TileShape tile;
-  int splits, k_per_split, tiles_m, tiles_n, group_m, grid;
-  double est;   // the planner's time model of this plan, seconds
-};
+}  // namespace
 
-struct TileInfo { TileShape t; int bm, bn, slots; double eff; };
+namespace gmlp {
+
 // slots: workgroups per CU that fit in LDS (a 2-stage 256x256 ring takes 128 KiB, a 3-stage
 // 256x128 one 144 KiB, a 2-stage 128x128 one 64 KiB). eff: the fraction of a CU's peak MFMA rate
 // one K-step of the tile sustains with every CU busy, measured per K-step on the bf16 GEMMs of
@@ -102,7 +79,7 @@ struct TileInfo { TileShape t; int bm, bn, slots; double eff; };
 // 8-wave 256x128 figure was refitted later from forced-plan runs: the LLaMA down projection
 // unsplit in 256 such tiles (one round, no reduce) runs 156 us against 164 for split-K 2 over
 // 256x256 tiles plus the reduce, i.e. 0.40 of the per-CU peak.
-const TileInfo kTiles[] = {
+const TileInfo kTiles[kTileInfos] = {
     {TILE_256x256_W8, 256, 256, 1, 0.44},   // 8 waves: two per SIMD hide each other's stalls
     {TILE_256x256, 256, 256, 1, 0.40},
     {TILE_256x128, 256, 128, 1, 0.33},
@@ -110,12 +87,11 @@ const TileInfo kTiles[] = {
     {TILE_128x128, 128, 128, 2, 0.36},
 };
 
-bool is_fp8(DType in) { return in == DT_E4M3 || in == DT_F8G; }
 int bk_of(DType in) { return is_fp8(in) ? 128 : (in == DT_F32 ? 32 : 64); }
 
 // gated: N counts hidden units and a tile covers bn/2 of them (gate + up rows). only_tile >= 0
 // restricts the choice to that tile shape.
-Plan plan_gemm(DType in, int64_t M, int64_t N, int64_t K, bool allow_split, bool gated, int only_tile = -1) {
+Plan plan_gemm(DType in, int64_t M, int64_t N, int64_t K, bool allow_split, bool gated, int only_tile) {
   const int bk = bk_of(in);
   const double per_cu = (is_fp8(in) ? 2.0 : in == DT_F32 ? 1.0 / 16.0 : 1.0) * 9.83e12;
   Plan best{};
@@ -177,12 +153,6 @@ size_t partial_bytes(const Plan& p, int64_t M, int64_t N) {
 // the chip or smaller tiles do (GPT shape: 510 tiles of 48 K-steps, then the other 5632 rows as
 // 132 tiles of 8-wave 256 x 128, one round).
 // A static form of what a stream-K schedule does for the last round. m1 = 0: `main` covers all.
-struct RowsPlan {
-  Plan main{};
-  int64_t m1 = 0;
-  Plan tail{};
-};
-
 RowsPlan plan_rows(DType in, int64_t M, int64_t N, int64_t K) {
   RowsPlan r;
   r.main = plan_gemm(in, M, N, K, true, false);
@@ -208,6 +178,10 @@ size_t partial_bytes(const RowsPlan& r, int64_t M, int64_t N) {
   return r.m1 ? std::max(partial_bytes(r.main, r.m1, N), partial_bytes(r.tail, M - r.m1, N))
               : partial_bytes(r.main, M, N);
 }
+
+}  // namespace gmlp
+
+namespace {
 
 // ---- workspace layout ----------------------------------------------------------------------
 
@@ -311,6 +285,10 @@ GemmDims bwd_dims(const mlp_desc* d, int which) {
   }
 }
 
+}  // namespace
+
+namespace gmlp {
+
 // Makespan, in K-steps, of list-scheduling the members' tiles on one XCD (it takes every 8th
 // workgroup of each member, in launch order): each tile goes to the first of the 32 CUs to free
 // up and holds it for its K-steps plus `overhead` (prologue and epilogue).
@@ -321,6 +299,10 @@ double list_makespan(const int64_t* tiles, const int64_t* steps, int count, doub
       *std::min_element(cu.begin(), cu.end()) += (double)steps[j] + overhead;
   return *std::max_element(cu.begin(), cu.end());
 }
+
+}  // namespace gmlp
+
+namespace {
 
 // One launch of the products `ids` (at least two), when the time model prefers it to launching
 // them one after another (each planned by plan_gemm: split-K allowed for the weight gradients and
@@ -479,7 +461,11 @@ mlp_status check_desc(const mlp_desc* d) {
   return MLP_OK;
 }
 
-mlp_status need_ptr(const void* p, const char* name, bool align = true) {
+}  // namespace
+
+namespace gmlp {
+
+mlp_status need_ptr(const void* p, const char* name, bool align) {
   if (!p) return fail(MLP_ERR_INVALID_ARG, "%s is NULL", name);
   if (align && !aligned16(p)) return fail(MLP_ERR_ALIGNMENT, "%s is not 16-byte aligned", name);
   if (!align && !aligned4(p)) return fail(MLP_ERR_ALIGNMENT, "%s is not 4-byte aligned", name);
@@ -490,11 +476,9 @@ mlp_status need_null(const void* p, const char* name, const char* why) {
   return p ? fail(MLP_ERR_INVALID_ARG, "%s must be NULL %s", name, why) : MLP_OK;
 }
 
-#define MLP_TRY(expr)                 \
-  do {                                \
-    const mlp_status st_ = (expr);    \
-    if (st_ != MLP_OK) return st_;    \
-  } while (0)
+}  // namespace gmlp
+
+namespace {
 
 mlp_status check_fp8(const mlp_desc* d, const mlp_fp8* f, bool fwd) {
   if (!d->fp8_fwd) return need_null(f, "fp8", "unless desc->fp8_fwd");
@@ -531,6 +515,10 @@ mlp_status check_ws(const mlp_desc* d, int phase, const void* ws, size_t ws_byte
   return MLP_OK;
 }
 
+}  // namespace
+
+namespace gmlp {
+
 mlp_status hip_status(hipError_t e, const char* what) {
   if (e == hipSuccess) return MLP_OK;
   return fail(MLP_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
@@ -564,6 +552,10 @@ mlp_status gemm(DType in, DType io, Layout lay, int epi, const Plan& p, GemmArgs
   return hip_status(run_gemm(in, io, lay, epi, p.tile, a, p.grid, s), what);
 }
 
+}  // namespace gmlp
+
+namespace {
+
 // A non-split GEMM over output columns [0, N) as two launches when that fills the CUs better:
 // 8-wave 256 x 256 tiles for the columns that make whole rounds of 256 tiles, 8-wave 256 x 128
 // tiles for the rest (one launch's last round otherwise idles part of the chip: the
@@ -592,6 +584,10 @@ mlp_status gemm_cols_split(DType in, DType io, Layout lay, int epi, const Plan& 
   return gemm(in, io, lay, epi, p2, b, M, N - n1, K, nullptr, s, what);
 }
 
+}  // namespace
+
+namespace gmlp {
+
 // A store-epilogue GEMM planned by plan_rows: rows [0, m1) with `main`, then rows [m1, M) with
 // `tail` (A and the output moved down by m1 rows; A is K-major for NT / NN, MN-major for TN).
 mlp_status gemm_rows(DType in, DType io, Layout lay, const RowsPlan& r, GemmArgs a, int64_t M, int64_t N,
@@ -604,6 +600,10 @@ mlp_status gemm_rows(DType in, DType io, Layout lay, const RowsPlan& r, GemmArgs
   b.C0 = static_cast<char*>(a.C0) + r.m1 * a.ldc0 * eo;
   return gemm(in, io, lay, EPI_STORE, r.tail, b, M - r.m1, N, K, partial, s, what);
 }
+
+}  // namespace gmlp
+
+namespace {
 
 GemmArgs base_args(const mlp_desc* d) {
   GemmArgs a{};
