@@ -4,6 +4,9 @@
 The functions below carry the C entry points' names and only marshal arguments: torch tensors
 become device pointers, the current HIP stream is passed along, and a non-OK status raises
 ``MlpError``. Every step of the MLP runs in the library's HIP kernels; there is no other path.
+
+The mixture-of-experts operators (``include/moe.h``: router, tokens by expert and back, linear layer,
+experts' products) are in ``moe.py`` and reached from here by the same names.
 """
 from __future__ import annotations
 
@@ -17,6 +20,9 @@ from ._lib import (  # noqa: F401
     MLP_FP8_E5M2, MLP_GATE_INSIDE, MLP_GATE_OUTSIDE,
     MLP_NOALLOC_SCRATCH_BYTES, MLP_PHASE_BWD, MLP_PHASE_FWD, MLP_PHASE_FWD_INFER, MlpDesc, MlpError, MlpFp8, check,
     lib,
+)
+from ._lib import (  # noqa: F401
+    LINEAR_ACT_NONE, LINEAR_BWD, LINEAR_FWD, MOE_MAX_CHOICES, MOE_MAX_EXPERTS, MOE_SIGMOID, MOE_SOFTMAX, LinearDesc,
 )
 
 _ACTS = {"swiglu": MLP_ACT_SWIGLU, "relu_sq": MLP_ACT_RELU_SQ, "geglu": MLP_ACT_GEGLU, "reglu": MLP_ACT_REGLU,
@@ -164,3 +170,9 @@ def mlp_bwd_grouped(desc: MlpDesc) -> int:
 
 def mlp_fp8_next_scale(amax: float, prev_scale: float, gain: float, floor: float) -> float:
     return float(lib().mlp_fp8_next_scale(amax, prev_scale, gain, floor))
+
+
+from .moe import (  # noqa: E402,F401
+    linear_bwd, linear_fwd, linear_workspace_bytes, make_linear_desc, moe_combine, moe_combine_bwd, moe_gather,
+    moe_gather_bwd, moe_route, moe_route_bwd, moe_sort, moe_sort_workspace_bytes,
+)

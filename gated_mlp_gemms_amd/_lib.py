@@ -59,6 +59,34 @@ _SIGNATURES = {
     "mlp_bwd_grouped": (C.c_int, [C.POINTER(MlpDesc), C.POINTER(C.c_int)]),
 }
 
+# moe.h, of the same library
+_I64, _I32 = C.c_int64, C.c_int
+MOE_SOFTMAX, MOE_SIGMOID = 0, 1
+MOE_MAX_EXPERTS, MOE_MAX_CHOICES = 1024, 16
+LINEAR_ACT_NONE = -1
+LINEAR_FWD, LINEAR_BWD = 0, 1
+
+
+class LinearDesc(C.Structure):
+    _fields_ = [("M", C.c_int64), ("K", C.c_int64), ("N", C.c_int64), ("act", C.c_int32), ("dtype", C.c_int32),
+                ("experts", C.c_int32)]
+
+
+_MOE_SIGNATURES = {
+    "moe_route": (C.c_int, [_P, _I32, _I64, _I64, _I64, _I32, _I32, _P, _P, _P]),
+    "moe_route_bwd": (C.c_int, [_P, _P, _P, _I32, _I64, _I64, _I64, _I32, _I32, _P, _P]),
+    "moe_sort_workspace_bytes": (C.c_size_t, [_I64, _I64]),
+    "moe_sort": (C.c_int, [_P, _I64, _I64, _P, _P, _P, _P, C.c_size_t, _P]),
+    "moe_gather": (C.c_int, [_P, _P, _P, _I32, _I64, _I64, _I64, _I64, _P, _P]),
+    "moe_gather_bwd": (C.c_int, [_P, _P, _P, _I32, _I64, _I64, _I64, _I64, _P, _P]),
+    "moe_combine": (C.c_int, [_P, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _I64, _P, _P]),
+    "moe_combine_bwd": (C.c_int, [_P, _P, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _I64, _P, _P, _P]),
+    "linear_workspace_bytes": (C.c_size_t, [C.POINTER(LinearDesc), C.c_int]),
+    "linear_fwd": (C.c_int, [C.POINTER(LinearDesc)] + [_P] * 10 + [C.c_size_t, _P]),
+    "linear_bwd": (C.c_int, [C.POINTER(LinearDesc)] + [_P] * 11 + [_I32, _P, C.c_size_t, _P]),
+    "moe_abi_version": (C.c_int, []),
+}
+
 _lib = None
 
 
@@ -71,7 +99,7 @@ def lib() -> C.CDLL:
                 f"{LIB_PATH} is missing: build it with `python -m gated_mlp_gemms_amd.build` "
                 "(the MLP engine has no non-HIP fallback)")
         handle = C.CDLL(LIB_PATH)
-        for name, (res, args) in _SIGNATURES.items():
+        for name, (res, args) in {**_SIGNATURES, **_MOE_SIGNATURES}.items():
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args

@@ -286,6 +286,50 @@ __device__ __forceinline__ void gated_act_grad(int fn, float gm, int inside, con
   }
 }
 
+// The linear layer's f and f'. gelu_tanh in its equal form z sigmoid(2 v), v = c (z + k z^3): unlike
+// 1 + tanh(v) it does not cancel for z < 0, so the error stays a few roundings of the result (the
+// MLP's own epilogues keep the tanh form: their results do not change).
+__device__ __forceinline__ float gelu_gate(float z) {
+  return sigmoidf_(2.0f * kGeluC * (z + kGeluK * (z * z) * z));
+}
+template <int N>
+__device__ __forceinline__ void linear_fn(int fn, const float (&z)[N], float (&f)[N]) {
+  if (fn == FN_GELU_TANH) {
+#pragma unroll
+    for (int r = 0; r < N; ++r) f[r] = z[r] * gelu_gate(z[r]);
+  } else {
+    act_fn<N>(fn, z, f);
+  }
+}
+template <int N>
+__device__ __forceinline__ void linear_fn_grad(int fn, const float (&z)[N], float (&f)[N], float (&df)[N]) {
+  if (fn == FN_GELU_TANH) {
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+      const float s = gelu_gate(z[r]);
+      f[r] = z[r] * s;
+      df[r] = s * (1.0f + z[r] * (1.0f - s) * (2.0f * kGeluC * (1.0f + 3.0f * kGeluK * (z[r] * z[r]))));
+    }
+  } else {
+    act_fn_grad<N>(fn, z, f, df);
+  }
+}
+
+// y of the linear epilogues: f(z), gated f(z) u, and z itself for FN_NONE.
+template <int N, bool GATED>
+__device__ __forceinline__ void linear_act(int fn, const float (&z)[N], const float (&u)[N], float (&y)[N]) {
+  if constexpr (GATED) {
+    linear_fn<N>(fn, z, y);
+#pragma unroll
+    for (int r = 0; r < N; ++r) y[r] *= u[r];
+  } else if (fn == FN_NONE) {
+#pragma unroll
+    for (int r = 0; r < N; ++r) y[r] = z[r];
+  } else {
+    linear_fn<N>(fn, z, y);
+  }
+}
+
 // ---- LDS tile geometry -------------------------------------------------------------------
 // Every operand tile in LDS is [rows][128 bytes]: the K extent of one pipeline stage is
 // 128 bytes of the element type (64 bf16, 32 fp32, 128 e4m3), split in 8 chunks of 16 bytes.

@@ -60,6 +60,8 @@ __device__ __forceinline__ void epi_prefetch(const GemmArgs& p, int m, int n, Au
       x.a = reinterpret_cast<const u32x4*>(q)[0];
       x.c = reinterpret_cast<const u32x4*>(q)[1];
     }
+  } else if constexpr (epi_linear(EPI)) {
+    if (p.res) x.a = *reinterpret_cast<const u32x4*>(elem_ptr<IoT>(p.res, m, p.ld_res, n));
   }
 }
 
@@ -134,6 +136,21 @@ __device__ __forceinline__ void epi_row8(const GemmArgs& p, int m, int n, int sp
     for (int r = 0; r < 8; ++r) dpre[r] *= v[r];
     Vec8<IoT>::store(elem_ptr<IoT>(p.C0, m, p.ldc0, n), dpre);
     if (p.flags & 2) Vec8<IoT>::store(elem_ptr<IoT>(p.C1, m, p.ldc1, n), post);
+  } else if constexpr (epi_linear(EPI)) {   // the bias is in v and u
+    constexpr bool GATED = epi_gated(EPI);
+    if (p.flags & 1) {
+      Vec8<IoT>::store(elem_ptr<IoT>(p.aux, m, p.ld_aux, n), v);
+      if constexpr (GATED) Vec8<IoT>::store(elem_ptr<IoT>(p.aux, m, p.ld_aux, p.half + n), u);
+    }
+    float y[8];
+    linear_act<8, GATED>(p.act, v, u, y);
+    if (p.res) {
+      float o[8];
+      unpack16x8<IoT>(x.a, o);
+#pragma unroll
+      for (int r = 0; r < 8; ++r) y[r] += o[r];
+    }
+    Vec8<IoT>::store(elem_ptr<IoT>(p.C0, m, p.ldc0, n), y);
   }
 }
 
@@ -217,7 +234,7 @@ constexpr int epilogue_lds_bytes() { return WAVES * epilogue_rows_per_round<WAVE
 template <int EPI, typename IoT, int BM, int BN, int MI, int NI, int WAVES, typename AccV>
 __device__ __forceinline__ void epilogue_rows(const GemmArgs& p, AccV (&acc)[MI][NI], int m0, int n0,
                                               int split, int wm, int wn, int lane, int wave, char* lds) {
-  constexpr bool GATED = EPI == EPI_GATED;
+  constexpr bool GATED = epi_gated(EPI);
   // 32x32 blocks (16 values per lane: rows l%32, columns 8g + 4(l/32) + r) or 16x16 blocks
   // (4 values per lane: row l%16, columns 4(l/16) + r)
   constexpr bool B16 = sizeof(AccV) == 4 * sizeof(float);
@@ -243,6 +260,14 @@ __device__ __forceinline__ void epilogue_rows(const GemmArgs& p, AccV (&acc)[MI]
 
   const int nbase = GATED ? n0 + wn * (WN / 2) : n0 + wn * WN;
   const int rl = lane / LPR, cl = (lane % LPR) * PW;      // this lane's row-in-pass / column
+  // the linear epilogues' bias: a lane has the same columns in every pass
+  float bias0[epi_linear(EPI) ? 8 : 1] = {}, bias1[EPI == EPI_LIN_GATED ? 8 : 1] = {};
+  if constexpr (epi_linear(EPI)) {
+    if (p.bias0 && nbase + cl < p.N) Vec8<IoT>::load(elem_ptr<IoT>(p.bias0, 0, 0, nbase + cl), bias0);
+    if constexpr (GATED) {
+      if (p.bias1 && nbase + cl < p.N) Vec8<IoT>::load(elem_ptr<IoT>(p.bias1, 0, 0, nbase + cl), bias1);
+    }
+  }
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
 #pragma unroll
@@ -331,6 +356,13 @@ __device__ __forceinline__ void epilogue_rows(const GemmArgs& p, AccV (&acc)[MI]
             a1 = su[1];
 #pragma unroll
             for (int q = 0; q < 4; ++q) { u[q] = a0[q]; u[4 + q] = a1[q]; }
+          }
+          if constexpr (epi_linear(EPI)) {
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+              v[q] += bias0[q];
+              if constexpr (GATED) u[q] += bias1[q];
+            }
           }
           if (m < p.M && n < p.N) epi_row8<EPI, IoT>(p, m, n, split, v, u, x[pass], local_amax);
         }

@@ -1,0 +1,10 @@
+// bf16 products of the experts, backward (gemm_experts.hpp).
+#include "gemm_experts.hpp"
+
+namespace gmlp {
+
+hipError_t run_expert_bwd_bf16(TileShape tile, const ExpertBwd& a, hipStream_t s) {
+  return expert_bwd16<bf16>(tile, a, s);
+}
+
+}  // namespace gmlp

@@ -8,7 +8,8 @@ namespace gmlp {
 // The activation functions of the fused epilogues (GemmArgs::act): the gate function f of a
 // gated activation a = f(g) * u (SwiGLU: silu, GeGLU: gelu_tanh, ReGLU: relu, GLU: sigmoid), or
 // the f of a non-gated post = f(pre) (relu^2, relu, gelu_tanh).
-enum ActFn : int { FN_SILU = 0, FN_GELU_TANH = 1, FN_RELU = 2, FN_SIGMOID = 3, FN_RELU_SQ = 4 };
+// FN_NONE: the linear epilogues only.
+enum ActFn : int { FN_SILU = 0, FN_GELU_TANH = 1, FN_RELU = 2, FN_SIGMOID = 3, FN_RELU_SQ = 4, FN_NONE = 5 };
 
 enum Epi : int {
   EPI_STORE = 0,    // C = alpha * acc (OutT); accumulate: C(f32) += alpha * acc; rows >= c_split go to C1
@@ -24,7 +25,14 @@ enum Epi : int {
   EPI_F8DACT = 7,   // dpre = alpha * acc * 2 max(pre, 0), pre <- aux (bf16 or fp32);
                     // C0 = e5m2(dpre / *s_post) (s_post holds the dpre scale here);
                     // *amax = max(*amax, max |dpre|); C1 set: C1 = e4m3(relu(pre)^2 / *s_c1)
+  EPI_LIN = 8,      // z = acc + bias0[n] -> aux (flag 1); C0 = res + f(z) (bias0, res may be NULL)
+  EPI_LIN_GATED = 9 // g, u = acc pair + bias0[n], bias1[n] -> aux[m][n], aux[m][half+n] (flag 1);
+                    // C0 = res + f(g) u
 };
+
+// Epilogues whose tile holds gate rows and the up rows of the same units.
+constexpr bool epi_gated(int epi) { return epi == EPI_GATED || epi == EPI_LIN_GATED; }
+constexpr bool epi_linear(int epi) { return epi == EPI_LIN || epi == EPI_LIN_GATED; }
 
 struct GemmArgs {
   int M, N, K;
@@ -43,7 +51,23 @@ struct GemmArgs {
   int k_per_split; float* partial;
   int tiles_m, tiles_n, group_m;
   const float* s_c1;   // F8DACT: scale of the e4m3 relu(pre)^2 codes written to C1
+  const void* bias0; const void* bias1; const void* res; int64_t ld_res;   // LIN, LIN_GATED
 };
+
+// One product an expert, rows grouped by expert: expert e has rows offsets[e] .. offsets[e+1]-1 of
+// the row-indexed operands (offsets NULL: one expert with all rows) and weight matrices, biases and
+// weight gradients w_stride, bias_stride and w_stride elements apart. The members' pointers are those
+// of expert 0 and row 0; M (products over rows) or K (weight gradients) is set per expert on the
+// device. tiles_m of a product over rows is unused.
+struct ExpertGemm {
+  GemmArgs g;
+  const int* offsets;
+  int experts, rows;
+  int64_t w_stride, bias_stride;
+  int grid;   // workgroups: an upper bound of the tiles for a product over rows
+};
+// The backward's two products, in one launch: workgroups [0, dx.grid) and the dw.grid after them.
+struct ExpertBwd { ExpertGemm dx, dw; };
 
 // Up to kGroupMax independent GEMMs run by one launch (gemm_dma_group_kernel): member j covers
 // workgroups [begin[j], begin[j+1]) (multiples of 8 apart), has items[j] tiles (one per

@@ -38,6 +38,28 @@ hipError_t dispatch16(DType io, int epi, const GemmArgs& a, int grid, hipStream_
   return hipErrorInvalidValue;
 }
 
+// The linear layer's product with its epilogue; the shapes plan_gemm chooses from for 16-bit types.
+template <typename T>
+hipError_t run_linear16(int epi, TileShape tile, const GemmArgs& a, int grid, hipStream_t s) {
+  auto shape = [&](auto bm, auto bn, auto waves) {
+    constexpr int BM = decltype(bm)::value, BN = decltype(bn)::value, W = decltype(waves)::value;
+    if (epi == EPI_LIN_GATED) return launch_gemm_dma<T, T, BM, BN, true, true, EPI_LIN_GATED, W>(a, grid, s);
+    if (epi == EPI_LIN) return launch_gemm_dma<T, T, BM, BN, true, true, EPI_LIN, W>(a, grid, s);
+    return hipErrorInvalidValue;
+  };
+  using std::integral_constant;
+  constexpr integral_constant<int, 256> k256{};
+  constexpr integral_constant<int, 128> k128{};
+  constexpr integral_constant<int, 8> w8{};
+  constexpr integral_constant<int, 4> w4{};
+  switch (tile) {
+    case TILE_256x256_W8: return shape(k256, k256, w8);
+    case TILE_256x128_W8: return shape(k256, k128, w8);
+    case TILE_128x128: return shape(k128, k128, w4);
+    default: return hipErrorInvalidValue;
+  }
+}
+
 template <typename T, int LAYOUT>
 hipError_t run_gemm16(DType io, int epi, TileShape tile, const GemmArgs& a, int grid, hipStream_t s) {
   switch (tile) {

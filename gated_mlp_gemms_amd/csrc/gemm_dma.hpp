@@ -467,7 +467,9 @@ constexpr int dma_ring_bytes() {
 // WAVES = 4: 2 x 2 waves, one per SIMD (wave tile up to 128 x 128, 256 accumulator registers).
 // WAVES = 8: 4 x 2 waves, two per SIMD, so one wave's MFMAs fill the other's stalls (wave tile
 // 64 x 128, 128 accumulator registers, half the register file each).
-template <typename T, typename IoT, int BM, int BN, bool A_KMAJ, bool B_KMAJ, int EPI, int WAVES>
+// SKIP: a wave whose rows all lie past the matrix takes part in the K-steps' DMAs and barriers only,
+// so a tile of few rows costs its SIMDs the MFMAs of the waves that have rows.
+template <typename T, typename IoT, int BM, int BN, bool A_KMAJ, bool B_KMAJ, int EPI, int WAVES, bool SKIP = false>
 __device__ __forceinline__ void gemm_dma_tile(const GemmArgs p, int item, char* smem) {
   static_assert(BM % 64 == 0 && BN % 64 == 0, "tile must split into 2x2 waves of 32x32 blocks");
   static_assert((A_KMAJ && B_KMAJ) || ElemTraits<T>::bytes == 2 || (WAVES == 4 && !A_KMAJ && !B_KMAJ),
@@ -486,7 +488,7 @@ __device__ __forceinline__ void gemm_dma_tile(const GemmArgs p, int item, char* 
   constexpr int A_BYTES = BM * ROWB, STAGE = (BM + BN) * ROWB;
   constexpr int NS = ring_stages(STAGE, BM * BN);
   static_assert(NS >= 2, "the ring needs two stages");
-  constexpr bool GATED = EPI == EPI_GATED;
+  constexpr bool GATED = epi_gated(EPI);
   constexpr int KMMA = M16 ? 32 : (ES == 1 ? 64 : 16);
   constexpr int NSUB = BK / KMMA;
   constexpr int KC = Mma<T>::kChunks;
@@ -756,6 +758,27 @@ __device__ __forceinline__ void gemm_dma_tile(const GemmArgs p, int item, char* 
     }
     wait_lgkmcnt0();
     __builtin_amdgcn_s_barrier();
+    if constexpr (SKIP) {
+      if (m0 + wm * WM >= p.M) {   // the K-steps' barriers, and this wave's share of their DMAs
+        int st = 0, st_a = 0;
+        for (int kt = 0; kt < nk; ++kt) {
+          wait_vmcnt<(NS - 2) * N_DMA + XA * KIA>();
+          __builtin_amdgcn_s_barrier();
+          if constexpr (XA) {
+            issue_b(kt + NS, st);
+            issue_a(kt + NSA, st_a);
+          } else {
+            issue(kt + NS, st);
+          }
+          st = st + 1 == NS ? 0 : st + 1;
+          st_a = XA ? (st_a + 1 == NSA ? 0 : st_a + 1) : st;
+        }
+        if constexpr (DW < WAVES) __builtin_amdgcn_s_setprio(0);
+        wait_vmcnt<0>();
+        __builtin_amdgcn_s_barrier();
+        return;   // the epilogue has no barrier
+      }
+    }
     read_frags(0, 0, 0, 0);
     // drained here so that the loop header's LDS waits are counted from the loop body alone:
     // the prologue issues these reads in another order, and a wait merged over both paths

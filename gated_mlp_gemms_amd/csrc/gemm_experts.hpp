@@ -1,0 +1,205 @@
+// One product an expert in one launch (ExpertGemm): the tile bodies of gemm_dma.hpp (16-bit) and
+// gemm_kernel.hpp (fp32) with the operands moved to an expert's rows and weights. How many rows an
+// expert has is known on the device only, so a launch over rows has as many workgroups as the rows
+// could need at most (every expert may end in a partial tile); each workgroup counts the experts'
+// tiles from the offsets (a wave scan, no memory but the offsets) and takes one or none.
+#pragma once
+
+#include "gemm_dma.hpp"
+#include "launch.hpp"
+
+namespace gmlp {
+
+// A piece of at most `step` rows of one expert.
+struct RowPiece {
+  int e;        // expert; the number of experts: rows behind the last offset
+  int row0;     // the expert's first row
+  int rows;     // the expert's rows
+  int index;    // the piece within the expert
+  int first;    // pieces of the experts before
+};
+
+// Rows of expert e (e = experts: what lies behind the last offset). Offsets are held inside [0, rows],
+// so whatever they contain, no row outside the operands is named.
+__device__ __forceinline__ void expert_rows(const int* offsets, int experts, int rows, int e, int& row0, int& n) {
+  if (offsets == nullptr) {   // one expert with every row
+    row0 = e == 0 ? 0 : rows;
+    n = e == 0 ? rows : 0;
+    return;
+  }
+  row0 = min(max(offsets[min(e, experts)], 0), rows);
+  const int end = e < experts ? min(max(offsets[e + 1], row0), rows) : rows;
+  n = e <= experts ? end - row0 : 0;
+}
+
+// Pieces of every expert (the rows behind the last offset included) are numbered in expert order.
+// count(total) -> the number of the piece wanted, or -1. Called by whole waves; every wave of a
+// workgroup gets the same answer, in scalar registers.
+template <typename Want>
+__device__ __forceinline__ bool find_row_piece(const int* offsets, int experts, int rows, int step, Want want,
+                                               RowPiece& out) {
+  const int lane = threadIdx.x & 63;
+  int row0, n, pieces, incl;
+  auto scan = [&](int base) {   // inclusive scan of the pieces of experts base .. base + 63
+    expert_rows(offsets, experts, rows, base + lane, row0, n);
+    pieces = (n + step - 1) / step;
+    incl = pieces;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(incl, o);
+      if (lane >= o) incl += v;
+    }
+  };
+  int total = 0;
+  for (int base = 0; base <= experts; base += 64) {
+    scan(base);
+    total += __builtin_amdgcn_readlane(incl, 63);
+  }
+  const int at = want(total);
+  if (at < 0) return false;
+  int before = 0;
+  for (int base = 0; base <= experts; base += 64) {
+    if (experts >= 64) scan(base);   // else the one scan above is this one
+    const uint64_t hit = __ballot(before + incl > at);
+    if (hit != 0) {
+      const int l = __builtin_ctzll(hit);
+      out.e = base + l;
+      out.row0 = __builtin_amdgcn_readlane(row0, l);
+      out.rows = __builtin_amdgcn_readlane(n, l);
+      out.first = before + __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(pieces, l);
+      out.index = at - out.first;
+      return true;
+    }
+    before += __builtin_amdgcn_readlane(incl, 63);
+  }
+  return false;
+}
+
+template <typename T> __device__ __forceinline__ const void* shift(const void* p, int64_t elems) {
+  return p ? reinterpret_cast<const char*>(p) + elems * ElemTraits<T>::bytes : nullptr;
+}
+template <typename T> __device__ __forceinline__ void* shift(void* p, int64_t elems) {
+  return p ? reinterpret_cast<char*>(p) + elems * ElemTraits<T>::bytes : nullptr;
+}
+
+template <typename T, int BM, int BN>
+constexpr int expert_lds_bytes() {
+  if constexpr (sizeof(T) == 4) return 2 * (BM + BN) * 128;
+  else return dma_ring_bytes<T, BM, BN>();
+}
+
+template <typename T, typename IoT, int BM, int BN, bool AK, bool BK, int EPI, int WAVES>
+__device__ __forceinline__ void expert_tile(const GemmArgs& p, int item, char* smem) {
+  if constexpr (sizeof(T) == 4) gemm_tile<T, IoT, BM, BN, AK, BK, EPI>(p, item, smem);
+  else gemm_dma_tile<T, IoT, BM, BN, AK, BK, EPI, WAVES, true>(p, item, smem);
+}
+
+// Tile b of a product over rows: y = x W_e^T with a linear epilogue, or dx = dz W_e.
+template <typename T, int BM, int BN, bool BK, int EPI, int WAVES>
+__device__ __forceinline__ void expert_rows_tile(const ExpertGemm& a, int b, char* smem) {
+  constexpr int BNC = epi_gated(EPI) ? BN / 2 : BN;   // output columns of a tile
+  const int tiles_n = a.g.tiles_n;
+  int tile = 0;
+  RowPiece t;
+  // XCD-contiguous over the tiles there are, not over the launch's upper bound
+  const bool found = find_row_piece(a.offsets, a.experts, a.rows, BM, [&](int total) {
+    const int tiles = (int)min((int64_t)total * tiles_n, (int64_t)a.grid);
+    if (b >= tiles) return -1;
+    tile = xcd_remap(b, tiles);
+    return tile / tiles_n;
+  }, t);
+  if (!found) return;
+  GemmArgs p = a.g;
+  if (t.e == a.experts) {   // rows of no expert: zeros (plus the residual)
+    const int m0 = t.row0 + t.index * BM, m1 = min(m0 + BM, a.rows);
+    const int n0 = (tile % tiles_n) * BNC, n1 = min(n0 + BNC, p.N);
+    constexpr int V = 16 / ElemTraits<T>::bytes, W = BNC / V;
+    for (int i = threadIdx.x; i < BM * W; i += 64 * WAVES) {
+      const int m = m0 + i / W, n = n0 + i % W * V;
+      if (m >= m1 || n >= n1) continue;
+      const u32x4 zero = {0u, 0u, 0u, 0u};
+      if (epi_linear(EPI) && (p.flags & 1)) {
+        *reinterpret_cast<u32x4*>(elem_ptr<T>(p.aux, m, p.ld_aux, n)) = zero;
+        if (epi_gated(EPI)) *reinterpret_cast<u32x4*>(elem_ptr<T>(p.aux, m, p.ld_aux, p.half + n)) = zero;
+      }
+      *reinterpret_cast<u32x4*>(elem_ptr<T>(p.C0, m, p.ldc0, n)) =
+          epi_linear(EPI) && p.res ? *reinterpret_cast<const u32x4*>(elem_ptr<T>(p.res, m, p.ld_res, n)) : zero;
+    }
+    return;
+  }
+  p.M = t.rows;
+  p.tiles_m = (t.rows + BM - 1) / BM;
+  p.A = shift<T>(p.A, t.row0 * p.lda);
+  p.C0 = shift<T>(p.C0, t.row0 * p.ldc0);
+  p.aux = shift<T>(p.aux, t.row0 * p.ld_aux);
+  p.res = shift<T>(p.res, t.row0 * p.ld_res);
+  p.B0 = shift<T>(p.B0, t.e * a.w_stride);
+  p.B1 = shift<T>(p.B1, t.e * a.w_stride);
+  p.bias0 = shift<T>(p.bias0, t.e * a.bias_stride);
+  p.bias1 = shift<T>(p.bias1, t.e * a.bias_stride);
+  expert_tile<T, T, BM, BN, true, BK, EPI, WAVES>(p, tile - t.first * tiles_n, smem);
+}
+
+// Tile `item` of the weight gradients dW_e = dz^T x over expert e's rows.
+template <typename T, typename GT, int BM, int BN, int WAVES>
+__device__ __forceinline__ void expert_grad_tile(const ExpertGemm& a, int item, char* smem) {
+  GemmArgs p = a.g;
+  const int tiles = p.tiles_m * p.tiles_n;
+  const int e = item / tiles;
+  int row0, n;
+  expert_rows(a.offsets, a.experts, a.rows, e, row0, n);
+  row0 = __builtin_amdgcn_readfirstlane(row0);
+  n = __builtin_amdgcn_readfirstlane(n);
+  if (n == 0 && p.accumulate) return;
+  p.K = p.k_per_split = n;
+  p.A = shift<T>(p.A, row0 * p.lda);
+  p.B0 = shift<T>(p.B0, row0 * p.ldb);
+  p.C0 = shift<GT>(p.C0, e * a.w_stride);
+  p.C1 = shift<GT>(p.C1, e * a.w_stride);
+  expert_tile<T, GT, BM, BN, false, false, EPI_STORE, WAVES>(p, item - e * tiles, smem);
+}
+
+template <typename T, int BM, int BN, int EPI, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 1) void expert_fwd_kernel(const ExpertGemm a) {
+  __shared__ __attribute__((aligned(1024))) char smem[expert_lds_bytes<T, BM, BN>()];
+  expert_rows_tile<T, BM, BN, true, EPI, WAVES>(a, blockIdx.x, smem);
+}
+
+template <typename T, typename GT, int BM, int BN, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 1) void expert_bwd_kernel(const ExpertBwd a) {
+  __shared__ __attribute__((aligned(1024))) char smem[expert_lds_bytes<T, BM, BN>()];
+  const int b = blockIdx.x;
+  if (b < a.dx.grid) expert_rows_tile<T, BM, BN, false, EPI_STORE, WAVES>(a.dx, b, smem);
+  else expert_grad_tile<T, GT, BM, BN, WAVES>(a.dw, xcd_remap(b - a.dx.grid, a.dw.grid), smem);
+}
+
+template <typename T, int BM, int BN, int WAVES>
+hipError_t launch_expert_fwd(int epi, const ExpertGemm& a, hipStream_t s) {
+  if (epi == EPI_LIN_GATED)
+    hipLaunchKernelGGL((expert_fwd_kernel<T, BM, BN, EPI_LIN_GATED, WAVES>), dim3(a.grid), dim3(64 * WAVES), 0, s, a);
+  else
+    hipLaunchKernelGGL((expert_fwd_kernel<T, BM, BN, EPI_LIN, WAVES>), dim3(a.grid), dim3(64 * WAVES), 0, s, a);
+  return hipGetLastError();
+}
+
+template <typename T, int BM, int BN, int WAVES>
+hipError_t launch_expert_bwd(const ExpertBwd& a, hipStream_t s) {
+  const dim3 grid(a.dx.grid + a.dw.grid), block(64 * WAVES);
+  if (a.dw.g.accumulate) hipLaunchKernelGGL((expert_bwd_kernel<T, float, BM, BN, WAVES>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((expert_bwd_kernel<T, T, BM, BN, WAVES>), grid, block, 0, s, a);
+  return hipGetLastError();
+}
+
+// The 16-bit experts' products of one type: 8-wave 256 x 256 tiles or 4-wave 128 x 128 ones.
+template <typename T> hipError_t expert_fwd16(int epi, TileShape tile, const ExpertGemm& a, hipStream_t s) {
+  if (tile == TILE_256x256_W8) return launch_expert_fwd<T, 256, 256, 8>(epi, a, s);
+  if (tile == TILE_128x128) return launch_expert_fwd<T, 128, 128, 4>(epi, a, s);
+  return hipErrorInvalidValue;
+}
+template <typename T> hipError_t expert_bwd16(TileShape tile, const ExpertBwd& a, hipStream_t s) {
+  if (tile == TILE_256x256_W8) return launch_expert_bwd<T, 256, 256, 8>(a, s);
+  if (tile == TILE_128x128) return launch_expert_bwd<T, 128, 128, 4>(a, s);
+  return hipErrorInvalidValue;
+}
+
+}  // namespace gmlp

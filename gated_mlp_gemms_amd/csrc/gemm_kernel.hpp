@@ -258,7 +258,7 @@ template <typename T, int ROWS> struct TileSel<false, T, ROWS> { using type = MN
 template <int EPI, typename IoT, int BM, int BN, int MI, int NI>
 __device__ __forceinline__ void epilogue(const GemmArgs& p, f32x16 (&acc)[MI][NI], int m0, int n0,
                                          int split, int wm, int wn, int lane) {
-  constexpr bool GATED = EPI == EPI_GATED;
+  constexpr bool GATED = epi_gated(EPI);
   constexpr int WM = BM / 2, WN = BN / 2;
   const int frow = lane & 31, fhalf = lane >> 5;
   float alpha = p.alpha;
@@ -350,6 +350,36 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, f32x16 (&acc)[MI][NI
             packed |= f32_to_e4m3(__fdiv_rn(post, sp)) << (8 * r);
           }
           *reinterpret_cast<uint32_t*>(elem_ptr<e4m3>(p.C0, m, p.ldc0, n)) = packed;
+        } else if constexpr (epi_linear(EPI)) {
+          float u[4], y[4];
+          if (p.bias0) {
+            float b[4];
+            Vec4<IoT>::load(elem_ptr<IoT>(p.bias0, 0, 0, n), b);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[r] += b[r];
+          }
+          if constexpr (GATED) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) u[r] = alpha * acc[i][j + NJ][4 * g + r];
+            if (p.bias1) {
+              float b[4];
+              Vec4<IoT>::load(elem_ptr<IoT>(p.bias1, 0, 0, n), b);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) u[r] += b[r];
+            }
+          }
+          if (p.flags & 1) {
+            Vec4<IoT>::store(elem_ptr<IoT>(p.aux, m, p.ld_aux, n), v);
+            if constexpr (GATED) Vec4<IoT>::store(elem_ptr<IoT>(p.aux, m, p.ld_aux, p.half + n), u);
+          }
+          linear_act<4, GATED>(p.act, v, u, y);
+          if (p.res) {
+            float o[4];
+            Vec4<IoT>::load(elem_ptr<IoT>(p.res, m, p.ld_res, n), o);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) y[r] += o[r];
+          }
+          Vec4<IoT>::store(elem_ptr<IoT>(p.C0, m, p.ldc0, n), y);
         }
       }
     }
@@ -363,25 +393,25 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, f32x16 (&acc)[MI][NI
 
 // ---- the kernel --------------------------------------------------------------------------------
 
+// One output tile: tile `item` of p's grid (tiles_m x tiles_n x splits), with `smem` the
+// workgroup's 2 * (BM + BN) * 128 bytes of LDS.
 template <typename T, typename IoT, int BM, int BN, bool A_KMAJ, bool B_KMAJ, int EPI>
-__global__ __launch_bounds__(kThreads, 1) void gemm_kernel(const GemmArgs p) {
+__device__ __forceinline__ void gemm_tile(const GemmArgs p, int item, char* smem) {
   static_assert(BM % 64 == 0 && BN % 64 == 0, "tile must split into 2x2 waves of 32x32 blocks");
-  static_assert(EPI != EPI_GATED || B_KMAJ, "gated epilogue reads K-major weights");
+  static_assert(!epi_gated(EPI) || B_KMAJ, "gated epilogue reads K-major weights");
   constexpr int ES = ElemTraits<T>::bytes;
   constexpr int E = 16 / ES;
   constexpr int BK = 8 * E;
   constexpr int WM = BM / 2, WN = BN / 2;
   constexpr int MI = WM / 32, NI = WN / 32;
   constexpr int A_BYTES = BM * 128, STAGE = (BM + BN) * 128;
-  constexpr bool GATED = EPI == EPI_GATED;
+  constexpr bool GATED = epi_gated(EPI);
   static_assert(!GATED || NI % 2 == 0, "gated tile needs gate and up blocks per wave");
-
-  __shared__ __attribute__((aligned(16))) char smem[2 * STAGE];
 
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave >> 1, wn = wave & 1;
 
-  int lid = xcd_remap(blockIdx.x, gridDim.x);
+  int lid = item;
   const int tiles = p.tiles_m * p.tiles_n;
   const int split = lid / tiles;
   lid -= split * tiles;
@@ -412,7 +442,8 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_kernel(const GemmArgs p) {
         return elem_ptr<T>(r < half ? p.B0 : p.B1, n, p.ldb, 0);
       } else {
         const int n = n0 + r;
-        return n < p.N ? elem_ptr<T>(p.B0, n, p.ldb, 0) : nullptr;
+        if (n >= p.N) return nullptr;   // rows n >= b_split from B1 (stacked [W_gate; W_up])
+        return n < p.b_split ? elem_ptr<T>(p.B0, n, p.ldb, 0) : elem_ptr<T>(p.B1, n - p.b_split, p.ldb, 0);
       }
     });
   }
@@ -499,6 +530,12 @@ __global__ __launch_bounds__(kThreads, 1) void gemm_kernel(const GemmArgs p) {
   }
 
   epilogue<EPI, IoT, BM, BN, MI, NI>(p, acc, m0, n0, split, wm, wn, lane);
+}
+
+template <typename T, typename IoT, int BM, int BN, bool A_KMAJ, bool B_KMAJ, int EPI>
+__global__ __launch_bounds__(kThreads, 1) void gemm_kernel(const GemmArgs p) {
+  __shared__ __attribute__((aligned(16))) char smem[2 * (BM + BN) * 128];
+  gemm_tile<T, IoT, BM, BN, A_KMAJ, B_KMAJ, EPI>(p, xcd_remap(blockIdx.x, gridDim.x), smem);
 }
 
 template <typename T, typename IoT, int BM, int BN, bool A_KMAJ, bool B_KMAJ, int EPI>

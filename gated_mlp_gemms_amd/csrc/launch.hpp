@@ -55,6 +55,58 @@ hipError_t run_skinny(DType in, int epi, const GemmArgs& a, hipStream_t s);
 constexpr int kSkinnyParts = 4;
 inline bool skinny_parts_for(int64_t M, int64_t N, int64_t K) { return M > 8 && N <= 8192 && K >= 2048; }
 
+// ---- linear layer and the experts' products ----------------------------------------------------
+
+// y = res + act(x W^T + b): EPI_LIN or EPI_LIN_GATED, K-major operands in `in`, unsplit.
+hipError_t run_gemm_linear(DType in, int epi, TileShape tile, const GemmArgs& a, int grid, hipStream_t s);
+hipError_t run_gemm_bf16_linear(int epi, TileShape tile, const GemmArgs& a, int grid, hipStream_t s);
+hipError_t run_gemm_f16_linear(int epi, TileShape tile, const GemmArgs& a, int grid, hipStream_t s);
+hipError_t run_gemm_f32_linear(int epi, const GemmArgs& a, int grid, hipStream_t s);
+// The same from fp32 partials [splits][M][N] (gated: [splits][M][2N], g then u), summed in order.
+hipError_t run_linear_reduce(DType io, int gated, const float* partial, int splits, const GemmArgs& a, hipStream_t s);
+
+// One product an expert (ExpertGemm). Tiles: TILE_256x256_W8 and TILE_128x128 (f32: the latter).
+hipError_t run_expert_fwd(DType in, int epi, TileShape tile, const ExpertGemm& a, hipStream_t s);
+hipError_t run_expert_bwd(DType in, TileShape tile, const ExpertBwd& a, hipStream_t s);
+hipError_t run_expert_fwd_bf16(int epi, TileShape tile, const ExpertGemm& a, hipStream_t s);
+hipError_t run_expert_fwd_f16(int epi, TileShape tile, const ExpertGemm& a, hipStream_t s);
+hipError_t run_expert_fwd_f32(int epi, const ExpertGemm& a, hipStream_t s);
+hipError_t run_expert_bwd_bf16(TileShape tile, const ExpertBwd& a, hipStream_t s);
+hipError_t run_expert_bwd_f16(TileShape tile, const ExpertBwd& a, hipStream_t s);
+hipError_t run_expert_bwd_f32(const ExpertBwd& a, hipStream_t s);
+// The forward with a few rows an expert, 16-bit (g.N output columns, any rows; grid is unused).
+hipError_t run_skinny_experts(DType in, int epi, const ExpertGemm& a, hipStream_t s);
+
+// dz = dy f'(z) (gated: [dy u f'(g) | dy f(g)]) into dz [rows, P] (NULL: not stored; fn FN_NONE: dz is
+// dy), and its column sums over pieces of at most kDactRows rows of one expert, fp32, into
+// sums [pieces][P] (NULL: not formed); P = 2N gated, else N.
+constexpr int kDactRows = 64;
+inline int64_t dact_pieces(int64_t rows, int64_t experts) { return rows / kDactRows + (rows < experts ? rows : experts) + 1; }
+hipError_t run_linear_dact(DType io, int gated, int fn, const void* dy, const void* preact, const int* offsets,
+                           int experts, int64_t rows, int64_t N, void* dz, float* sums, hipStream_t s);
+// The pieces' sums joined in order: db0 (gated: the first N columns; db1 the others) [experts, N], in
+// `io` or added into fp32 (accumulate).
+hipError_t run_linear_dbias(DType io, int gated, const float* sums, const int* offsets, int experts, int64_t rows,
+                            int64_t N, void* db0, void* db1, int accumulate, hipStream_t s);
+
+// ---- router, sort, rows ---------------------------------------------------------------------------
+
+hipError_t run_moe_route(DType dt, const void* logits, int64_t T, int E, int k, int sigmoid, int renorm, int* ids,
+                         float* weights, hipStream_t s);
+hipError_t run_moe_route_bwd(DType dt, const void* logits, const int* ids, const float* dweights, int64_t T, int E,
+                             int k, int sigmoid, int renorm, void* dlogits, hipStream_t s);
+size_t moe_sort_counts_bytes(int64_t n, int E);   // 0: one workgroup sorts them
+hipError_t run_moe_sort(const int* ids, int64_t n, int E, int* offsets, int* row_of, int* slot_of, int* counts,
+                        hipStream_t s);
+// rows of `pieces` 16-byte pieces
+hipError_t run_moe_gather(const void* x, const int* slot_of, const int* offsets, int n, int E, int k, int pieces,
+                          void* xs, hipStream_t s);
+hipError_t run_moe_combine(DType dt, const void* ys, const float* weights, const int* row_of, const int* offsets,
+                           const void* residual, int T, int E, int k, int pieces, void* out, hipStream_t s);
+hipError_t run_moe_combine_bwd(DType dt, const void* dout, const void* ys, const float* weights, const int* row_of,
+                               const int* slot_of, const int* offsets, int n, int E, int k, int pieces, void* dys,
+                               float* dweights, hipStream_t s);
+
 // out = alpha * sum_s partial[s] (fixed order), stored as `io` or added into fp32 (accumulate).
 // Rows >= c_split go to C1 (row - c_split).
 hipError_t run_splitk_reduce(DType io, const float* partial, int splits, int M, int N, void* C0,

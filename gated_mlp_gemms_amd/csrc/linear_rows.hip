@@ -1,0 +1,224 @@
+// The linear layer's row passes: the split-K finish with its epilogue, and the backward's
+// activation gradient with the bias gradient's column sums.
+#include "gemm_experts.hpp"
+#include "launch.hpp"
+
+#include <algorithm>
+
+namespace gmlp {
+
+namespace {
+
+constexpr int kThr = 256;
+
+// y = res + act(sum_s partial[s] + bias), 4 columns a thread.
+template <typename T, bool GATED>
+__global__ __launch_bounds__(kThr) void linear_reduce_kernel(const float* __restrict__ partial, int splits,
+                                                             const GemmArgs p) {
+  const int n4 = p.N / 4, width = GATED ? 2 * p.N : p.N;
+  const int64_t total = (int64_t)p.M * n4, slice = (int64_t)p.M * width;
+  for (int64_t i = blockIdx.x * (int64_t)kThr + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThr) {
+    const int m = (int)(i / n4), n = (int)(i % n4) * 4;
+    const float* row = partial + (int64_t)m * width + n;
+    f32x4 g = *reinterpret_cast<const f32x4*>(row), u = {};
+    if constexpr (GATED) u = *reinterpret_cast<const f32x4*>(row + p.N);
+#pragma unroll 4
+    for (int sp = 1; sp < splits; ++sp) {
+      g += *reinterpret_cast<const f32x4*>(row + sp * slice);
+      if constexpr (GATED) u += *reinterpret_cast<const f32x4*>(row + sp * slice + p.N);
+    }
+    float z[4] = {g[0], g[1], g[2], g[3]}, v[4] = {u[0], u[1], u[2], u[3]}, b[4], y[4];
+    if (p.bias0) {
+      Vec4<T>::load(elem_ptr<T>(p.bias0, 0, 0, n), b);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) z[r] += b[r];
+    }
+    if (GATED && p.bias1) {
+      Vec4<T>::load(elem_ptr<T>(p.bias1, 0, 0, n), b);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) v[r] += b[r];
+    }
+    if (p.flags & 1) {
+      Vec4<T>::store(elem_ptr<T>(p.aux, m, p.ld_aux, n), z);
+      if constexpr (GATED) Vec4<T>::store(elem_ptr<T>(p.aux, m, p.ld_aux, p.half + n), v);
+    }
+    linear_act<4, GATED>(p.act, z, v, y);
+    if (p.res) {
+      Vec4<T>::load(elem_ptr<T>(p.res, m, p.ld_res, n), b);
+#pragma unroll
+      for (int r = 0; r < 4; ++r) y[r] += b[r];
+    }
+    Vec4<T>::store(elem_ptr<T>(p.C0, m, p.ldc0, n), y);
+  }
+}
+
+// dz and its column sums over one piece of rows: 32 lanes x 8 columns across, 8 rows down.
+constexpr int kDactCols = 256;
+
+template <typename T, bool GATED>
+__global__ __launch_bounds__(kThr) void linear_dact_kernel(int fn, const void* __restrict__ dy,
+                                                           const void* __restrict__ preact,
+                                                           const int* __restrict__ offsets, int experts, int rows,
+                                                           int N, void* __restrict__ dz, float* __restrict__ sums) {
+  __shared__ float red[8][kDactCols];
+  const int strips = (N + kDactCols - 1) / kDactCols;
+  const int piece = blockIdx.x / strips, strip = blockIdx.x % strips;
+  RowPiece t;
+  if (!find_row_piece(offsets, experts, rows, kDactRows, [&](int total) { return piece < total ? piece : -1; }, t))
+    return;
+  if (t.e == experts) return;   // rows of no expert have no part in any product or sum
+  const int P = GATED ? 2 * N : N;
+  const int c = strip * kDactCols + (threadIdx.x & 31) * 8, rl = threadIdx.x >> 5;
+  const int r0 = t.row0 + t.index * kDactRows, r1 = min(r0 + kDactRows, t.row0 + t.rows);
+  const bool in0 = c < N;
+  const bool half = sizeof(T) == 4 && in0 && c + 8 > N;   // fp32 widths are multiples of 4 only
+  float sg[8] = {}, su[GATED ? 8 : 1] = {};
+  auto load = [&](const void* p, int64_t row, int64_t ld, int col, float (&v)[8]) {
+    if (half) {
+      Vec4<T>::load(elem_ptr<T>(p, row, ld, col), v);
+#pragma unroll
+      for (int q = 4; q < 8; ++q) v[q] = 0.0f;
+    } else {
+      Vec8<T>::load(elem_ptr<T>(p, row, ld, col), v);
+    }
+  };
+  auto store = [&](void* p, int64_t row, int64_t ld, int col, const float (&v)[8]) {
+    if (half) Vec4<T>::store(elem_ptr<T>(p, row, ld, col), v);
+    else Vec8<T>::store(elem_ptr<T>(p, row, ld, col), v);
+  };
+  if (in0) {
+#pragma unroll 2
+    for (int r = r0 + rl; r < r1; r += 8) {
+      float d[8];
+      load(dy, r, N, c, d);
+      if (fn != FN_NONE) {
+        float z[8], f[8], df[8];
+        load(preact, r, P, c, z);
+        linear_fn_grad<8>(fn, z, f, df);
+        if constexpr (GATED) {
+          float u[8], du[8];
+          load(preact, r, P, N + c, u);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            du[q] = d[q] * f[q];
+            d[q] *= u[q] * df[q];
+            su[q] += du[q];
+          }
+          if (dz) store(dz, r, P, N + c, du);
+        } else {
+#pragma unroll
+          for (int q = 0; q < 8; ++q) d[q] *= df[q];
+        }
+        if (dz) store(dz, r, P, c, d);
+      }
+#pragma unroll
+      for (int q = 0; q < 8; ++q) sg[q] += d[q];
+    }
+  }
+  if (sums == nullptr) return;
+  auto join = [&](const float (&v)[8], int col0) {   // the 8 row lanes' sums, in order
+#pragma unroll
+    for (int q = 0; q < 8; ++q) red[rl][(threadIdx.x & 31) * 8 + q] = v[q];
+    __syncthreads();
+    const int n = strip * kDactCols + threadIdx.x;
+    if (n < N) {
+      float s = red[0][threadIdx.x];
+#pragma unroll
+      for (int w = 1; w < 8; ++w) s += red[w][threadIdx.x];
+      sums[(int64_t)piece * P + col0 + n] = s;
+    }
+    __syncthreads();
+  };
+  join(sg, 0);
+  if constexpr (GATED) join(su, N);
+}
+
+// db[e][n] = the sum of expert e's pieces, 64 columns x 4 runs of pieces a workgroup.
+template <typename GT, bool GATED>
+__global__ __launch_bounds__(kThr) void linear_dbias_kernel(const float* __restrict__ sums,
+                                                            const int* __restrict__ offsets, int experts, int rows,
+                                                            int N, int max_pieces, void* db0, void* db1,
+                                                            int accumulate) {
+  __shared__ float red[4][64];
+  const int P = GATED ? 2 * N : N, blocks = (P + 63) / 64;
+  const int e = blockIdx.x / blocks, n = (blockIdx.x % blocks) * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
+  // the expert's first piece: the pieces of the experts before, counted 64 experts at a time
+  int first = 0;
+  for (int base = 0; base < e; base += 64) {
+    int r0, m;
+    const int i = base + (int)(threadIdx.x & 63);
+    expert_rows(offsets, experts, rows, i, r0, m);
+    int v = i < e ? (m + kDactRows - 1) / kDactRows : 0;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    first += v;
+  }
+  int row0, m;
+  expert_rows(offsets, experts, rows, e, row0, m);
+  const int pieces = (m + kDactRows - 1) / kDactRows;
+  const int b = (int)((int64_t)q * pieces / 4);
+  const int end = min((int)((int64_t)(q + 1) * pieces / 4), max_pieces - first);   // offsets may be anything
+  float s = 0.0f;
+  if (n < P) {
+#pragma unroll 8
+    for (int i = b; i < end; ++i) s += sums[(int64_t)(first + i) * P + n];
+  }
+  red[q][threadIdx.x & 63] = s;
+  __syncthreads();
+  if (q != 0 || n >= P) return;
+  s = ((red[0][threadIdx.x] + red[1][threadIdx.x]) + red[2][threadIdx.x]) + red[3][threadIdx.x];
+  void* db = GATED && n >= N ? db1 : db0;
+  const int64_t at = (int64_t)e * N + (GATED && n >= N ? n - N : n);
+  if (accumulate) {
+    if (pieces > 0) reinterpret_cast<float*>(db)[at] += s;
+  } else if constexpr (sizeof(GT) == 4) {
+    reinterpret_cast<float*>(db)[at] = s;
+  } else {
+    reinterpret_cast<uint16_t*>(db)[at] = (uint16_t)Bits16<GT>::from_f32(s);
+  }
+}
+
+// f(type, gated) with the element type of `dt` and an integral constant.
+template <typename F> hipError_t by_type(DType dt, int gated, F f) {
+  auto g = [&](auto v) { return gated ? f(v, std::true_type{}) : f(v, std::false_type{}); };
+  switch (dt) {
+    case DT_F32: return g(float{});
+    case DT_BF16: return g(bf16{});
+    case DT_F16: return g(f16{});
+    default: return hipErrorInvalidValue;
+  }
+}
+
+}  // namespace
+
+hipError_t run_linear_reduce(DType io, int gated, const float* partial, int splits, const GemmArgs& a, hipStream_t s) {
+  const int64_t items = (int64_t)a.M * (a.N / 4);
+  const dim3 grid((unsigned)std::min<int64_t>((items + kThr - 1) / kThr, 256 * 64));
+  return by_type(io, gated, [&](auto v, auto g) {
+    hipLaunchKernelGGL((linear_reduce_kernel<decltype(v), decltype(g)::value>), grid, dim3(kThr), 0, s, partial, splits, a);
+    return hipGetLastError();
+  });
+}
+
+hipError_t run_linear_dact(DType io, int gated, int fn, const void* dy, const void* preact, const int* offsets,
+                           int experts, int64_t rows, int64_t N, void* dz, float* sums, hipStream_t s) {
+  const dim3 grid((unsigned)(dact_pieces(rows, experts) * ((N + kDactCols - 1) / kDactCols)));
+  return by_type(io, gated, [&](auto v, auto g) {
+    hipLaunchKernelGGL((linear_dact_kernel<decltype(v), decltype(g)::value>), grid, dim3(kThr), 0, s, fn, dy, preact,
+                       offsets, experts, (int)rows, (int)N, dz, sums);
+    return hipGetLastError();
+  });
+}
+
+hipError_t run_linear_dbias(DType io, int gated, const float* sums, const int* offsets, int experts, int64_t rows,
+                            int64_t N, void* db0, void* db1, int accumulate, hipStream_t s) {
+  const int64_t P = gated ? 2 * N : N;
+  const dim3 grid((unsigned)(experts * ((P + 63) / 64)));
+  return by_type(io, gated, [&](auto v, auto g) {
+    hipLaunchKernelGGL((linear_dbias_kernel<decltype(v), decltype(g)::value>), grid, dim3(kThr), 0, s, sums, offsets,
+                       experts, (int)rows, (int)N, (int)dact_pieces(rows, experts), db0, db1, accumulate);
+    return hipGetLastError();
+  });
+}
+
+}  // namespace gmlp

@@ -16,7 +16,7 @@
 // narrow store product with a long K (the down projection) splits K over workgroups into fp32
 // partials for the split-K reduce, so that each workgroup reads a quarter of the token rows.
 #include "common.hpp"
-#include "gemm_kernel.hpp"
+#include "gemm_experts.hpp"
 #include "launch.hpp"
 
 namespace gmlp {
@@ -26,6 +26,38 @@ namespace {
 constexpr int kKBlock = 128;       // K per block: four lane groups x 32
 constexpr int kTwoBlocksFrom = 1024;   // output column blocks of 16 from which a workgroup takes two
 
+// The linear epilogues on tokens 4 q .. 4 q + 3 of unit n (those below M): v and u are the
+// sums, rows and pointers those of p.
+template <typename T, int EPI>
+__device__ __forceinline__ void linear_finish(const GemmArgs& p, int M, int q, int n, float (&v)[4], float (&u)[4]) {
+  constexpr bool GATED = epi_gated(EPI);
+  auto get = [](const void* b, int64_t row, int64_t ld, int col) {
+    return Bits16<T>::to_f32(*reinterpret_cast<const uint16_t*>(elem_ptr<T>(b, row, ld, col)));
+  };
+  auto put = [](void* b, int64_t row, int64_t ld, int col, float x) {
+    *reinterpret_cast<uint16_t*>(elem_ptr<T>(b, row, ld, col)) = (uint16_t)Bits16<T>::from_f32(x);
+  };
+  const float b0 = p.bias0 ? get(p.bias0, 0, 0, n) : 0.0f;
+  const float b1 = GATED && p.bias1 ? get(p.bias1, 0, 0, n) : 0.0f;
+  float y[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] += b0;
+    u[i] += b1;
+  }
+  linear_act<4, GATED>(p.act, v, u, y);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = 4 * q + i;
+    if (t >= M) continue;
+    if (p.flags & 1) {
+      put(p.aux, t, p.ld_aux, n, v[i]);
+      if (GATED) put(p.aux, t, p.ld_aux, p.half + n, u[i]);
+    }
+    put(p.C0, t, p.ldc0, n, p.res ? y[i] + get(p.res, t, p.ld_res, n) : y[i]);
+  }
+}
+
 // NCB column blocks of 16 units per workgroup (more units share each load of the token rows);
 // NBUF blocks of loads in flight per wave. KQ > 1 (EPI_PARTIAL): workgroup b takes part b % KQ
 // of K (in 128-wide blocks) for the column blocks of b / KQ and writes unscaled fp32 partial
@@ -34,7 +66,7 @@ constexpr int kTwoBlocksFrom = 1024;   // output column blocks of 16 from which 
 template <typename T, int EPI, int WAVES, int NCB, int NBUF, int KQ = 1>
 __global__ __launch_bounds__(64 * WAVES) void skinny_kernel(const GemmArgs p) {
   static_assert((KQ > 1) == (EPI == EPI_PARTIAL), "K parts across workgroups write partial sums");
-  constexpr bool GATED = EPI == EPI_GATED;
+  constexpr bool GATED = epi_gated(EPI);
   constexpr int NB = GATED ? 2 : 1;   // weight matrices read: gate and up, or one
   constexpr int NACC = NB * NCB;
   __shared__ f32x4 red[WAVES][NACC][64];
@@ -154,7 +186,9 @@ __global__ __launch_bounds__(64 * WAVES) void skinny_kernel(const GemmArgs p) {
         if (t < p.M) *reinterpret_cast<uint16_t*>(elem_ptr<T>(base, t, ld, col)) = (uint16_t)Bits16<T>::from_f32(val[i]);
       }
     };
-    if constexpr (GATED) {
+    if constexpr (epi_linear(EPI)) {
+      linear_finish<T, EPI>(p, p.M, q, n, v, u);
+    } else if constexpr (GATED) {
       if (p.flags & 1) {
         put(p.aux, p.ld_aux, n, v);
         put(p.aux, p.ld_aux, p.half + n, u);
@@ -184,7 +218,7 @@ __global__ __launch_bounds__(64 * WAVES) void skinny_kernel(const GemmArgs p) {
 // column block meet in LDS (over the staged x, no longer read) and are added in kq order.
 constexpr int kLdsBlocks = 32;   // K up to 4096: 128 KB of LDS
 
-template <typename T, int CB, int KQ, int NBUF>
+template <typename T, int EPI, int CB, int KQ, int NBUF>
 __global__ __launch_bounds__(64 * CB * KQ, 1) void skinny_gated_lds_kernel(const GemmArgs p) {
   constexpr int WAVES = CB * KQ;
   __shared__ u32x4 xs[kLdsBlocks * 4 * 64];
@@ -287,6 +321,10 @@ __global__ __launch_bounds__(64 * CB * KQ, 1) void skinny_gated_lds_kernel(const
     v[t] = alpha * s0[t];
     u[t] = alpha * s1[t];
   }
+  if constexpr (epi_linear(EPI)) {
+    linear_finish<T, EPI>(p, p.M, q, n, v, u);
+    return;
+  }
   auto put = [&](void* base, int64_t ld, int col, const float (&val)[4]) {
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -306,13 +344,13 @@ __global__ __launch_bounds__(64 * CB * KQ, 1) void skinny_gated_lds_kernel(const
 
 template <typename T, int EPI>
 hipError_t launch_skinny(const GemmArgs& a, hipStream_t s) {
-  if (EPI == EPI_GATED && a.M > 8 && a.K <= kLdsBlocks * kKBlock) {
+  if constexpr (epi_gated(EPI)) if (a.M > 8 && a.K <= kLdsBlocks * kKBlock) {
     // 3 column blocks x 4 parts of K: 48 units per workgroup of 12 waves, one per CU (128 KB of
     // LDS; 230 workgroups at H = 11008). Measured against the kernel above at the LLaMA widths:
     // 16 tokens 63.9 -> 60.5 us per inference forward, 8 tokens even, 1-4 tokens 1.4 us slower
     // (the x rows it saves are few there), hence the 8-token threshold. 4 x 4 blocks (172
     // workgroups) streamed slower than 230 on more CUs.
-    hipLaunchKernelGGL((skinny_gated_lds_kernel<T, 3, 4, 3>), dim3((a.N + 47) / 48), dim3(768), 0, s, a);
+    hipLaunchKernelGGL((skinny_gated_lds_kernel<T, EPI, 3, 4, 3>), dim3((a.N + 47) / 48), dim3(768), 0, s, a);
     return hipGetLastError();
   }
   const int groups = (a.N + 15) / 16;   // column blocks of 16 units
@@ -324,7 +362,7 @@ hipError_t launch_skinny(const GemmArgs& a, hipStream_t s) {
   } else {
     // few workgroups: K split over more waves, so enough loads are in flight (the gated body
     // keeps two weight matrices in flight and stops at 8 waves, within its register budget)
-    constexpr int W = EPI == EPI_GATED ? 8 : 16;
+    constexpr int W = epi_gated(EPI) ? 8 : 16;
     hipLaunchKernelGGL((skinny_kernel<T, EPI, W, 1, 3>), dim3(groups), dim3(64 * W), 0, s, a);
   }
   return hipGetLastError();
@@ -347,12 +385,142 @@ hipError_t skinny_epi(int epi, const GemmArgs& a, hipStream_t s) {
     case EPI_STORE: return launch_skinny<T, EPI_STORE>(a, s);
     case EPI_ACT: return launch_skinny<T, EPI_ACT>(a, s);
     case EPI_GATED: return launch_skinny<T, EPI_GATED>(a, s);
+    case EPI_LIN: return launch_skinny<T, EPI_LIN>(a, s);
+    case EPI_LIN_GATED: return launch_skinny<T, EPI_LIN_GATED>(a, s);
     case EPI_PARTIAL: return launch_skinny_parts<T>(a, s);
     default: return hipErrorInvalidValue;
   }
 }
 
+// The experts' products with a few rows an expert: workgroup b takes column block b % blocks of expert
+// b / blocks and streams its weights once for every 16 of the expert's rows (once, for most), K over its
+// waves as above; experts without rows cost their workgroups one look at the offsets. The workgroups
+// of "expert" `experts` fill the rows behind the last offset.
+template <typename T, int EPI, int WAVES, int NBUF>
+__global__ __launch_bounds__(64 * WAVES) void skinny_experts_kernel(const ExpertGemm a) {
+  constexpr bool GATED = epi_gated(EPI);
+  constexpr int NB = GATED ? 2 : 1;
+  __shared__ f32x4 red[WAVES][NB][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int r = lane & 15, q = lane >> 4;
+  GemmArgs p = a.g;
+  const int blocks = (p.N + 15) / 16;
+  const int e = blockIdx.x / blocks, n = (blockIdx.x % blocks) * 16 + r;
+  int row0, rows;
+  expert_rows(a.offsets, a.experts, a.rows, e, row0, rows);
+  row0 = __builtin_amdgcn_readfirstlane(row0);
+  rows = __builtin_amdgcn_readfirstlane(rows);
+  const bool row_ok = n < p.N;
+  if (e == a.experts) {
+    if (!row_ok) return;
+    for (int m = row0 + wave * 4 + q; m < row0 + rows; m += 4 * WAVES) {
+      if (p.flags & 1) {
+        *reinterpret_cast<uint16_t*>(elem_ptr<T>(p.aux, m, p.ld_aux, n)) = 0;
+        if (GATED) *reinterpret_cast<uint16_t*>(elem_ptr<T>(p.aux, m, p.ld_aux, p.half + n)) = 0;
+      }
+      *reinterpret_cast<uint16_t*>(elem_ptr<T>(p.C0, m, p.ldc0, n)) =
+          p.res ? *reinterpret_cast<const uint16_t*>(elem_ptr<T>(p.res, m, p.ld_res, n)) : (uint16_t)0;
+    }
+    return;
+  }
+  p.bias0 = shift<T>(p.bias0, e * a.bias_stride);
+  p.bias1 = shift<T>(p.bias1, e * a.bias_stride);
+  const int64_t wrow0 = e * a.w_stride + (int64_t)(row_ok ? n : 0) * p.ldb;
+  const char* wrow[NB];
+  wrow[0] = reinterpret_cast<const char*>(shift<T>(p.B0, wrow0));
+  if constexpr (GATED) wrow[1] = reinterpret_cast<const char*>(shift<T>(p.B1, wrow0));
+  const int nblk = (p.K + kKBlock - 1) / kKBlock;
+  const int b0 = wave * nblk / WAVES, nb = (wave + 1) * nblk / WAVES - b0;
+
+  for (int m0 = 0; m0 < rows; m0 += 16) {
+    const int M = min(16, rows - m0);   // token rows of this pass
+    const bool tok_ok = r < M;
+    const char* xrow = reinterpret_cast<const char*>(elem_ptr<T>(p.A, row0 + m0 + (tok_ok ? r : 0), p.lda, 0));
+    u32x4 xa[NBUF][4], wa[NBUF][NB][4];
+    auto load = [&](int b, int s) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const int k = b * kKBlock + c * 32 + q * 8;
+        const bool k_ok = k < p.K;
+        const int64_t off = (int64_t)k * (int64_t)sizeof(T);
+#pragma unroll
+        for (int m = 0; m < NB; ++m)
+          wa[s][m][c] = (row_ok && k_ok) ? *reinterpret_cast<const u32x4*>(wrow[m] + off) : u32x4{0u, 0u, 0u, 0u};
+        xa[s][c] = (tok_ok && k_ok) ? *reinterpret_cast<const u32x4*>(xrow + off) : u32x4{0u, 0u, 0u, 0u};
+      }
+    };
+    f32x4 acc[NB];
+#pragma unroll
+    for (int m = 0; m < NB; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    auto compute = [&](int s) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int m = 0; m < NB; ++m) Mma16<T>::mma(xa[s][c], wa[s][m][c], acc[m]);
+    };
+#pragma unroll
+    for (int j = 0; j < NBUF - 1; ++j)
+      if (j < nb) load(b0 + j, j);
+    int i = 0;
+    for (; i + NBUF <= nb; i += NBUF) {
+#pragma unroll
+      for (int j = 0; j < NBUF; ++j) {
+        if (i + j + NBUF - 1 < nb) load(b0 + i + j + NBUF - 1, (j + NBUF - 1) % NBUF);
+        compute(j);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < NBUF; ++j)
+      if (i + j < nb) compute(j);
+
+    if (m0 > 0) __syncthreads();   // the first wave has read the last pass's sums
+#pragma unroll
+    for (int m = 0; m < NB; ++m) red[wave][m][lane] = acc[m];
+    __syncthreads();
+    if (wave == 0 && row_ok) {
+      f32x4 s0 = red[0][0][lane], s1 = red[0][NB - 1][lane];
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) {
+        s0 += red[w][0][lane];
+        if constexpr (GATED) s1 += red[w][1][lane];
+      }
+      float v[4] = {s0[0], s0[1], s0[2], s0[3]}, u[4] = {s1[0], s1[1], s1[2], s1[3]};
+      GemmArgs c = p;   // this pass's rows
+      const int64_t at = row0 + m0;
+      c.C0 = shift<T>(p.C0, at * p.ldc0);
+      c.aux = shift<T>(p.aux, at * p.ld_aux);
+      c.res = shift<T>(p.res, at * p.ld_res);
+      linear_finish<T, EPI>(c, M, q, n, v, u);
+    }
+  }
+}
+
+template <typename T, int EPI>
+hipError_t launch_skinny_experts(const ExpertGemm& a, hipStream_t s) {
+  const int64_t blocks = (int64_t)(a.experts + 1) * ((a.g.N + 15) / 16);
+  if (blocks >= 512) {
+    hipLaunchKernelGGL((skinny_experts_kernel<T, EPI, 4, 3>), dim3((unsigned)blocks), dim3(256), 0, s, a);
+  } else {   // few workgroups: K over more waves, so enough loads are in flight
+    hipLaunchKernelGGL((skinny_experts_kernel<T, EPI, 8, 3>), dim3((unsigned)blocks), dim3(512), 0, s, a);
+  }
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t skinny_experts_epi(int epi, const ExpertGemm& a, hipStream_t s) {
+  if (epi == EPI_LIN) return launch_skinny_experts<T, EPI_LIN>(a, s);
+  if (epi == EPI_LIN_GATED) return launch_skinny_experts<T, EPI_LIN_GATED>(a, s);
+  return hipErrorInvalidValue;
+}
+
 }  // namespace
+
+hipError_t run_skinny_experts(DType in, int epi, const ExpertGemm& a, hipStream_t s) {
+  if (a.g.N < 1 || a.g.K < 1 || a.g.K % 8) return hipErrorInvalidValue;
+  if (in == DT_BF16) return skinny_experts_epi<bf16>(epi, a, s);
+  if (in == DT_F16) return skinny_experts_epi<f16>(epi, a, s);
+  return hipErrorInvalidValue;
+}
 
 hipError_t run_skinny(DType in, int epi, const GemmArgs& a, hipStream_t s) {
   if (a.M < 1 || a.M > kSkinnyMaxRows || a.N < 1 || a.K < 1 || a.K % 8) return hipErrorInvalidValue;
