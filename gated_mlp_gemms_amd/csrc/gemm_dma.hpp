@@ -1,10 +1,10 @@
-// The bf16 / e4m3 GEMM kernel: the same contraction and fused epilogues as gemm_kernel.hpp,
+// The 16-bit / 8-bit GEMM kernel, and the linear layer's fp32 one: the same contraction and fused epilogues as gemm_kernel.hpp,
 // with operands moved HBM -> LDS by the LDS-DMA form of the global load (no VGPR staging, no
 // LDS store instructions) through a ring of LDS stages, and a software-pipelined MFMA loop.
 //
 // Per workgroup (4 wave64 in 2 x 2, or 8 in 4 x 2 with two per SIMD; waves of WM x WN):
 //  * one K-step is 128 bytes of K per operand row: 64 k for bf16 (four K=16 MFMA substeps),
-//    128 k for e4m3 (two K=64 substeps); full 128-byte row segments keep every DMA request a
+//    128 k for e4m3 (two K=64 substeps), 32 k for fp32 (four substeps of four K=2 MFMAs); full 128-byte row segments keep every DMA request a
 //    whole cache line;
 //  * K-major operand tiles are [rows][ROWB], 16-byte chunks XOR-swizzled by row;
 //  * MN-major operand tiles (bf16) are [64 k-rows][rows * 2 B], chunks XOR-swizzled by
@@ -111,6 +111,7 @@ template <> struct StepGeo<bf16> { static constexpr int ROWB = 128; };
 template <> struct StepGeo<f16> { static constexpr int ROWB = 128; };
 template <> struct StepGeo<e4m3> { static constexpr int ROWB = 128; };
 template <> struct StepGeo<f8g> { static constexpr int ROWB = 128; };
+template <> struct StepGeo<float> { static constexpr int ROWB = 128; };
 
 // ---- K-major operand: ROWS rows x ROWB bytes per stage -------------------------------------
 // One DMA instruction fills 1 KB = 8 rows of 128 bytes: lane l -> row 8 j + l / 8, slot l % 8,
@@ -434,6 +435,74 @@ struct MNTileDma8 {
   }
 };
 
+// ---- MN-major fp32 operand: 32 k-rows x ROWS columns per stage ---------------------------------
+// DMA instruction j fills KPI = 256 / ROWS k-rows of ROWS * 4 bytes. A fragment is four 4-byte reads a
+// lane (k-row 8 s + 4 (l / 32) + e, column l % 32 of the block): the fp32 MFMA takes 64 cycles for 2 k
+// of a 32 x 32 block, so its reads need not be wide. The two halves of a wave read k-rows 4 apart;
+// their chunks are XORed 8 chunks (half the banks) apart, so the halves meet no common bank.
+template <int ROWS, int WAVES>
+struct MNTileDma32 {
+  static constexpr int KROWS = 32;
+  static constexpr int ROWB = ROWS * 4;                  // bytes per k-row
+  static constexpr int CPR = ROWB / 16;                  // 16-byte chunks per k-row
+  static constexpr int KPI = 1024 / ROWB;                // k-rows per DMA instruction
+  static constexpr int kInst = KROWS * ROWB / 1024 / WAVES;   // per wave per stage
+  static_assert(ROWS == 64 || ROWS == 128, "64- or 128-column tiles");
+  static_assert(kInst >= 1, "tile too narrow");
+  uint32_t voff[kInst];   // per lane: k-row pitch + column bytes
+  const char* base;       // uniform: the matrix at the split's first k, tile column 0
+  int64_t ld_bytes;       // uniform pitch
+
+  static __device__ __forceinline__ int phys_chunk(int c, int kr) { return c ^ (((kr >> 2) & 1) << 3); }
+
+  // ncols: columns of the matrix from tile column 0 on (a multiple of 4); chunks past them read its last one
+  __device__ __forceinline__ void init(int wave, int lane, const char* b, int64_t ld, int kbeg, int ncols) {
+    base = b + (int64_t)kbeg * ld;
+    ld_bytes = ld;
+#pragma unroll
+    for (int i = 0; i < kInst; ++i) {
+      const int kr = KPI * (wave * kInst + i) + lane / CPR;
+      const int col = min(phys_chunk(lane % CPR, kr) * 4, ncols - 4);   // the XOR is an involution
+      voff[i] = (uint32_t)(kr * ld) + (uint32_t)(col * 4);
+    }
+  }
+  __device__ __forceinline__ void issue(char* tile, int wave, int lane, int k0, int kend, int64_t step_off, int k_split,
+                                        int64_t second) const {
+    if (k0 + KROWS <= kend && (k0 + KROWS <= k_split || k0 >= k_split)) {
+      const char* b = base + step_off + (k0 >= k_split ? second : 0);
+#pragma unroll
+      for (int i = 0; i < kInst; ++i) issue_fast_i(tile, wave, i, b);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kInst; ++i) issue_i(tile, wave, lane, i, k0, kend, step_off, k_split, second);
+    }
+  }
+  __device__ __forceinline__ void issue_fast_i(char* tile, int wave, int i, const char* b) const {
+    dma16s(b, voff[i], tile + (wave * kInst + i) * 1024);
+  }
+  __device__ __forceinline__ void issue_i(char* tile, int wave, int lane, int i, int k0, int kend, int64_t step_off,
+                                          int k_split, int64_t second) const {
+    const int k = k0 + KPI * (wave * kInst + i) + lane / CPR;
+    const char* s = opaque_sgpr(base + step_off) + (k >= k_split ? second : 0) + voff[i];
+    dma16(k < kend ? (const void*)s : (const void*)g_zero_chunk, tile + (wave * kInst + i) * 1024);
+  }
+  static __device__ __forceinline__ u32x4 read(const char* tile, int cb, int s, int lane) {
+    const int c = cb + (lane & 31);
+    u32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int kr = 8 * s + 4 * (lane >> 5) + e;
+      v[e] = *reinterpret_cast<const uint32_t*>(tile + kr * ROWB + (phys_chunk(c >> 2, kr) << 4) + (c & 3) * 4);
+    }
+    return v;
+  }
+};
+
+// The MN-major loader of an element type: 8-bit codes, 16-bit (PAT as there), fp32.
+template <int ES, int ROWS, int WAVES, bool PAT> struct MNTileSel { using type = MNTileDma<ROWS, WAVES, PAT>; };
+template <int ROWS, int WAVES, bool PAT> struct MNTileSel<1, ROWS, WAVES, PAT> { using type = MNTileDma8<ROWS, WAVES>; };
+template <int ROWS, int WAVES, bool PAT> struct MNTileSel<4, ROWS, WAVES, PAT> { using type = MNTileDma32<ROWS, WAVES>; };
+
 // Stages in the ring: as many as fit the 160 KiB of LDS, at most 4; tiles of 128 x 128 and
 // below keep room for two workgroups per CU (a second workgroup hides latency better than a
 // deeper ring).
@@ -452,7 +521,7 @@ template <typename T, int BM, int BN>
 constexpr int extra_a_stages() {
   constexpr int stage = (BM + BN) * StepGeo<T>::ROWB, a = BM * StepGeo<T>::ROWB;
   constexpr int ns = ring_stages(stage, BM * BN);
-  return (BM * BN <= 128 * 128 && ns < 4 && ns * stage + a <= 80 * 1024) ? 1 : 0;
+  return (BM * BN <= 128 * 128 && ns == 2 && ns * stage + a <= 80 * 1024) ? 1 : 0;
 }
 
 // LDS of one workgroup's ring (NS stages of a BM x BN tile's K-step, plus the extra A stages).
@@ -472,7 +541,8 @@ constexpr int dma_ring_bytes() {
 template <typename T, typename IoT, int BM, int BN, bool A_KMAJ, bool B_KMAJ, int EPI, int WAVES, bool SKIP = false>
 __device__ __forceinline__ void gemm_dma_tile(const GemmArgs p, int item, char* smem) {
   static_assert(BM % 64 == 0 && BN % 64 == 0, "tile must split into 2x2 waves of 32x32 blocks");
-  static_assert((A_KMAJ && B_KMAJ) || ElemTraits<T>::bytes == 2 || (WAVES == 4 && !A_KMAJ && !B_KMAJ),
+  static_assert(ElemTraits<T>::bytes != 4 || WAVES == 4, "fp32 tiles have one wave per SIMD");
+  static_assert((A_KMAJ && B_KMAJ) || ElemTraits<T>::bytes != 1 || (WAVES == 4 && !A_KMAJ && !B_KMAJ),
                 "8-bit operands are MN-major only in 4-wave TN tiles");
   constexpr int ES = ElemTraits<T>::bytes;
   constexpr int ROWB = StepGeo<T>::ROWB;
@@ -489,12 +559,11 @@ __device__ __forceinline__ void gemm_dma_tile(const GemmArgs p, int item, char* 
   constexpr int NS = ring_stages(STAGE, BM * BN);
   static_assert(NS >= 2, "the ring needs two stages");
   constexpr bool GATED = epi_gated(EPI);
-  constexpr int KMMA = M16 ? 32 : (ES == 1 ? 64 : 16);
+  constexpr int KMMA = M16 ? 32 : (ES == 1 ? 64 : ES == 4 ? 8 : 16);
   constexpr int NSUB = BK / KMMA;
   constexpr int KC = Mma<T>::kChunks;
   static_assert(NSUB % 2 == 0, "fragment double buffer alternates per substep");
-  // the MN-major loaders (16-bit, or 8-bit codes)
-  using MNA = typename std::conditional<ES == 1, MNTileDma8<BM, WAVES>, MNTileDma<BM, WAVES>>::type;
+  using MNA = typename MNTileSel<ES, BM, WAVES, true>::type;
   static_assert(A_KMAJ || BK == MNA::KROWS, "MN-major stage depth");
 
   // XA = 1: A has a ring of its own, NSA = NS + 1 stages, and B one of NS (A stages first,
@@ -531,8 +600,8 @@ __device__ __forceinline__ void gemm_dma_tile(const GemmArgs p, int item, char* 
   KTileDma<T, BM, DW> ka;
   KTileDma<T, BN, DW> kb;
   // offsets per pattern with the burst issue, per instruction when spread (16-bit)
-  using NLA = typename std::conditional<ES == 1, MNTileDma8<BM, DW>, MNTileDma<BM, DW, A_KMAJ>>::type;
-  using NLB = typename std::conditional<ES == 1, MNTileDma8<BN, DW>, MNTileDma<BN, DW, A_KMAJ>>::type;
+  using NLA = typename MNTileSel<ES, BM, DW, A_KMAJ>::type;
+  using NLB = typename MNTileSel<ES, BN, DW, A_KMAJ>::type;
   NLA na;
   NLB nb;
   // K-major tile rows: locA / locB(r) -> {base, rows past it} (rows past the matrix clamped)
@@ -665,7 +734,7 @@ __device__ __forceinline__ void gemm_dma_tile(const GemmArgs p, int item, char* 
         else if constexpr (M16) fa[slot][i][c] = MNTileDma<BM, WAVES>::read16(sa, a_base[i], s, lane);
         else if constexpr (ES == 1) {
           if (c == 0) MNTileDma8<BM, WAVES>::read8(sa, a_base[i], s, lane, fa[slot][i][0], fa[slot][i][1]);
-        } else fa[slot][i][c] = MNTileDma<BM, WAVES>::read(sa, a_base[i], s, lane);
+        } else fa[slot][i][c] = MNTileSel<ES, BM, WAVES, true>::type::read(sa, a_base[i], s, lane);
       }
     }
   };
@@ -678,7 +747,7 @@ __device__ __forceinline__ void gemm_dma_tile(const GemmArgs p, int item, char* 
       else if constexpr (M16) fb[slot][j][c] = MNTileDma<BN, WAVES>::read16(sb, b_base[j], s, lane);
       else if constexpr (ES == 1) {
         if (c == 0) MNTileDma8<BN, WAVES>::read8(sb, b_base[j], s, lane, fb[slot][j][0], fb[slot][j][1]);
-      } else fb[slot][j][c] = MNTileDma<BN, WAVES>::read(sb, b_base[j], s, lane);
+      } else fb[slot][j][c] = MNTileSel<ES, BN, WAVES, true>::type::read(sb, b_base[j], s, lane);
     }
   };
   auto read_frags = [&](int stage_a, int stage_b, int s, int slot) {
@@ -697,7 +766,7 @@ __device__ __forceinline__ void gemm_dma_tile(const GemmArgs p, int item, char* 
 #pragma unroll
       for (int r = 0; r < ACC_N; ++r) acc[i][j][r] = 0.0f;
 
-  constexpr int MN_RD = ES == 1 ? 4 : 2;   // transposing LDS reads per MN-major fragment
+  constexpr int MN_RD = ES == 2 ? 2 : 4;   // LDS reads per MN-major fragment
   constexpr int N_RD = (A_KMAJ ? MI * KC : MN_RD * MI) + (B_KMAJ ? NI * KC : MN_RD * NI);
   constexpr int N_MMA = MI * NI;
 
@@ -862,7 +931,9 @@ __device__ __forceinline__ void gemm_dma_tile(const GemmArgs p, int item, char* 
   wait_vmcnt<0>();
   wait_lgkmcnt0();
   __builtin_amdgcn_s_barrier();
-  epilogue_rows<EPI, IoT, BM, BN, MI, NI, WAVES>(p, acc, m0, n0, split, wm, wn, lane, wave, smem);
+  // fp32 widths are multiples of 4 only: straight from the accumulators, 4 columns at a time
+  if constexpr (ES == 4) epilogue<EPI, IoT, BM, BN, MI, NI>(p, acc, m0, n0, split, wm, wn, lane);
+  else epilogue_rows<EPI, IoT, BM, BN, MI, NI, WAVES>(p, acc, m0, n0, split, wm, wn, lane, wave, smem);
 }
 
 // One GEMM: a workgroup per tile, placed XCD-aware (xcd_remap).

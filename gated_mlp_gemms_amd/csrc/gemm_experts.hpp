@@ -1,5 +1,4 @@
-// One product an expert in one launch (ExpertGemm): the tile bodies of gemm_dma.hpp (16-bit) and
-// gemm_kernel.hpp (fp32) with the operands moved to an expert's rows and weights. How many rows an
+// One product an expert in one launch (ExpertGemm): the tile body of gemm_dma.hpp with the operands moved to an expert's rows and weights. How many rows an
 // expert has is known on the device only, so a launch over rows has as many workgroups as the rows
 // could need at most (every expert may end in a partial tile); each workgroup counts the experts'
 // tiles from the offsets (a wave scan, no memory but the offsets) and takes one or none.
@@ -82,18 +81,6 @@ template <typename T> __device__ __forceinline__ void* shift(void* p, int64_t el
   return p ? reinterpret_cast<char*>(p) + elems * ElemTraits<T>::bytes : nullptr;
 }
 
-template <typename T, int BM, int BN>
-constexpr int expert_lds_bytes() {
-  if constexpr (sizeof(T) == 4) return 2 * (BM + BN) * 128;
-  else return dma_ring_bytes<T, BM, BN>();
-}
-
-template <typename T, typename IoT, int BM, int BN, bool AK, bool BK, int EPI, int WAVES>
-__device__ __forceinline__ void expert_tile(const GemmArgs& p, int item, char* smem) {
-  if constexpr (sizeof(T) == 4) gemm_tile<T, IoT, BM, BN, AK, BK, EPI>(p, item, smem);
-  else gemm_dma_tile<T, IoT, BM, BN, AK, BK, EPI, WAVES, true>(p, item, smem);
-}
-
 // Tile b of a product over rows: y = x W_e^T with a linear epilogue, or dx = dz W_e.
 template <typename T, int BM, int BN, bool BK, int EPI, int WAVES>
 __device__ __forceinline__ void expert_rows_tile(const ExpertGemm& a, int b, char* smem) {
@@ -137,7 +124,7 @@ __device__ __forceinline__ void expert_rows_tile(const ExpertGemm& a, int b, cha
   p.B1 = shift<T>(p.B1, t.e * a.w_stride);
   p.bias0 = shift<T>(p.bias0, t.e * a.bias_stride);
   p.bias1 = shift<T>(p.bias1, t.e * a.bias_stride);
-  expert_tile<T, T, BM, BN, true, BK, EPI, WAVES>(p, tile - t.first * tiles_n, smem);
+  gemm_dma_tile<T, T, BM, BN, true, BK, EPI, WAVES, true>(p, tile - t.first * tiles_n, smem);
 }
 
 // Tile `item` of the weight gradients dW_e = dz^T x over expert e's rows.
@@ -156,18 +143,18 @@ __device__ __forceinline__ void expert_grad_tile(const ExpertGemm& a, int item, 
   p.B0 = shift<T>(p.B0, row0 * p.ldb);
   p.C0 = shift<GT>(p.C0, e * a.w_stride);
   p.C1 = shift<GT>(p.C1, e * a.w_stride);
-  expert_tile<T, GT, BM, BN, false, false, EPI_STORE, WAVES>(p, item - e * tiles, smem);
+  gemm_dma_tile<T, GT, BM, BN, false, false, EPI_STORE, WAVES, true>(p, item - e * tiles, smem);
 }
 
 template <typename T, int BM, int BN, int EPI, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 1) void expert_fwd_kernel(const ExpertGemm a) {
-  __shared__ __attribute__((aligned(1024))) char smem[expert_lds_bytes<T, BM, BN>()];
+  __shared__ __attribute__((aligned(1024))) char smem[dma_ring_bytes<T, BM, BN>()];
   expert_rows_tile<T, BM, BN, true, EPI, WAVES>(a, blockIdx.x, smem);
 }
 
 template <typename T, typename GT, int BM, int BN, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 1) void expert_bwd_kernel(const ExpertBwd a) {
-  __shared__ __attribute__((aligned(1024))) char smem[expert_lds_bytes<T, BM, BN>()];
+  __shared__ __attribute__((aligned(1024))) char smem[dma_ring_bytes<T, BM, BN>()];
   const int b = blockIdx.x;
   if (b < a.dx.grid) expert_rows_tile<T, BM, BN, false, EPI_STORE, WAVES>(a.dx, b, smem);
   else expert_grad_tile<T, GT, BM, BN, WAVES>(a.dw, xcd_remap(b - a.dx.grid, a.dw.grid), smem);

@@ -393,10 +393,8 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, f32x16 (&acc)[MI][NI
 
 // ---- the kernel --------------------------------------------------------------------------------
 
-// One output tile: tile `item` of p's grid (tiles_m x tiles_n x splits), with `smem` the
-// workgroup's 2 * (BM + BN) * 128 bytes of LDS.
 template <typename T, typename IoT, int BM, int BN, bool A_KMAJ, bool B_KMAJ, int EPI>
-__device__ __forceinline__ void gemm_tile(const GemmArgs p, int item, char* smem) {
+__global__ __launch_bounds__(kThreads, 1) void gemm_kernel(const GemmArgs p) {
   static_assert(BM % 64 == 0 && BN % 64 == 0, "tile must split into 2x2 waves of 32x32 blocks");
   static_assert(!epi_gated(EPI) || B_KMAJ, "gated epilogue reads K-major weights");
   constexpr int ES = ElemTraits<T>::bytes;
@@ -408,10 +406,12 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs p, int item, char* smem
   constexpr bool GATED = epi_gated(EPI);
   static_assert(!GATED || NI % 2 == 0, "gated tile needs gate and up blocks per wave");
 
+  __shared__ __attribute__((aligned(16))) char smem[2 * STAGE];
+
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int wm = wave >> 1, wn = wave & 1;
 
-  int lid = item;
+  int lid = xcd_remap(blockIdx.x, gridDim.x);
   const int tiles = p.tiles_m * p.tiles_n;
   const int split = lid / tiles;
   lid -= split * tiles;
@@ -442,8 +442,7 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs p, int item, char* smem
         return elem_ptr<T>(r < half ? p.B0 : p.B1, n, p.ldb, 0);
       } else {
         const int n = n0 + r;
-        if (n >= p.N) return nullptr;   // rows n >= b_split from B1 (stacked [W_gate; W_up])
-        return n < p.b_split ? elem_ptr<T>(p.B0, n, p.ldb, 0) : elem_ptr<T>(p.B1, n - p.b_split, p.ldb, 0);
+        return n < p.N ? elem_ptr<T>(p.B0, n, p.ldb, 0) : nullptr;
       }
     });
   }
@@ -530,12 +529,6 @@ __device__ __forceinline__ void gemm_tile(const GemmArgs p, int item, char* smem
   }
 
   epilogue<EPI, IoT, BM, BN, MI, NI>(p, acc, m0, n0, split, wm, wn, lane);
-}
-
-template <typename T, typename IoT, int BM, int BN, bool A_KMAJ, bool B_KMAJ, int EPI>
-__global__ __launch_bounds__(kThreads, 1) void gemm_kernel(const GemmArgs p) {
-  __shared__ __attribute__((aligned(16))) char smem[2 * (BM + BN) * 128];
-  gemm_tile<T, IoT, BM, BN, A_KMAJ, B_KMAJ, EPI>(p, xcd_remap(blockIdx.x, gridDim.x), smem);
 }
 
 template <typename T, typename IoT, int BM, int BN, bool A_KMAJ, bool B_KMAJ, int EPI>

@@ -64,6 +64,9 @@ int bk_of(DType in);   // K elements of one K-step
 // gated: N counts hidden units and a tile covers bn/2 of them (gate + up rows). only_tile >= 0
 // restricts the choice to that tile shape.
 Plan plan_gemm(DType in, int64_t M, int64_t N, int64_t K, bool allow_split, bool gated, int only_tile = -1);
+// The same over another list of tile shapes.
+Plan plan_tiles(const TileInfo* tiles, int count, DType in, int64_t M, int64_t N, int64_t K, bool allow_split,
+                bool gated);
 size_t partial_bytes(const Plan& p, int64_t M, int64_t N);
 
 // A store-epilogue GEMM cut along M: rows [0, m1) by `main`, the rest by `tail` (m1 = 0: all by

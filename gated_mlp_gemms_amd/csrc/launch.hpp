@@ -11,9 +11,11 @@ namespace gmlp {
 // DT_F8G: the fp8-gradient GEMM operand pair (A e5m2, B e4m3); an input type only.
 enum DType : int { DT_F32 = 0, DT_BF16 = 1, DT_E4M3 = 2, DT_F16 = 3, DT_F8G = 4 };
 enum Layout : int { NT = 0, NN = 1, TN = 2 };   // A K-major/B K-major, A K/B MN, A MN/B MN
-// Tile shapes of the bf16 / e4m3 kernel; _W8 runs the tile with 8 waves (two per SIMD).
+// Tile shapes of the bf16 / e4m3 kernel; _W8 runs the tile with 8 waves (two per SIMD). _RING: the
+// linear layer's and the experts' fp32 tiles, on the 16-bit kernels' DMA ring (64 x 64: 64 x 128 gated).
 enum TileShape : int {
-  TILE_256x256 = 0, TILE_256x128 = 1, TILE_128x128 = 2, TILE_256x256_W8 = 3, TILE_256x128_W8 = 4, TILE_COUNT = 5
+  TILE_256x256 = 0, TILE_256x128 = 1, TILE_128x128 = 2, TILE_256x256_W8 = 3, TILE_256x128_W8 = 4, TILE_128x128_RING = 5,
+  TILE_64x64_RING = 6, TILE_COUNT = 7
 };
 
 // One GEMM launch. `io` is the element type of the epilogue's stored/loaded tensors (for
@@ -61,19 +63,20 @@ inline bool skinny_parts_for(int64_t M, int64_t N, int64_t K) { return M > 8 && 
 hipError_t run_gemm_linear(DType in, int epi, TileShape tile, const GemmArgs& a, int grid, hipStream_t s);
 hipError_t run_gemm_bf16_linear(int epi, TileShape tile, const GemmArgs& a, int grid, hipStream_t s);
 hipError_t run_gemm_f16_linear(int epi, TileShape tile, const GemmArgs& a, int grid, hipStream_t s);
-hipError_t run_gemm_f32_linear(int epi, const GemmArgs& a, int grid, hipStream_t s);
+// fp32 on the DMA ring: NT with the linear epilogues or partial sums, NN and TN with the store or those.
+hipError_t run_gemm_f32_ring(Layout layout, int epi, TileShape tile, const GemmArgs& a, int grid, hipStream_t s);
 // The same from fp32 partials [splits][M][N] (gated: [splits][M][2N], g then u), summed in order.
 hipError_t run_linear_reduce(DType io, int gated, const float* partial, int splits, const GemmArgs& a, hipStream_t s);
 
-// One product an expert (ExpertGemm). Tiles: TILE_256x256_W8 and TILE_128x128 (f32: the latter).
+// One product an expert (ExpertGemm). Tiles: TILE_256x256_W8 and TILE_128x128, f32 the _RING ones.
 hipError_t run_expert_fwd(DType in, int epi, TileShape tile, const ExpertGemm& a, hipStream_t s);
 hipError_t run_expert_bwd(DType in, TileShape tile, const ExpertBwd& a, hipStream_t s);
 hipError_t run_expert_fwd_bf16(int epi, TileShape tile, const ExpertGemm& a, hipStream_t s);
 hipError_t run_expert_fwd_f16(int epi, TileShape tile, const ExpertGemm& a, hipStream_t s);
-hipError_t run_expert_fwd_f32(int epi, const ExpertGemm& a, hipStream_t s);
+hipError_t run_expert_fwd_f32(int epi, TileShape tile, const ExpertGemm& a, hipStream_t s);
 hipError_t run_expert_bwd_bf16(TileShape tile, const ExpertBwd& a, hipStream_t s);
 hipError_t run_expert_bwd_f16(TileShape tile, const ExpertBwd& a, hipStream_t s);
-hipError_t run_expert_bwd_f32(const ExpertBwd& a, hipStream_t s);
+hipError_t run_expert_bwd_f32(TileShape tile, const ExpertBwd& a, hipStream_t s);
 // The forward with a few rows an expert, 16-bit (g.N output columns, any rows; grid is unused).
 hipError_t run_skinny_experts(DType in, int epi, const ExpertGemm& a, hipStream_t s);
 

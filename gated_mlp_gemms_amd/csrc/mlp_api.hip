@@ -91,15 +91,14 @@ int bk_of(DType in) { return is_fp8(in) ? 128 : (in == DT_F32 ? 32 : 64); }
 
 // gated: N counts hidden units and a tile covers bn/2 of them (gate + up rows). only_tile >= 0
 // restricts the choice to that tile shape.
-Plan plan_gemm(DType in, int64_t M, int64_t N, int64_t K, bool allow_split, bool gated, int only_tile) {
+Plan plan_tiles(const TileInfo* tiles, int count, DType in, int64_t M, int64_t N, int64_t K, bool allow_split,
+                bool gated) {
   const int bk = bk_of(in);
   const double per_cu = (is_fp8(in) ? 2.0 : in == DT_F32 ? 1.0 / 16.0 : 1.0) * 9.83e12;
   Plan best{};
   double best_t = 1e300;
-  for (const TileInfo& ti : kTiles) {
-    if (in == DT_F32 && ti.t != TILE_128x128) continue;
-    if (is_fp8(in) && (ti.t == TILE_256x256_W8 || ti.t == TILE_256x128_W8)) continue;
-    if (only_tile >= 0 && ti.t != only_tile) continue;
+  for (int i = 0; i < count; ++i) {
+    const TileInfo& ti = tiles[i];
     const int64_t bn_units = gated ? ti.bn / 2 : ti.bn;
     const int64_t tm = (M + ti.bm - 1) / ti.bm, tn = (N + bn_units - 1) / bn_units;
     const int max_split = allow_split ? 16 : 1;
@@ -141,6 +140,18 @@ Plan plan_gemm(DType in, int64_t M, int64_t N, int64_t K, bool allow_split, bool
 // takes the same plan as the forward.
 Plan plan_quantizing(DType in, int64_t M, int64_t N, int64_t K) {
   return plan_gemm(in, M, N, K, false, false, TILE_128x128);
+}
+
+Plan plan_gemm(DType in, int64_t M, int64_t N, int64_t K, bool allow_split, bool gated, int only_tile) {
+  TileInfo tiles[kTileInfos];
+  int count = 0;
+  for (const TileInfo& ti : kTiles) {
+    if (in == DT_F32 && ti.t != TILE_128x128) continue;
+    if (is_fp8(in) && (ti.t == TILE_256x256_W8 || ti.t == TILE_256x128_W8)) continue;
+    if (only_tile >= 0 && ti.t != only_tile) continue;
+    tiles[count++] = ti;
+  }
+  return plan_tiles(tiles, count, in, M, N, K, allow_split, gated);
 }
 
 size_t partial_bytes(const Plan& p, int64_t M, int64_t N) {

@@ -60,10 +60,54 @@ __device__ __forceinline__ float key_score(uint32_t key) {
   return __uint_as_float(key ^ ((key >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
+// A 16-bit score's key and its expert in one word that orders by score, then lowest expert first.
+template <typename T> __device__ __forceinline__ uint32_t packed_key(float x, int e) {
+  const float y = x + 0.0f;
+  uint32_t h;   // y's own 16 bits, which it came from
+  if constexpr (__is_same(T, bf16)) h = __float_as_uint(y) >> 16;
+  else h = Bits16<T>::from_f32(y);
+  const uint32_t key = x != x ? 0xffffu : h ^ ((h >> 15) ? 0xffffu : 0x8000u);
+  return (key << 16) | (uint32_t)(0xffff - e);
+}
+template <typename T> __device__ __forceinline__ float packed_score(uint32_t m) {
+  const uint32_t key = m >> 16;
+  return Bits16<T>::to_f32(key ^ ((key >> 15) ? 0x8000u : 0xffffu));
+}
+
 constexpr int kRouteThreads = 256;
 
+template <typename T, int C> struct ScorePart {   // C scores as one aligned piece
+  static constexpr int B = C * (int)sizeof(T);
+  struct alignas(B < 4 ? 4 : B < 16 ? B : 16) type { uint32_t w[(B + 3) / 4]; };
+};
+
+// The scores of lane `lane`'s experts lane C .. lane C + C - 1 of a row of E; `pad` past the row. Where C
+// divides E a lane's scores are one aligned piece, loaded whole.
+template <typename T, int C>
+__device__ __forceinline__ void load_scores(const void* logits, int64_t row, int E, int lane, bool live, float pad,
+                                            float (&x)[C]) {
+  const int e0 = lane * C;
+  if (C > 1 && E % C == 0) {
+    using Part = typename ScorePart<T, C>::type;
+    Part part = {};
+    const bool in = live && e0 < E;
+    if (in) part = *reinterpret_cast<const Part*>(reinterpret_cast<const char*>(logits) + (row * E + e0) * (int64_t)sizeof(T));
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+      if constexpr (sizeof(T) == 4) x[j] = in ? __uint_as_float(part.w[j]) : pad;
+      else x[j] = in ? Bits16<T>::to_f32(j & 1 ? part.w[j / 2] >> 16 : part.w[j / 2] & 0xffffu) : pad;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < C; ++j) x[j] = live && e0 + j < E ? load1<T>(logits, row * E + e0 + j) : pad;
+  }
+}
+
 // L lanes a token, C scores a lane (lane l holds experts l C .. l C + C - 1). Each of the k rounds
-// takes the largest key left, lowest expert first, and clears it.
+// takes the largest key left, lowest expert first, and clears it. A 16-bit score and its expert fit one
+// 32-bit key (upper half of the score's key, lower half counting experts down), so a round is one
+// reduction; fp32 scores take a second one for the expert.
+// 16384 tokens x 128 scores, k = 8: bound by the rounds' instructions (reading the scores takes 1 us).
 template <typename T, int L, int C>
 __global__ __launch_bounds__(kRouteThreads) void route_kernel(const void* __restrict__ logits, int64_t tokens, int E,
                                                               int k, int sigmoid, int renorm, int* __restrict__ ids,
@@ -71,15 +115,16 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const void* __rest
   const int lane = threadIdx.x & (L - 1);
   const int64_t t = (int64_t)blockIdx.x * (kRouteThreads / L) + threadIdx.x / L;
   const bool live = t < tokens;
+  constexpr bool PACKED = sizeof(T) == 2;
+  float x[C];
   uint32_t key[C];
+  load_scores<T, C>(logits, t, E, lane, live, 0.0f, x);
 #pragma unroll
   for (int j = 0; j < C; ++j) {
     const int e = lane * C + j;
-    key[j] = live && e < E ? score_key(load1<T>(logits, t * E + e)) : 0u;
+    if constexpr (PACKED) key[j] = e < E ? packed_key<T>(x[j], e) : 0u;
+    else key[j] = e < E ? score_key(x[j]) : 0u;
   }
-  float x[C];   // kept for the softmax over every expert
-#pragma unroll
-  for (int j = 0; j < C; ++j) x[j] = key_score(key[j]);
 
   int my_id = 0;
   float my_score = 0.0f, top = 0.0f;
@@ -88,13 +133,22 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const void* __rest
 #pragma unroll
     for (int j = 1; j < C; ++j) m = max(m, key[j]);
     m = group_max<L>(m);
-    uint32_t at = 0xffffffffu;
+    uint32_t at;
+    float s;
+    if constexpr (PACKED) {
 #pragma unroll
-    for (int j = C - 1; j >= 0; --j) at = key[j] == m ? (uint32_t)(lane * C + j) : at;
-    at = group_min<L>(at);
+      for (int j = 0; j < C; ++j) key[j] = key[j] == m ? 0u : key[j];   // keys are distinct
+      at = 0xffffu - (m & 0xffffu);
+      s = packed_score<T>(m);
+    } else {
+      at = 0xffffffffu;
 #pragma unroll
-    for (int j = 0; j < C; ++j) key[j] = at == (uint32_t)(lane * C + j) ? 0u : key[j];
-    const float s = key_score(m);
+      for (int j = C - 1; j >= 0; --j) at = key[j] == m ? (uint32_t)(lane * C + j) : at;
+      at = group_min<L>(at);
+#pragma unroll
+      for (int j = 0; j < C; ++j) key[j] = at == (uint32_t)(lane * C + j) ? 0u : key[j];
+      s = key_score(m);
+    }
     if (i == 0) top = s;
     if (i == lane) {
       my_id = (int)at;
@@ -125,6 +179,21 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const void* __rest
   if (live && mine) {
     ids[t * k + lane] = my_id;
     weights[t * k + lane] = w;
+  }
+}
+
+// f(id, coefficient) of choice I, I + 1, .. k - 1, which lane I of the group holds. Lane I of 16 reaches its
+// row as a DPP operand (row broadcast); wider groups shuffle.
+template <int L, int I, typename F>
+__device__ __forceinline__ void each_choice(int k, int id, float coef, F f) {
+  if constexpr (I < 16) {
+    if (I < k) {   // uniform
+      if constexpr (L == 16)
+        f((int)dpp<0x150 + I>((uint32_t)id), __uint_as_float(dpp<0x150 + I>(__float_as_uint(coef))));
+      else
+        f(__shfl(id, I, L), __shfl(coef, I, L));
+      each_choice<L, I + 1>(k, id, coef, f);
+    }
   }
 }
 
@@ -176,12 +245,9 @@ __global__ __launch_bounds__(kRouteThreads) void route_bwd_kernel(const void* __
   } else {
     float x[C];
     uint32_t m = 0u;
+    load_scores<T, C>(logits, t, E, lane, live, -INFINITY, x);
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-      const int e = lane * C + j;
-      x[j] = live && e < E ? load1<T>(logits, t * E + e) : -INFINITY;
-      m = max(m, score_key(x[j]));
-    }
+    for (int j = 0; j < C; ++j) m = max(m, score_key(x[j]));
     const float top = key_score(group_max<L>(m));
     if (top != -INFINITY) {
       float part = 0.0f;
@@ -198,13 +264,23 @@ __global__ __launch_bounds__(kRouteThreads) void route_bwd_kernel(const void* __
       for (int j = 0; j < C; ++j) d[j] = -(x[j] / total) * mean;
     }
   }
-  for (int i = 0; i < k; ++i) {
-    const int at = __shfl(id, i, L);
-    const float c = __shfl(coef, i, L);
+  each_choice<L, 0>(k, id, coef, [&](int at, float c) {
 #pragma unroll
     for (int j = 0; j < C; ++j) d[j] += at == lane * C + j ? c : 0.0f;
-  }
+  });
   if (!live) return;
+  if (C > 1 && E % C == 0) {   // a lane's gradients are one aligned piece
+    using Part = typename ScorePart<T, C>::type;
+    Part part;
+#pragma unroll
+    for (int j = 0; j < (int)(sizeof part.w / 4); ++j) {
+      if constexpr (sizeof(T) == 4) part.w[j] = __float_as_uint(d[j]);
+      else part.w[j] = pack16x2<T>(d[2 * j], d[C > 1 ? 2 * j + 1 : 0]);
+    }
+    if (lane * C < E)
+      *reinterpret_cast<Part*>(reinterpret_cast<char*>(dlogits) + (t * E + lane * C) * (int64_t)sizeof(T)) = part;
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < C; ++j) {
     const int e = lane * C + j;

@@ -95,6 +95,14 @@ GemmArgs linear_args(const linear_desc* d) {
   return a;
 }
 
+// plan_gemm, with fp32 on the ring tiles. A 64 x 64 tile's K-step takes a quarter of a 128 x 128 one's:
+// small products, and those whose large tiles leave CUs idle.
+Plan plan_linear_gemm(DType in, int64_t M, int64_t N, int64_t K, bool allow_split, bool gated) {
+  if (in != DT_F32) return plan_gemm(in, M, N, K, allow_split, gated);
+  const TileInfo tiles[] = {{TILE_128x128_RING, 128, 128, 2, 0.85}, {TILE_64x64_RING, 64, gated ? 128 : 64, 2, 0.70}};
+  return plan_tiles(tiles, 2, in, M, N, K, allow_split, gated);
+}
+
 // Forward with one weight: the fused product, or split along K into fp32 partials that
 // run_linear_reduce finishes (gated: of the stacked [g | u]); whichever the time model prefers.
 struct LinearFwd {
@@ -107,8 +115,9 @@ LinearFwd plan_linear(const linear_desc* d) {
   const bool gated = is_gated(d->act);
   f.skinny = io != DT_F32 && d->M <= kSkinnyMaxRows;
   if (f.skinny || d->M == 0) return f;
-  f.plan = plan_gemm(io, d->M, d->N, d->K, false, gated);
-  const Plan split = plan_gemm(io, d->M, gated ? 2 * d->N : d->N, d->K, true, false);
+  f.plan = plan_linear_gemm(io, d->M, d->N, d->K, false, gated);
+  if (gated && d->N % 8) return f;   // the stacked operand changes matrices at a multiple of 8 rows only
+  const Plan split = plan_linear_gemm(io, d->M, gated ? 2 * d->N : d->N, d->K, true, false);
   if (split.splits > 1 && split.est < f.plan.est) f.plan = split;
   return f;
 }
@@ -120,14 +129,23 @@ struct ExpertPlan {
   TileShape tile;
   int bm, bn;
 };
-ExpertPlan plan_experts(DType io, int64_t M, int64_t E, bool fwd) {
-  if (fwd && io != DT_F32 && M <= kSkinnyMaxRows * E) return {EXPERT_SKINNY, TILE_128x128, 128, 128};
-  if (io == DT_F32 || M < 256 * E) return {EXPERT_TILES, TILE_128x128, 128, 128};
-  return {EXPERT_TILES, TILE_256x256_W8, 256, 256};
-}
-
 // Row tiles of bm rows that M rows of E experts (and the rows behind them) take at most.
 int64_t row_tiles(int64_t M, int64_t E, int64_t bm) { return M / bm + std::min(M, E) + 1; }
+
+ExpertPlan plan_experts(const linear_desc* d, bool fwd) {
+  const DType io = dtype_of(d->dtype);
+  const int64_t M = d->M, E = std::max(d->experts, 1), N = fwd ? d->N : d->K;
+  const bool gated = is_gated(d->act);
+  if (io == DT_F32) {
+    // 128 x 128 tiles that leave CUs idle: smaller ones (a K-step of theirs takes a quarter as long)
+    const int64_t tn = (N + (fwd && gated ? 63 : 127)) / (fwd && gated ? 64 : 128);
+    if (row_tiles(M, E, 128) * tn < 512) return {EXPERT_TILES, TILE_64x64_RING, 64, fwd && gated ? 128 : 64};
+    return {EXPERT_TILES, TILE_128x128_RING, 128, 128};
+  }
+  if (fwd && M <= kSkinnyMaxRows * E) return {EXPERT_SKINNY, TILE_128x128, 128, 128};
+  if (M < 256 * E) return {EXPERT_TILES, TILE_128x128, 128, 128};
+  return {EXPERT_TILES, TILE_256x256_W8, 256, 256};
+}
 
 // The backward's launches.
 struct LinearBwd {
@@ -140,8 +158,9 @@ LinearBwd plan_linear_bwd(const linear_desc* d, bool dx, bool dw) {
   LinearBwd b{};
   const DType io = dtype_of(d->dtype);
   const int64_t P = is_gated(d->act) ? 2 * d->N : d->N;
-  b.dx = plan_rows(io, d->M, d->K, P);
-  b.dw = plan_gemm(io, P, d->K, d->M, true, false);
+  if (io == DT_F32) b.dx.main = plan_linear_gemm(io, d->M, d->K, P, true, false);
+  else b.dx = plan_rows(io, d->M, d->K, P);
+  b.dw = plan_linear_gemm(io, P, d->K, d->M, true, false);
   if (!dx || !dw || io == DT_F32) return b;
   b.gdx = plan_gemm(io, d->M, d->K, P, false, false, TILE_256x256_W8);
   b.gdw = plan_gemm(io, P, d->K, d->M, false, false, TILE_256x256_W8);
@@ -364,7 +383,7 @@ mlp_status linear_fwd(const linear_desc* d, const void* x, const void* w, const 
   a.ld_res = N;
 
   if (d->experts) {
-    const ExpertPlan p = plan_experts(io, M, d->experts, true);
+    const ExpertPlan p = plan_experts(d, true);
     a.N = (int)N;
     a.K = a.k_per_split = (int)K;
     ExpertGemm e = expert_gemm(d, a, offsets);
@@ -451,7 +470,7 @@ mlp_status linear_bwd(const linear_desc* d, const void* dy, const void* x, const
   gw.accumulate = grad_accum;
 
   if (d->experts || M == 0) {   // (one weight without rows: as one expert without rows)
-    const ExpertPlan p = plan_experts(io, M, E, false);
+    const ExpertPlan p = plan_experts(d, false);
     ExpertBwd b{};
     gx.N = (int)K;
     gx.K = gx.k_per_split = (int)P;
@@ -498,7 +517,7 @@ hipError_t run_gemm_linear(DType in, int epi, TileShape tile, const GemmArgs& a,
   switch (in) {
     case DT_BF16: return run_gemm_bf16_linear(epi, tile, a, grid, s);
     case DT_F16: return run_gemm_f16_linear(epi, tile, a, grid, s);
-    case DT_F32: return run_gemm_f32_linear(epi, a, grid, s);
+    case DT_F32: return run_gemm_f32_ring(NT, epi, tile, a, grid, s);
     default: return hipErrorInvalidValue;
   }
 }
@@ -507,7 +526,7 @@ hipError_t run_expert_fwd(DType in, int epi, TileShape tile, const ExpertGemm& a
   switch (in) {
     case DT_BF16: return run_expert_fwd_bf16(epi, tile, a, s);
     case DT_F16: return run_expert_fwd_f16(epi, tile, a, s);
-    case DT_F32: return run_expert_fwd_f32(epi, a, s);
+    case DT_F32: return run_expert_fwd_f32(epi, tile, a, s);
     default: return hipErrorInvalidValue;
   }
 }
@@ -516,7 +535,7 @@ hipError_t run_expert_bwd(DType in, TileShape tile, const ExpertBwd& a, hipStrea
   switch (in) {
     case DT_BF16: return run_expert_bwd_bf16(tile, a, s);
     case DT_F16: return run_expert_bwd_f16(tile, a, s);
-    case DT_F32: return run_expert_bwd_f32(a, s);
+    case DT_F32: return run_expert_bwd_f32(tile, a, s);
     default: return hipErrorInvalidValue;
   }
 }

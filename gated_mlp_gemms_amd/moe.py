@@ -45,7 +45,7 @@ def _bad(t, name, dtype, shape):
 
 def _stream(dev, stream):
     if stream is None:
-        return torch.cuda.current_stream(dev).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(dev)   # current_stream(dev) without making a Stream: 1 us less
     return stream if isinstance(stream, int) else stream.cuda_stream
 
 
