@@ -226,12 +226,12 @@ __device__ __forceinline__ void epi_row16(const GemmArgs& p, int m, int n, const
 template <int WAVES> constexpr int epilogue_rows_per_round() { return WAVES == 8 ? 16 : 32; }
 
 // Bytes of LDS the row-staged epilogue uses (waves x rows per round x padded WN fp32 columns).
-template <int BN, int WAVES>
-constexpr int epilogue_lds_bytes() { return WAVES * epilogue_rows_per_round<WAVES>() * ((BN / 2) * 4 + 16); }
+template <int BN, int WAVES, int WGN = 2>
+constexpr int epilogue_lds_bytes() { return WAVES * epilogue_rows_per_round<WAVES>() * ((BN / WGN) * 4 + 16); }
 
 // acc[i][j]: the MFMA layout of the wave's WM x WN tile (see epilogue()). lds: this
 // workgroup's LDS, at least epilogue_lds_bytes<BN>() bytes, not in use by any wave.
-template <int EPI, typename IoT, int BM, int BN, int MI, int NI, int WAVES, typename AccV>
+template <int EPI, typename IoT, int BM, int BN, int MI, int NI, int WAVES, int WGN, typename AccV>
 __device__ __forceinline__ void epilogue_rows(const GemmArgs& p, AccV (&acc)[MI][NI], int m0, int n0,
                                               int split, int wm, int wn, int lane, int wave, char* lds) {
   constexpr bool GATED = epi_gated(EPI);
@@ -239,7 +239,7 @@ __device__ __forceinline__ void epilogue_rows(const GemmArgs& p, AccV (&acc)[MI]
   // (4 values per lane: row l%16, columns 4(l/16) + r)
   constexpr bool B16 = sizeof(AccV) == 4 * sizeof(float);
   constexpr int BLK = B16 ? 16 : 32;
-  constexpr int WM = BM / (WAVES / 2), WN = BN / 2;
+  constexpr int WM = BM / (WAVES / WGN), WN = BN / WGN;
   constexpr int RR = epilogue_rows_per_round<WAVES>();   // rows staged per round
   constexpr int STRIDE = WN * 4 + 16;                 // padded: rows 16 bytes apart in bank space
   constexpr int UNITS = GATED ? WN / 2 : WN;          // output columns of the wave

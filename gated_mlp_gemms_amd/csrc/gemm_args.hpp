@@ -65,6 +65,7 @@ struct ExpertGemm {
   int experts, rows;
   int64_t w_stride, bias_stride;
   int grid;   // workgroups: an upper bound of the tiles for a product over rows
+  int split_tail;   // products over rows in 256-row tiles: a last round of at most half the CUs runs as halves
 };
 // The backward's two products, in one launch: workgroups [0, dx.grid) and the dw.grid after them.
 struct ExpertBwd { ExpertGemm dx, dw; };

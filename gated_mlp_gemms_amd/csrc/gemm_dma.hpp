@@ -538,7 +538,9 @@ constexpr int dma_ring_bytes() {
 // 64 x 128, 128 accumulator registers, half the register file each).
 // SKIP: a wave whose rows all lie past the matrix takes part in the K-steps' DMAs and barriers only,
 // so a tile of few rows costs its SIMDs the MFMAs of the waves that have rows.
-template <typename T, typename IoT, int BM, int BN, bool A_KMAJ, bool B_KMAJ, int EPI, int WAVES, bool SKIP = false>
+// WGN: wave columns (2; 4 for the experts' 128 x 256 tiles).
+template <typename T, typename IoT, int BM, int BN, bool A_KMAJ, bool B_KMAJ, int EPI, int WAVES, bool SKIP = false,
+          int WGN = 2>
 __device__ __forceinline__ void gemm_dma_tile(const GemmArgs p, int item, char* smem) {
   static_assert(BM % 64 == 0 && BN % 64 == 0, "tile must split into 2x2 waves of 32x32 blocks");
   static_assert(ElemTraits<T>::bytes != 4 || WAVES == 4, "fp32 tiles have one wave per SIMD");
@@ -548,8 +550,8 @@ __device__ __forceinline__ void gemm_dma_tile(const GemmArgs p, int item, char* 
   constexpr int ROWB = StepGeo<T>::ROWB;
   constexpr int BK = ROWB / ES;
   static_assert(WAVES == 4 || WAVES == 8, "4 or 8 waves");
-  constexpr int WGM = WAVES / 2;                     // wave rows; two wave columns
-  constexpr int WM = BM / WGM, WN = BN / 2;
+  constexpr int WGM = WAVES / WGN;                   // wave rows
+  constexpr int WM = BM / WGM, WN = BN / WGN;
   // two waves per SIMD (16-bit types): 16x16x32 MFMA blocks; otherwise 32x32 blocks
   constexpr bool M16 = WAVES == 8 && ES == 2;
   constexpr int BLK = M16 ? 16 : 32;
@@ -578,7 +580,7 @@ __device__ __forceinline__ void gemm_dma_tile(const GemmArgs p, int item, char* 
   auto b_stage = [&](int st) -> char* { return XA ? smem + NSA * A_BYTES + st * B_BYTES : smem + st * STAGE + A_BYTES; };
 
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave >> 1, wn = wave & 1;
+  const int wm = wave / WGN, wn = wave % WGN;
 
   int lid = item;
   const int tiles = p.tiles_m * p.tiles_n;
@@ -926,14 +928,14 @@ __device__ __forceinline__ void gemm_dma_tile(const GemmArgs p, int item, char* 
   for (; kt < nk; ++kt) k_step(kt, slow_t{});
   // the trailing zero-fill DMAs have landed and no wave reads the ring any more: its LDS
   // becomes the epilogue's staging area
-  static_assert(epilogue_lds_bytes<BN, WAVES>() <= NS * STAGE, "epilogue staging must fit the ring");
+  static_assert(epilogue_lds_bytes<BN, WAVES, WGN>() <= NS * STAGE, "epilogue staging must fit the ring");
   if constexpr (DW < WAVES) __builtin_amdgcn_s_setprio(0);   // the last issue raised it
   wait_vmcnt<0>();
   wait_lgkmcnt0();
   __builtin_amdgcn_s_barrier();
   // fp32 widths are multiples of 4 only: straight from the accumulators, 4 columns at a time
   if constexpr (ES == 4) epilogue<EPI, IoT, BM, BN, MI, NI>(p, acc, m0, n0, split, wm, wn, lane);
-  else epilogue_rows<EPI, IoT, BM, BN, MI, NI, WAVES>(p, acc, m0, n0, split, wm, wn, lane, wave, smem);
+  else epilogue_rows<EPI, IoT, BM, BN, MI, NI, WAVES, WGN>(p, acc, m0, n0, split, wm, wn, lane, wave, smem);
 }
 
 // One GEMM: a workgroup per tile, placed XCD-aware (xcd_remap).

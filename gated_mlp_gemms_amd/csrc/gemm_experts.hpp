@@ -81,23 +81,44 @@ template <typename T> __device__ __forceinline__ void* shift(void* p, int64_t el
   return p ? reinterpret_cast<char*>(p) + elems * ElemTraits<T>::bytes : nullptr;
 }
 
-// Tile b of a product over rows: y = x W_e^T with a linear epilogue, or dx = dz W_e.
+template <typename T, int BM, int BN, int WAVES>
+constexpr int expert_lds_bytes() {
+  constexpr int whole = dma_ring_bytes<T, BM, BN>();
+  if constexpr (WAVES == 8) return whole > dma_ring_bytes<T, BM / 2, BN>() ? whole : dma_ring_bytes<T, BM / 2, BN>();
+  else return whole;
+}
+
+// Tile b of a product over rows: y = x W_e^T with a linear epilogue, or dx = dz W_e. 8-wave tiles are 256
+// rows, or 128 where an expert has no more left. With split_tail the tiles of a last, at most half
+// filled round of the 256 CUs run as two 128-row halves each: 32768 rows of 32 uneven experts are 6.3 rounds
+// of full tiles, which without the halves take the time of 7.
 template <typename T, int BM, int BN, bool BK, int EPI, int WAVES>
 __device__ __forceinline__ void expert_rows_tile(const ExpertGemm& a, int b, char* smem) {
   constexpr int BNC = epi_gated(EPI) ? BN / 2 : BN;   // output columns of a tile
+  constexpr bool HALVES = WAVES == 8;
+  constexpr int HM = BM / 2;
   const int tiles_n = a.g.tiles_n;
-  int tile = 0;
+  int tile = 0, half = -1;
   RowPiece t;
   // XCD-contiguous over the tiles there are, not over the launch's upper bound
   const bool found = find_row_piece(a.offsets, a.experts, a.rows, BM, [&](int total) {
     const int tiles = (int)min((int64_t)total * tiles_n, (int64_t)a.grid);
-    if (b >= tiles) return -1;
-    tile = xcd_remap(b, tiles);
+    const int rem = tiles % 256, tail = HALVES && a.split_tail && rem <= 128 && tiles > 256 ? rem : 0;
+    const int whole = tiles - tail;
+    if (b < whole) {
+      tile = xcd_remap(b, whole);
+    } else {
+      if (b - whole >= 2 * tail) return -1;
+      const int i = xcd_remap(b - whole, 2 * tail);
+      tile = whole + i / 2;
+      half = i & 1;
+    }
     return tile / tiles_n;
   }, t);
   if (!found) return;
   GemmArgs p = a.g;
   if (t.e == a.experts) {   // rows of no expert: zeros (plus the residual)
+    if (half > 0) return;   // (the first half fills the whole tile)
     const int m0 = t.row0 + t.index * BM, m1 = min(m0 + BM, a.rows);
     const int n0 = (tile % tiles_n) * BNC, n1 = min(n0 + BNC, p.N);
     constexpr int V = 16 / ElemTraits<T>::bytes, W = BNC / V;
@@ -114,17 +135,30 @@ __device__ __forceinline__ void expert_rows_tile(const ExpertGemm& a, int b, cha
     }
     return;
   }
-  p.M = t.rows;
-  p.tiles_m = (t.rows + BM - 1) / BM;
-  p.A = shift<T>(p.A, t.row0 * p.lda);
-  p.C0 = shift<T>(p.C0, t.row0 * p.ldc0);
-  p.aux = shift<T>(p.aux, t.row0 * p.ld_aux);
-  p.res = shift<T>(p.res, t.row0 * p.ld_res);
+  // this tile's rows as a product of its own
+  int tm, tn;
+  grouped_tile(tile - t.first * tiles_n, (t.rows + BM - 1) / BM, tiles_n, p.group_m, tm, tn);
+  const int skip = tm * BM + (half > 0 ? HM : 0);
+  const int rows = min(t.rows - skip, half >= 0 ? HM : BM);
+  if (rows <= 0) return;   // the second half of a tile of few rows
+  const int64_t row0 = t.row0 + skip;
+  p.M = rows;
+  p.tiles_m = 1;
+  p.A = shift<T>(p.A, row0 * p.lda);
+  p.C0 = shift<T>(p.C0, row0 * p.ldc0);
+  p.aux = shift<T>(p.aux, row0 * p.ld_aux);
+  p.res = shift<T>(p.res, row0 * p.ld_res);
   p.B0 = shift<T>(p.B0, t.e * a.w_stride);
   p.B1 = shift<T>(p.B1, t.e * a.w_stride);
   p.bias0 = shift<T>(p.bias0, t.e * a.bias_stride);
   p.bias1 = shift<T>(p.bias1, t.e * a.bias_stride);
-  gemm_dma_tile<T, T, BM, BN, true, BK, EPI, WAVES, true>(p, tile - t.first * tiles_n, smem);
+  if constexpr (HALVES) {
+    if (rows <= HM) {
+      gemm_dma_tile<T, T, HM, BN, true, BK, EPI, WAVES, true, 4>(p, tn, smem);
+      return;
+    }
+  }
+  gemm_dma_tile<T, T, BM, BN, true, BK, EPI, WAVES, true>(p, tn, smem);
 }
 
 // Tile `item` of the weight gradients dW_e = dz^T x over expert e's rows.
@@ -148,13 +182,13 @@ __device__ __forceinline__ void expert_grad_tile(const ExpertGemm& a, int item, 
 
 template <typename T, int BM, int BN, int EPI, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 1) void expert_fwd_kernel(const ExpertGemm a) {
-  __shared__ __attribute__((aligned(1024))) char smem[dma_ring_bytes<T, BM, BN>()];
+  __shared__ __attribute__((aligned(1024))) char smem[expert_lds_bytes<T, BM, BN, WAVES>()];
   expert_rows_tile<T, BM, BN, true, EPI, WAVES>(a, blockIdx.x, smem);
 }
 
 template <typename T, typename GT, int BM, int BN, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 1) void expert_bwd_kernel(const ExpertBwd a) {
-  __shared__ __attribute__((aligned(1024))) char smem[dma_ring_bytes<T, BM, BN>()];
+  __shared__ __attribute__((aligned(1024))) char smem[expert_lds_bytes<T, BM, BN, WAVES>()];
   const int b = blockIdx.x;
   if (b < a.dx.grid) expert_rows_tile<T, BM, BN, false, EPI_STORE, WAVES>(a.dx, b, smem);
   else expert_grad_tile<T, GT, BM, BN, WAVES>(a.dw, xcd_remap(b - a.dx.grid, a.dw.grid), smem);

@@ -392,6 +392,10 @@ mlp_status linear_fwd(const linear_desc* d, const void* x, const void* w, const 
     e.g.tiles_n = (int)((N + bn - 1) / bn);
     e.g.group_m = 8;
     e.grid = (int)(row_tiles(M, d->experts, p.bm) * e.g.tiles_n);
+    if (p.tile == TILE_256x256_W8) {
+      e.split_tail = 1;
+      e.grid += 128;   // the tail's second halves
+    }
     return hip_status(run_expert_fwd(io, epi, p.tile, e, s), "experts' products");
   }
   const LinearFwd f = plan_linear(d);
