@@ -78,6 +78,10 @@ hipError_t run_expert_bwd_bf16(TileShape tile, const ExpertBwd& a, hipStream_t s
 hipError_t run_expert_bwd_f16(TileShape tile, const ExpertBwd& a, hipStream_t s);
 hipError_t run_expert_bwd_f32(TileShape tile, const ExpertBwd& a, hipStream_t s);
 // The forward with a few rows an expert, 16-bit (g.N output columns, any rows; grid is unused).
+// Taken up to kExpertFewRows rows an expert on average. 64 experts, 2048 x 1376 gate and up, uneven rows,
+// against 128 x 128 tiles: 96 rows 78 and 96 us, 300 rows 134 and 153, 600 rows 161 and 154, 1000 rows 207 and 158
+// (an expert's weights are streamed again for every 16 of its rows).
+constexpr int kExpertFewRows = 8;
 hipError_t run_skinny_experts(DType in, int epi, const ExpertGemm& a, hipStream_t s);
 
 // dz = dy f'(z) (gated: [dy u f'(g) | dy f(g)]) into dz [rows, P] (NULL: not stored; fn FN_NONE: dz is

@@ -142,7 +142,7 @@ ExpertPlan plan_experts(const linear_desc* d, bool fwd) {
     if (row_tiles(M, E, 128) * tn < 512) return {EXPERT_TILES, TILE_64x64_RING, 64, fwd && gated ? 128 : 64};
     return {EXPERT_TILES, TILE_128x128_RING, 128, 128};
   }
-  if (fwd && M <= kSkinnyMaxRows * E) return {EXPERT_SKINNY, TILE_128x128, 128, 128};
+  if (fwd && M <= kExpertFewRows * E) return {EXPERT_SKINNY, TILE_128x128, 128, 128};
   if (M < 256 * E) return {EXPERT_TILES, TILE_128x128, 128, 128};
   return {EXPERT_TILES, TILE_256x256_W8, 256, 256};
 }

@@ -498,11 +498,11 @@ __global__ __launch_bounds__(64 * WAVES) void skinny_experts_kernel(const Expert
 template <typename T, int EPI>
 hipError_t launch_skinny_experts(const ExpertGemm& a, hipStream_t s) {
   const int64_t blocks = (int64_t)(a.experts + 1) * ((a.g.N + 15) / 16);
-  if (blocks >= 512) {
-    hipLaunchKernelGGL((skinny_experts_kernel<T, EPI, 4, 3>), dim3((unsigned)blocks), dim3(256), 0, s, a);
-  } else {   // few workgroups: K over more waves, so enough loads are in flight
-    hipLaunchKernelGGL((skinny_experts_kernel<T, EPI, 8, 3>), dim3((unsigned)blocks), dim3(512), 0, s, a);
-  }
+  // Four waves, two buffers of loads: with three the gated body takes all registers, one wave a SIMD (96
+  // rows, 36 of 64 experts live, 2048 x 1376 gate and up: 110 us, against 78 us = 5.2 TB/s of weights);
+  // eight waves a workgroup are slower there (104 us) and no faster with few workgroups (4 rows of 2
+  // experts, 4096 x 512: 9.5 against 9.0 us).
+  hipLaunchKernelGGL((skinny_experts_kernel<T, EPI, 4, 2>), dim3((unsigned)blocks), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 
