@@ -80,7 +80,7 @@ _MOE_SIGNATURES = {
     "moe_gather": (C.c_int, [_P, _P, _P, _I32, _I64, _I64, _I64, _I64, _P, _P]),
     "moe_gather_bwd": (C.c_int, [_P, _P, _P, _I32, _I64, _I64, _I64, _I64, _P, _P]),
     "moe_combine": (C.c_int, [_P, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _I64, _P, _P]),
-    "moe_combine_bwd": (C.c_int, [_P, _P, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _I64, _P, _P, _P]),
+    "moe_combine_bwd": (C.c_int, [_P, _P, _P, _P, _P, _I32, _I64, _I64, _I64, _I64, _P, _P, _P]),
     "linear_workspace_bytes": (C.c_size_t, [C.POINTER(LinearDesc), C.c_int]),
     "linear_fwd": (C.c_int, [C.POINTER(LinearDesc)] + [_P] * 10 + [C.c_size_t, _P]),
     "linear_bwd": (C.c_int, [C.POINTER(LinearDesc)] + [_P] * 11 + [_I32, _P, C.c_size_t, _P]),

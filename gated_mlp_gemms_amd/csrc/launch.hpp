@@ -110,9 +110,9 @@ hipError_t run_moe_gather(const void* x, const int* slot_of, const int* offsets,
                           void* xs, hipStream_t s);
 hipError_t run_moe_combine(DType dt, const void* ys, const float* weights, const int* row_of, const int* offsets,
                            const void* residual, int T, int E, int k, int pieces, void* out, hipStream_t s);
-hipError_t run_moe_combine_bwd(DType dt, const void* dout, const void* ys, const float* weights, const int* row_of,
-                               const int* slot_of, const int* offsets, int n, int E, int k, int pieces, void* dys,
-                               float* dweights, hipStream_t s);
+hipError_t run_moe_combine_bwd(DType dt, const void* dout, const void* ys, const float* weights, const int* slot_of,
+                               const int* offsets, int n, int E, int k, int pieces, void* dys, float* dweights,
+                               hipStream_t s);
 
 // out = alpha * sum_s partial[s] (fixed order), stored as `io` or added into fp32 (accumulate).
 // Rows >= c_split go to C1 (row - c_split).

@@ -445,7 +445,24 @@ template <typename T> struct Piece {   // 16 bytes of a row
   }
 };
 
+// Rows that no cache will hold until they are read again are streamed (NT: non-temporal loads of the
+// rows read once, non-temporal stores): from 100 MB of sorted rows on. Bound by HBM. 49152 rows of 2048 bf16
+// (201 MB): gather 67 -> 55 us (4.2 TB/s), combine 55 -> 45 (5.9), its gradient 93 -> 86 (5.0), gather's 50 -> 41 (5.7);
+// 15009 rows of 1036 fp32 (62 MB): gather's gradient 17 -> 20 us, the others even.
+constexpr int64_t kStreamBytes = 100 << 20;
+inline bool stream_rows(int64_t rows, int pieces) { return rows * pieces * 16 >= kStreamBytes; }
+
+template <bool NT> __device__ __forceinline__ u32x4 load_piece(const u32x4* p) {
+  if constexpr (NT) return __builtin_nontemporal_load(p);
+  else return *p;
+}
+template <bool NT> __device__ __forceinline__ void store_piece(u32x4* p, u32x4 v) {
+  if constexpr (NT) __builtin_nontemporal_store(v, p);
+  else *p = v;
+}
+
 // xs[r] = x[slot_of[r] / k]: a row is moved as it is, in 16-byte pieces.
+template <bool NT>
 __global__ __launch_bounds__(kRowThreads) void gather_kernel(const u32x4* __restrict__ x,
                                                              const int* __restrict__ slot_of,
                                                              const int* __restrict__ offsets, int n, int E, int k,
@@ -456,19 +473,20 @@ __global__ __launch_bounds__(kRowThreads) void gather_kernel(const u32x4* __rest
   const bool kept = r < offsets[E] && (uint32_t)slot < (uint32_t)n;
   const u32x4* src = x + (int64_t)(kept ? slot / k : 0) * pieces;
   u32x4* dst = xs + (int64_t)r * pieces;
-  for (int c = threadIdx.x & ((1 << sh) - 1); c < pieces; c += 1 << sh) dst[c] = kept ? src[c] : u32x4{0u, 0u, 0u, 0u};
+  for (int c = threadIdx.x & ((1 << sh) - 1); c < pieces; c += 1 << sh) store_piece<NT>(dst + c, kept ? src[c] : u32x4{0u, 0u, 0u, 0u});
 }
 
 // out[t] = residual[t] + sum_j weights[t][j] ys[row_of[t k + j]] over the kept rows (weights NULL: 1,
-// residual NULL: 0). The k rows of a piece are loaded J at a time before they are summed in order.
-template <typename T>
+// residual NULL: 0). The k rows of a piece are loaded J at a time before they are
+// summed in order.
+template <typename T, int J, bool NT>
 __global__ __launch_bounds__(kRowThreads) void combine_kernel(const u32x4* __restrict__ ys,
                                                               const float* __restrict__ weights,
                                                               const int* __restrict__ row_of,
                                                               const int* __restrict__ offsets, const u32x4* residual,
                                                               int tokens, int E, int k, int pieces, int sh,
                                                               u32x4* out) {
-  constexpr int N = Piece<T>::N, J = 4;
+  constexpr int N = Piece<T>::N;
   const int t = blockIdx.x * (kRowThreads >> sh) + (threadIdx.x >> sh);
   if (t >= tokens) return;
   const int kept = min(offsets[E], tokens * k);
@@ -486,7 +504,7 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(const u32x4* __res
         const int row = j0 + j < k ? row_of[slot] : -1;
         ok[j] = row >= 0 && row < kept;
         w[j] = ok[j] && weights != nullptr ? weights[slot] : 1.0f;
-        v[j] = ok[j] ? ys[(int64_t)row * pieces + c] : u32x4{0u, 0u, 0u, 0u};
+        v[j] = ok[j] ? load_piece<NT>(ys + (int64_t)row * pieces + c) : u32x4{0u, 0u, 0u, 0u};
       }
 #pragma unroll
       for (int j = 0; j < J; ++j) {
@@ -503,17 +521,16 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(const u32x4* __res
 #pragma unroll
       for (int q = 0; q < N; ++q) acc[q] += f[q];
     }
-    out[(int64_t)t * pieces + c] = Piece<T>::pack(acc);
+    store_piece<NT>(out + (int64_t)t * pieces + c, Piece<T>::pack(acc));
   }
 }
 
 // A wave a row r: with t the row's token, dys[r] = weight dout[t] and the weight's gradient
 // dot(ys[r], dout[t]); zeros for a dropped row.
-template <typename T>
+template <typename T, bool NT>
 __global__ __launch_bounds__(kRowThreads) void combine_bwd_kernel(const u32x4* __restrict__ dout,
                                                                   const u32x4* __restrict__ ys,
                                                                   const float* __restrict__ weights,
-                                                                  const int* __restrict__ row_of,
                                                                   const int* __restrict__ slot_of,
                                                                   const int* __restrict__ offsets, int n, int E, int k,
                                                                   int pieces, u32x4* __restrict__ dys,
@@ -530,16 +547,17 @@ __global__ __launch_bounds__(kRowThreads) void combine_bwd_kernel(const u32x4* _
     const float w = weights[slot];
     const u32x4* g = dout + (int64_t)(slot / k) * pieces;
     const u32x4* y = ys + (int64_t)r * pieces;
+#pragma unroll 4
     for (int c = lane; c < pieces; c += 64) {
       float gv[N], yv[N], o[N];
       Piece<T>::unpack(g[c], gv);
-      Piece<T>::unpack(y[c], yv);
+      Piece<T>::unpack(load_piece<NT>(y + c), yv);
 #pragma unroll
       for (int q = 0; q < N; ++q) {
         dot = __builtin_fmaf(gv[q], yv[q], dot);
         o[q] = w * gv[q];
       }
-      dst[c] = Piece<T>::pack(o);
+      store_piece<NT>(dst + c, Piece<T>::pack(o));
     }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o);
@@ -557,6 +575,10 @@ template <typename F> hipError_t by_type(DType dt, F f) {
     case DT_F16: return f(f16{});
     default: return hipErrorInvalidValue;
   }
+}
+
+template <typename F> hipError_t by_stream(int64_t rows, int pieces, F f) {
+  return stream_rows(rows, pieces) ? f(std::true_type{}) : f(std::false_type{});
 }
 
 }  // namespace
@@ -614,30 +636,42 @@ hipError_t run_moe_sort(const int* ids, int64_t n, int E, int* offsets, int* row
 hipError_t run_moe_gather(const void* x, const int* slot_of, const int* offsets, int n, int E, int k, int pieces,
                           void* xs, hipStream_t s) {
   const int sh = row_shift(pieces);
-  hipLaunchKernelGGL(gather_kernel, dim3((unsigned)row_grid(n, sh)), dim3(kRowThreads), 0, s,
-                     static_cast<const u32x4*>(x), slot_of, offsets, n, E, k, pieces, sh, static_cast<u32x4*>(xs));
-  return hipGetLastError();
+  return by_stream(n, pieces, [&](auto nt) {
+    hipLaunchKernelGGL((gather_kernel<decltype(nt)::value>), dim3((unsigned)row_grid(n, sh)), dim3(kRowThreads), 0, s,
+                       static_cast<const u32x4*>(x), slot_of, offsets, n, E, k, pieces, sh, static_cast<u32x4*>(xs));
+    return hipGetLastError();
+  });
 }
 
 hipError_t run_moe_combine(DType dt, const void* ys, const float* weights, const int* row_of, const int* offsets,
                            const void* residual, int T, int E, int k, int pieces, void* out, hipStream_t s) {
   const int sh = row_shift(pieces);
   return by_type(dt, [&](auto v) {
-    hipLaunchKernelGGL((combine_kernel<decltype(v)>), dim3((unsigned)row_grid(T, sh)), dim3(kRowThreads), 0, s,
-                       static_cast<const u32x4*>(ys), weights, row_of, offsets, static_cast<const u32x4*>(residual), T,
-                       E, k, pieces, sh, static_cast<u32x4*>(out));
-    return hipGetLastError();
+    auto launch = [&](auto j) {   // J: rows of a token in flight at once
+      return by_stream((int64_t)T * k, pieces, [&](auto nt) {
+        hipLaunchKernelGGL((combine_kernel<decltype(v), decltype(j)::value, decltype(nt)::value>),
+                           dim3((unsigned)row_grid(T, sh)), dim3(kRowThreads), 0, s, static_cast<const u32x4*>(ys),
+                           weights, row_of, offsets, static_cast<const u32x4*>(residual), T, E, k, pieces, sh,
+                           static_cast<u32x4*>(out));
+        return hipGetLastError();
+      });
+    };
+    using std::integral_constant;
+    if (k <= 2) return launch(integral_constant<int, 2>{});
+    return k <= 4 ? launch(integral_constant<int, 4>{}) : launch(integral_constant<int, 8>{});
   });
 }
 
-hipError_t run_moe_combine_bwd(DType dt, const void* dout, const void* ys, const float* weights, const int* row_of,
-                               const int* slot_of, const int* offsets, int n, int E, int k, int pieces, void* dys,
-                               float* dweights, hipStream_t s) {
+hipError_t run_moe_combine_bwd(DType dt, const void* dout, const void* ys, const float* weights, const int* slot_of,
+                               const int* offsets, int n, int E, int k, int pieces, void* dys, float* dweights,
+                               hipStream_t s) {
   return by_type(dt, [&](auto v) {
-    hipLaunchKernelGGL((combine_bwd_kernel<decltype(v)>), dim3((unsigned)((n + 3) / 4)), dim3(kRowThreads), 0, s,
-                       static_cast<const u32x4*>(dout), static_cast<const u32x4*>(ys), weights, row_of, slot_of,
-                       offsets, n, E, k, pieces, static_cast<u32x4*>(dys), dweights);
-    return hipGetLastError();
+    return by_stream(n, pieces, [&](auto nt) {
+      hipLaunchKernelGGL((combine_bwd_kernel<decltype(v), decltype(nt)::value>), dim3((unsigned)((n + 3) / 4)),
+                         dim3(kRowThreads), 0, s, static_cast<const u32x4*>(dout), static_cast<const u32x4*>(ys),
+                         weights, slot_of, offsets, n, E, k, pieces, static_cast<u32x4*>(dys), dweights);
+      return hipGetLastError();
+    });
   });
 }
 

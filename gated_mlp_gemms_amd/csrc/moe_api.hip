@@ -318,20 +318,19 @@ mlp_status moe_combine(const void* ys, const float* weights, const int32_t* row_
                                     pieces_of(dtype, d), out, stream_of(stream)), "moe_combine");
 }
 
-mlp_status moe_combine_bwd(const void* dout, const void* ys, const float* weights, const int32_t* row_of,
-                           const int32_t* slot_of, const int32_t* offsets, int dtype, int64_t T, int64_t E, int64_t k,
-                           int64_t d, void* dys, float* dweights, void* stream) {
+mlp_status moe_combine_bwd(const void* dout, const void* ys, const float* weights, const int32_t* slot_of,
+                           const int32_t* offsets, int dtype, int64_t T, int64_t E, int64_t k, int64_t d, void* dys,
+                           float* dweights, void* stream) {
   MLP_TRY(check_rows(dtype, T, E, k, d));
   MLP_TRY(need_buf(dout, T, "dout"));
   MLP_TRY(need_buf(ys, T, "ys"));
   MLP_TRY(need_buf(weights, T, "weights", false));
-  MLP_TRY(need_buf(row_of, T, "row_of", false));
   MLP_TRY(need_buf(slot_of, T, "slot_of", false));
   MLP_TRY(need_ptr(offsets, "offsets", false));
   MLP_TRY(need_buf(dys, T, "dys"));
   MLP_TRY(need_buf(dweights, T, "dweights", false));
   if (T == 0) return MLP_OK;
-  return hip_status(run_moe_combine_bwd(dtype_of(dtype), dout, ys, weights, row_of, slot_of, offsets, (int)(T * k),
+  return hip_status(run_moe_combine_bwd(dtype_of(dtype), dout, ys, weights, slot_of, offsets, (int)(T * k),
                                         (int)E, (int)k, pieces_of(dtype, d), dys, dweights, stream_of(stream)),
                     "moe_combine_bwd");
 }

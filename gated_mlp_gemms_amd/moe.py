@@ -204,13 +204,15 @@ def moe_combine(ys, weights, row_of, offsets, out, residual=None, stream=None):
 
 def moe_combine_bwd(dout, ys, weights, row_of, slot_of, offsets, dys, dweights, stream=None):
     """Both gradients of :func:`moe_combine` against ``dout`` [T, d]: ``dys`` [T k, d] (zeros in the
-    dropped rows) and ``dweights`` [T, k] (fp32, 0 for a dropped slot). The residual's is ``dout``."""
+    dropped rows) and ``dweights`` [T, k] (fp32, 0 for a dropped slot). The residual's is ``dout``.
+    It goes by rows and reads ``slot_of``; ``row_of``, its inverse, is only checked."""
     a = _Args()
     dt, code, T, E, k, d = _rows(dout, "dout", ys, "ys", offsets, a)
     n = T * k
+    a(row_of, "row_of", _I32, (n,))
     p = (a(dout, "dout", dt, (T, d)), a(ys, "ys", dt, (n, d)), a(weights, "weights", _F32, (T, k)),
-         a(row_of, "row_of", _I32, (n,)), a(slot_of, "slot_of", _I32, (n,)), a(offsets, "offsets", _I32, (E + 1,)), code,
-         T, E, k, d, a(dys, "dys", dt, (n, d)), a(dweights, "dweights", _F32, (T, k)))
+         a(slot_of, "slot_of", _I32, (n,)), a(offsets, "offsets", _I32, (E + 1,)), code, T, E, k, d,
+         a(dys, "dys", dt, (n, d)), a(dweights, "dweights", _F32, (T, k)))
     check(lib().moe_combine_bwd(*p, a.stream(stream)), "moe_combine_bwd")
     return dys, dweights
 

@@ -85,13 +85,13 @@ mlp_status moe_combine(const void* ys, const float* weights, const int32_t* row_
                        const void* residual, int dtype, int64_t T, int64_t E, int64_t k, int64_t d, void* out,
                        void* stream);
 /*
- * With t = slot_of[r] / k: dys[r] = weights[slot_of[r]] dout[t] for kept rows, zeros behind them;
- * dweights [T, k] (fp32) = dot(ys[row_of[t k + j]], dout[t]), 0 for a dropped slot. (The
- * residual's gradient is dout itself.)
+ * Row by row, with s = slot_of[r] and t = s / k: for kept rows dys[r] = weights[s] dout[t] and
+ * dweights[s] = dot(ys[r], dout[t]) (fp32 [T, k]); behind them zeros and 0. (The residual's
+ * gradient is dout itself.)
  */
-mlp_status moe_combine_bwd(const void* dout, const void* ys, const float* weights, const int32_t* row_of,
-                           const int32_t* slot_of, const int32_t* offsets, int dtype, int64_t T, int64_t E, int64_t k,
-                           int64_t d, void* dys, float* dweights, void* stream);
+mlp_status moe_combine_bwd(const void* dout, const void* ys, const float* weights, const int32_t* slot_of,
+                           const int32_t* offsets, int dtype, int64_t T, int64_t E, int64_t k, int64_t d, void* dys,
+                           float* dweights, void* stream);
 
 /* linear_desc.act: an mlp_act, or LINEAR_ACT_NONE (y = x W^T + b). */
 #define LINEAR_ACT_NONE (-1)

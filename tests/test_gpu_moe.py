@@ -552,3 +552,41 @@ def test_layer_on_another_stream_and_twice():
     side.synchronize()
     for n, t in L.outputs().items():
         assert torch.equal(first[n], t), n
+
+
+@pytest.mark.parametrize("dtype", list(R.DT))
+def test_streamed_rows_equal_cached_ones(dtype):
+    """From 100 MB of sorted rows on they are streamed: the same values as of the same rows in parts."""
+    g, dt = gen(21), R.DT[dtype]
+    d = 2048 if dt == torch.float32 else 4096
+    T, E, k = 4500, 20, 3
+    assert T * k * d * torch.empty(0, dtype=dt).element_size() >= 100 << 20
+    n, h = T * k, T // 2
+    ids = torch.rand(T, E, device=DEV, generator=g).topk(k, dim=1)[1].to(torch.int32)
+    ids[torch.rand(T, k, device=DEV, generator=g) < 0.1] = -1
+    off, row, slot = (poison(m, dtype=torch.int32) for m in (E + 1, n, n))
+    gm.moe_sort(ids, E, off, row, slot)
+    kept = int(off[E])
+    x, ys, w = normal(g, T, d, dtype=dt), normal(g, n, d, dtype=dt), torch.rand(T, k, device=DEV, generator=g)
+    xs, out, dx, dys, dw = (poison(*s, dtype=t) for s, t in (((n, d), dt), ((T, d), dt), ((T, d), dt), ((n, d), dt),
+                                                            ((T, k), torch.float32)))
+    gm.moe_gather(x, slot, off, xs)
+    assert torch.equal(xs[:kept], x[slot[:kept].long() // k]) and not xs[kept:].any()
+    gm.moe_combine(ys, w, row, off, out, residual=x)
+    gm.moe_gather_bwd(ys, row, off, dx)
+    gm.moe_combine_bwd(x, ys, w, row, slot, off, dys, dw)
+    # halves of the tokens, each a smaller problem of its own: every slot of the first expert, in token order
+    for a, b in ((0, h), (h, T)):
+        m = (b - a) * k
+        live = ids[a:b].reshape(-1) >= 0
+        part = torch.where(live, 0, -1).to(torch.int32)
+        o1, r1, s1 = (poison(c, dtype=torch.int32) for c in (k + 1, m, m))
+        gm.moe_sort(part, k, o1, r1, s1)
+        ys1 = ys[row[a * k:b * k].long()][s1.long()].contiguous()
+        out1, dx1, dys1, dw1 = (poison(*s, dtype=t) for s, t in (((b - a, d), dt), ((b - a, d), dt), ((m, d), dt),
+                                                                 ((b - a, k), torch.float32)))
+        gm.moe_combine(ys1, w[a:b].contiguous(), r1, o1, out1, residual=x[a:b].contiguous())
+        gm.moe_gather_bwd(ys1, r1, o1, dx1)
+        gm.moe_combine_bwd(x[a:b].contiguous(), ys1, w[a:b].contiguous(), r1, s1, o1, dys1, dw1)
+        assert torch.equal(out[a:b], out1) and torch.equal(dx[a:b], dx1) and torch.equal(dw[a:b], dw1)
+        assert torch.equal(dys[row[a * k:b * k].long()][s1.long()], dys1)

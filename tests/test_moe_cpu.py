@@ -100,12 +100,12 @@ def test_row_checks():
         v = {**dims, **kw}
         return L.moe_combine(ys, w, row, off, res, *v.values(), out, None)
 
-    def combine_bwd(dout=FAKE, ys=FAKE, w=FAKE, row=FAKE, slot=FAKE, off=FAKE, dys=FAKE, dw=FAKE, **kw):
+    def combine_bwd(dout=FAKE, ys=FAKE, w=FAKE, slot=FAKE, off=FAKE, dys=FAKE, dw=FAKE, **kw):
         v = {**dims, **kw}
-        return L.moe_combine_bwd(dout, ys, w, row, slot, off, *v.values(), dys, dw, None)
+        return L.moe_combine_bwd(dout, ys, w, slot, off, *v.values(), dys, dw, None)
 
     for call, names in ((gather, "x slot off xs"), (gather_bwd, "dxs row off dx"), (combine, "ys w row off out"),
-                        (combine_bwd, "dout ys w row slot off dys dw")):
+                        (combine_bwd, "dout ys w slot off dys dw")):
         assert call(dtype=9) == MLP_ERR_INVALID_ARG
         assert call(d=0) == MLP_ERR_INVALID_ARG
         assert call(d=68) == MLP_ERR_ALIGNMENT and "multiple of 8" in err()
