@@ -85,10 +85,16 @@ constexpr int kExpertFewRows = 8;
 hipError_t run_skinny_experts(DType in, int epi, const ExpertGemm& a, hipStream_t s);
 
 // dz = dy f'(z) (gated: [dy u f'(g) | dy f(g)]) into dz [rows, P] (NULL: not stored; fn FN_NONE: dz is
-// dy), and its column sums over pieces of at most kDactRows rows of one expert, fp32, into
-// sums [pieces][P] (NULL: not formed); P = 2N gated, else N.
-constexpr int kDactRows = 64;
-inline int64_t dact_pieces(int64_t rows, int64_t experts) { return rows / kDactRows + (rows < experts ? rows : experts) + 1; }
+// dy), and its column sums over pieces of at most dact_rows() rows of one expert, fp32, into
+// sums [pieces][P] (NULL: not formed); P = 2N gated, else N. Pieces are 64 rows (8 rows a thread); where those
+// would leave CUs idle, 16: a few rows after another are latency (1003 rows of 516 fp32: 8.2 -> 5.4 us).
+constexpr int kDactRowsFew = 16, kDactRows = 64, kDactCols = 256;
+inline int dact_rows(int64_t rows, int64_t N) {
+  return rows / kDactRows * ((N + kDactCols - 1) / kDactCols) < 512 ? kDactRowsFew : kDactRows;
+}
+inline int64_t dact_pieces(int64_t rows, int64_t N, int64_t experts) {
+  return rows / dact_rows(rows, N) + (rows < experts ? rows : experts) + 1;
+}
 hipError_t run_linear_dact(DType io, int gated, int fn, const void* dy, const void* preact, const int* offsets,
                            int experts, int64_t rows, int64_t N, void* dz, float* sums, hipStream_t s);
 // The pieces' sums joined in order: db0 (gated: the first N columns; db1 the others) [experts, N], in

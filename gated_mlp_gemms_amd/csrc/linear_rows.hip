@@ -53,23 +53,21 @@ __global__ __launch_bounds__(kThr) void linear_reduce_kernel(const float* __rest
 }
 
 // dz and its column sums over one piece of rows: 32 lanes x 8 columns across, 8 rows down.
-constexpr int kDactCols = 256;
-
 template <typename T, bool GATED>
 __global__ __launch_bounds__(kThr) void linear_dact_kernel(int fn, const void* __restrict__ dy,
                                                            const void* __restrict__ preact,
                                                            const int* __restrict__ offsets, int experts, int rows,
-                                                           int N, void* __restrict__ dz, float* __restrict__ sums) {
+                                                           int N, int step, void* __restrict__ dz, float* __restrict__ sums) {
   __shared__ float red[8][kDactCols];
   const int strips = (N + kDactCols - 1) / kDactCols;
   const int piece = blockIdx.x / strips, strip = blockIdx.x % strips;
   RowPiece t;
-  if (!find_row_piece(offsets, experts, rows, kDactRows, [&](int total) { return piece < total ? piece : -1; }, t))
+  if (!find_row_piece(offsets, experts, rows, step, [&](int total) { return piece < total ? piece : -1; }, t))
     return;
   if (t.e == experts) return;   // rows of no expert have no part in any product or sum
   const int P = GATED ? 2 * N : N;
   const int c = strip * kDactCols + (threadIdx.x & 31) * 8, rl = threadIdx.x >> 5;
-  const int r0 = t.row0 + t.index * kDactRows, r1 = min(r0 + kDactRows, t.row0 + t.rows);
+  const int r0 = t.row0 + t.index * step, r1 = min(r0 + step, t.row0 + t.rows);
   const bool in0 = c < N;
   const bool half = sizeof(T) == 4 && in0 && c + 8 > N;   // fp32 widths are multiples of 4 only
   float sg[8] = {}, su[GATED ? 8 : 1] = {};
@@ -137,7 +135,7 @@ __global__ __launch_bounds__(kThr) void linear_dact_kernel(int fn, const void* _
 template <typename GT, bool GATED>
 __global__ __launch_bounds__(kThr) void linear_dbias_kernel(const float* __restrict__ sums,
                                                             const int* __restrict__ offsets, int experts, int rows,
-                                                            int N, int max_pieces, void* db0, void* db1,
+                                                            int N, int step, int max_pieces, void* db0, void* db1,
                                                             int accumulate) {
   __shared__ float red[4][64];
   const int P = GATED ? 2 * N : N, blocks = (P + 63) / 64;
@@ -148,14 +146,14 @@ __global__ __launch_bounds__(kThr) void linear_dbias_kernel(const float* __restr
     int r0, m;
     const int i = base + (int)(threadIdx.x & 63);
     expert_rows(offsets, experts, rows, i, r0, m);
-    int v = i < e ? (m + kDactRows - 1) / kDactRows : 0;
+    int v = i < e ? (m + step - 1) / step : 0;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
     first += v;
   }
   int row0, m;
   expert_rows(offsets, experts, rows, e, row0, m);
-  const int pieces = (m + kDactRows - 1) / kDactRows;
+  const int pieces = (m + step - 1) / step;
   const int b = (int)((int64_t)q * pieces / 4);
   const int end = min((int)((int64_t)(q + 1) * pieces / 4), max_pieces - first);   // offsets may be anything
   float s = 0.0f;
@@ -202,10 +200,10 @@ hipError_t run_linear_reduce(DType io, int gated, const float* partial, int spli
 
 hipError_t run_linear_dact(DType io, int gated, int fn, const void* dy, const void* preact, const int* offsets,
                            int experts, int64_t rows, int64_t N, void* dz, float* sums, hipStream_t s) {
-  const dim3 grid((unsigned)(dact_pieces(rows, experts) * ((N + kDactCols - 1) / kDactCols)));
+  const dim3 grid((unsigned)(dact_pieces(rows, N, experts) * ((N + kDactCols - 1) / kDactCols)));
   return by_type(io, gated, [&](auto v, auto g) {
     hipLaunchKernelGGL((linear_dact_kernel<decltype(v), decltype(g)::value>), grid, dim3(kThr), 0, s, fn, dy, preact,
-                       offsets, experts, (int)rows, (int)N, dz, sums);
+                       offsets, experts, (int)rows, (int)N, dact_rows(rows, N), dz, sums);
     return hipGetLastError();
   });
 }
@@ -216,7 +214,7 @@ hipError_t run_linear_dbias(DType io, int gated, const float* sums, const int* o
   const dim3 grid((unsigned)(experts * ((P + 63) / 64)));
   return by_type(io, gated, [&](auto v, auto g) {
     hipLaunchKernelGGL((linear_dbias_kernel<decltype(v), decltype(g)::value>), grid, dim3(kThr), 0, s, sums, offsets,
-                       experts, (int)rows, (int)N, (int)dact_pieces(rows, experts), db0, db1, accumulate);
+                       experts, (int)rows, (int)N, dact_rows(rows, N), (int)dact_pieces(rows, N, experts), db0, db1, accumulate);
     return hipGetLastError();
   });
 }

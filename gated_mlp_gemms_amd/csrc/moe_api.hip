@@ -79,8 +79,8 @@ mlp_status check_linear(const linear_desc* d) {
     return fail(MLP_ERR_UNSUPPORTED, "a leading dimension (K, N, or 2N gated) is 2^25 elements or more");
   if (d->M > lim / P || d->M > lim / d->K || E * P > lim / d->K)
     return fail(MLP_ERR_UNSUPPORTED, "a matrix of the problem has more than 2^37 elements");
-  if ((d->M / kDactRows + 1) * (E + 1) >= (int64_t)1 << 31)
-    return fail(MLP_ERR_UNSUPPORTED, "M times experts is above 2^37");
+  if ((d->M / kDactRowsFew + 1) * (E + 1) >= (int64_t)1 << 31)
+    return fail(MLP_ERR_UNSUPPORTED, "M times experts is above 2^35");
   const int q = d->dtype == MLP_F32 ? 4 : 8;
   if (d->K % q || d->N % q) return fail(MLP_ERR_ALIGNMENT, "K and N must be multiples of %d (16-byte rows)", q);
   return MLP_OK;
@@ -185,7 +185,7 @@ LinearWs linear_ws(const linear_desc* d, int phase) {
     take(w.partial, partial_bytes(f.plan, d->M, P));
   } else {
     take(w.dz, d->act == LINEAR_ACT_NONE ? 0 : (size_t)d->M * P * esize(d->dtype));
-    take(w.sums, (size_t)dact_pieces(d->M, E) * P * sizeof(float));
+    take(w.sums, (size_t)dact_pieces(d->M, d->N, E) * P * sizeof(float));
     if (d->experts == 0 && d->M > 0) {
       const LinearBwd b = plan_linear_bwd(d, false, false);
       take(w.partial, std::max(partial_bytes(b.dx, d->M, d->K), partial_bytes(b.dw, P, d->K)));

@@ -590,3 +590,11 @@ def test_streamed_rows_equal_cached_ones(dtype):
         gm.moe_combine_bwd(x[a:b].contiguous(), ys1, w[a:b].contiguous(), r1, s1, o1, dys1, dw1)
         assert torch.equal(out[a:b], out1) and torch.equal(dx[a:b], dx1) and torch.equal(dw[a:b], dw1)
         assert torch.equal(dys[row[a * k:b * k].long()][s1.long()], dys1)
+
+
+@pytest.mark.parametrize("M,K,N,act", [(8192, 2048, 4864, "gelu_tanh"), (4100, 1544, 8200, "none"), (6000, 2056, 2312, "swiglu"),
+                                       (9000, 1032, 2056, "reglu"), (3080, 4096, 4096, "relu")])
+def test_linear_backward_in_one_launch(M, K, N, act):
+    """Sizes whose dx and dW may share a launch, ragged ones among them."""
+    for dt in (torch.bfloat16, torch.float16):
+        check_linear(M, K, N, act, dt, bias=False, residual=False)
