@@ -53,7 +53,7 @@ __device__ __forceinline__ void epi_prefetch(const GemmArgs& p, int m, int n, Au
     x.b = *reinterpret_cast<const u32x4*>(elem_ptr<IoT>(p.aux, m, p.ld_aux, p.half + n));
   } else if constexpr (EPI == EPI_DACT) {
     x.a = *reinterpret_cast<const u32x4*>(elem_ptr<IoT>(p.aux, m, p.ld_aux, n));
-  } else if constexpr (EPI == EPI_STORE) {
+  } else if constexpr (EPI == EPI_STORE || EPI == EPI_STORE_PART) {
     if (p.accumulate) {
       const bool lo = m < p.c_split;
       const float* q = reinterpret_cast<const float*>(elem_ptr<float>(lo ? p.C0 : p.C1, lo ? m : m - p.c_split, p.ldc0, n));
@@ -82,7 +82,11 @@ template <int EPI, typename IoT>
 __device__ __forceinline__ void epi_row8(const GemmArgs& p, int m, int n, int split, const float (&v)[8],
                                          const float (&u)[8], const AuxPiece& x, float& local_amax) {
   static_assert(EPI != EPI_F8ACT && EPI != EPI_F8DACT, "the quantizing epilogues are 16 columns wide");
-  if constexpr (EPI == EPI_STORE) {
+  if constexpr (EPI == EPI_STORE || EPI == EPI_STORE_PART) {
+    if (EPI == EPI_STORE_PART && p.partial) {
+      Vec8<float>::store(elem_ptr<float>(p.partial, m, p.N, n), v);
+      return;
+    }
     const bool lo = m < p.c_split;
     void* base = lo ? p.C0 : p.C1;
     const int row = lo ? m : m - p.c_split;

@@ -26,8 +26,9 @@ enum Epi : int {
                     // C0 = e5m2(dpre / *s_post) (s_post holds the dpre scale here);
                     // *amax = max(*amax, max |dpre|); C1 set: C1 = e4m3(relu(pre)^2 / *s_c1)
   EPI_LIN = 8,      // z = acc + bias0[n] -> aux (flag 1); C0 = res + f(z) (bias0, res may be NULL)
-  EPI_LIN_GATED = 9 // g, u = acc pair + bias0[n], bias1[n] -> aux[m][n], aux[m][half+n] (flag 1);
+  EPI_LIN_GATED = 9,// g, u = acc pair + bias0[n], bias1[n] -> aux[m][n], aux[m][half+n] (flag 1);
                     // C0 = res + f(g) u
+  EPI_STORE_PART = 10   // STORE, or with partial set the accumulators in fp32 to partial[m][n]
 };
 
 // Epilogues whose tile holds gate rows and the up rows of the same units.
@@ -67,8 +68,28 @@ struct ExpertGemm {
   int grid;   // workgroups: an upper bound of the tiles for a product over rows
   int split_tail;   // products over rows in 256-row tiles: a last round of at most half the CUs runs as halves
 };
-// The backward's two products, in one launch: workgroups [0, dx.grid) and the dw.grid after them.
-struct ExpertBwd { ExpertGemm dx, dw; };
+// The bias gradients from the column sums of pieces of at most `step` rows (run_linear_dact): db0
+// [experts, N], and db1 for the other N columns of a gated layer; written, or added into fp32.
+struct BiasGrad {
+  const float* sums;
+  const int* offsets;
+  int experts, rows, N, step, max_pieces, accumulate;
+  void* db0; void* db1;
+  int grid;
+};
+// The backward's two products and the bias gradient in one launch: the workgroups of dx and of dW (dw_first:
+// the other way round), then the bias gradient's.
+//  * dx_splits > 1: dx's K in parts of dx_kps, fp32 sums in part_x [dx_splits][rows][N];
+//  * piece_rows: an expert of more rows has its weight gradient summed over pieces of that many, fp32 sums in
+//    part_w [slots][M][N], slots counted over such experts in order, max_slots at most (0: never).
+// run_expert_join adds up either.
+struct ExpertBwd {
+  ExpertGemm dx, dw;
+  BiasGrad db;
+  int dw_first;
+  int dx_splits, dx_kps; float* part_x;
+  int piece_rows, max_slots; float* part_w;
+};
 
 // Up to kGroupMax independent GEMMs run by one launch (gemm_dma_group_kernel): member j covers
 // workgroups [begin[j], begin[j+1]) (multiples of 8 apart), has items[j] tiles (one per

@@ -245,7 +245,11 @@ struct MNTileDma {
 
   // k-rows kr .. kr+3 land in distinct 64-byte groups, and k-rows 8 apart (read in the same pass
   // by the 16x16 fragments) in distinct 32-byte halves of them
-  static __device__ __forceinline__ int phys_chunk(int c, int kr) { return c ^ ((kr & 3) << 2) ^ (((kr >> 3) & 1) << 1); }
+  // (64-column tiles have 8 chunks a k-row: the same k-row bits, inside them)
+  static __device__ __forceinline__ int phys_chunk(int c, int kr) {
+    if constexpr (ROWS == 64) return c ^ ((kr & 3) << 1) ^ ((kr >> 3) & 1);
+    return c ^ ((kr & 3) << 2) ^ (((kr >> 3) & 1) << 1);
+  }
 
   // b: element (0, tile column 0) of the first matrix; ld: its row pitch in bytes; ncols: columns
   // of the matrix from tile column 0 on (a multiple of 8). Chunks of tile columns past the matrix

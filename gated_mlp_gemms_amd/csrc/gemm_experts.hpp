@@ -33,8 +33,9 @@ __device__ __forceinline__ void expert_rows(const int* offsets, int experts, int
 
 // Pieces of every expert (the rows behind the last offset included) are numbered in expert order.
 // count(total) -> the number of the piece wanted, or -1. Called by whole waves; every wave of a
-// workgroup gets the same answer, in scalar registers.
-template <typename Want>
+// workgroup gets the same answer, in scalar registers. LEAST: pieces an expert has at least (the rows
+// behind the last offset then have none).
+template <int LEAST = 0, typename Want>
 __device__ __forceinline__ bool find_row_piece(const int* offsets, int experts, int rows, int step, Want want,
                                                RowPiece& out) {
   const int lane = threadIdx.x & 63;
@@ -42,6 +43,7 @@ __device__ __forceinline__ bool find_row_piece(const int* offsets, int experts, 
   auto scan = [&](int base) {   // inclusive scan of the pieces of experts base .. base + 63
     expert_rows(offsets, experts, rows, base + lane, row0, n);
     pieces = (n + step - 1) / step;
+    if constexpr (LEAST > 0) pieces = base + lane < experts ? max(pieces, LEAST) : 0;
     incl = pieces;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -93,16 +95,24 @@ constexpr int expert_lds_bytes() {
 // filled round of the 256 CUs run as two 128-row halves each: 32768 rows of 32 uneven experts are 6.3 rounds
 // of full tiles, which without the halves take the time of 7.
 template <typename T, int BM, int BN, bool BK, int EPI, int WAVES>
-__device__ __forceinline__ void expert_rows_tile(const ExpertGemm& a, int b, char* smem) {
+__device__ __forceinline__ void expert_rows_tile(const ExpertGemm& a, int b, char* smem, int splits = 1, int kps = 0,
+                                                 float* part = nullptr) {
   constexpr int BNC = epi_gated(EPI) ? BN / 2 : BN;   // output columns of a tile
   constexpr bool HALVES = WAVES == 8;
   constexpr int HM = BM / 2;
   const int tiles_n = a.g.tiles_n;
-  int tile = 0, half = -1;
+  int tile = 0, half = -1, split = 0;
   RowPiece t;
   // XCD-contiguous over the tiles there are, not over the launch's upper bound
   const bool found = find_row_piece(a.offsets, a.experts, a.rows, BM, [&](int total) {
-    const int tiles = (int)min((int64_t)total * tiles_n, (int64_t)a.grid);
+    const int tiles = (int)min((int64_t)total * tiles_n, (int64_t)(a.grid / splits));
+    if (EPI == EPI_STORE_PART && splits > 1) {
+      if (b >= tiles * splits) return -1;
+      tile = xcd_remap(b, tiles * splits);
+      split = tile / tiles;
+      tile -= split * tiles;
+      return tile / tiles_n;
+    }
     const int rem = tiles % 256, tail = HALVES && a.split_tail && rem <= 128 && tiles > 256 ? rem : 0;
     const int whole = tiles - tail;
     if (b < whole) {
@@ -118,7 +128,7 @@ __device__ __forceinline__ void expert_rows_tile(const ExpertGemm& a, int b, cha
   if (!found) return;
   GemmArgs p = a.g;
   if (t.e == a.experts) {   // rows of no expert: zeros (plus the residual)
-    if (half > 0) return;   // (the first half fills the whole tile)
+    if (half > 0 || splits > 1) return;   // (the first half fills the whole tile; joining sums fills them, too)
     const int m0 = t.row0 + t.index * BM, m1 = min(m0 + BM, a.rows);
     const int n0 = (tile % tiles_n) * BNC, n1 = min(n0 + BNC, p.N);
     constexpr int V = 16 / ElemTraits<T>::bytes, W = BNC / V;
@@ -152,6 +162,21 @@ __device__ __forceinline__ void expert_rows_tile(const ExpertGemm& a, int b, cha
   p.B1 = shift<T>(p.B1, t.e * a.w_stride);
   p.bias0 = shift<T>(p.bias0, t.e * a.bias_stride);
   p.bias1 = shift<T>(p.bias1, t.e * a.bias_stride);
+  if (EPI == EPI_STORE_PART && splits > 1) {   // this part of K (B stacked from B0 and B1 along it)
+    const int k0 = split * kps;
+    p.K = min(kps, p.K - k0);
+    p.k_per_split = p.K;
+    p.A = shift<T>(p.A, k0);
+    if (p.B1 != nullptr && k0 >= p.b_split) {
+      p.B0 = shift<T>(p.B1, (k0 - p.b_split) * p.ldb);
+      p.B1 = nullptr;
+      p.b_split = 1 << 30;
+    } else {
+      p.B0 = shift<T>(p.B0, k0 * p.ldb);
+      if (p.B1 != nullptr) p.b_split -= k0;
+    }
+    p.partial = part + ((int64_t)split * a.rows + row0) * p.N;
+  }
   if constexpr (HALVES) {
     if (rows <= HM) {
       gemm_dma_tile<T, T, HM, BN, true, BK, EPI, WAVES, true, 4>(p, tn, smem);
@@ -161,23 +186,106 @@ __device__ __forceinline__ void expert_rows_tile(const ExpertGemm& a, int b, cha
   gemm_dma_tile<T, T, BM, BN, true, BK, EPI, WAVES, true>(p, tn, smem);
 }
 
-// Tile `item` of the weight gradients dW_e = dz^T x over expert e's rows.
+// The first slot of expert e's partial sums: pieces of the experts before it that have more than one.
+__device__ __forceinline__ int expert_slots_before(const int* offsets, int experts, int rows, int piece_rows, int e) {
+  const int lane = threadIdx.x & 63;
+  int slots = 0;
+  for (int base = 0; base < e; base += 64) {
+    int r0, n;
+    expert_rows(offsets, experts, rows, base + lane, r0, n);
+    int v = base + lane < e && n > piece_rows ? (n + piece_rows - 1) / piece_rows : 0;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    slots += v;
+  }
+  return __builtin_amdgcn_readfirstlane(slots);
+}
+
+// Tile b of the weight gradients dW_e = dz^T x over expert e's rows, or over a piece of them.
 template <typename T, typename GT, int BM, int BN, int WAVES>
-__device__ __forceinline__ void expert_grad_tile(const ExpertGemm& a, int item, char* smem) {
+__device__ __forceinline__ void expert_grad_tile(const ExpertBwd& all, int b, char* smem) {
+  const ExpertGemm& a = all.dw;
   GemmArgs p = a.g;
   const int tiles = p.tiles_m * p.tiles_n;
-  const int e = item / tiles;
-  int row0, n;
-  expert_rows(a.offsets, a.experts, a.rows, e, row0, n);
-  row0 = __builtin_amdgcn_readfirstlane(row0);
-  n = __builtin_amdgcn_readfirstlane(n);
+  int e, row0, n, item;
+  if (all.piece_rows) {
+    RowPiece t;
+    int tile = 0;
+    const bool found = find_row_piece<1>(a.offsets, a.experts, a.rows, all.piece_rows, [&](int total) {
+      const int count = (int)min((int64_t)total * tiles, (int64_t)a.grid);
+      if (b >= count) return -1;
+      tile = xcd_remap(b, count);
+      return tile / tiles;
+    }, t);
+    if (!found) return;
+    e = t.e;
+    row0 = t.row0 + t.index * all.piece_rows;
+    n = min(t.rows - t.index * all.piece_rows, all.piece_rows);
+    item = tile - (t.first + t.index) * tiles;
+    if (t.rows > all.piece_rows) {
+      const int slot = expert_slots_before(a.offsets, a.experts, a.rows, all.piece_rows, e) + t.index;
+      if (slot >= all.max_slots) return;   // offsets may be anything
+      p.partial = all.part_w + (int64_t)slot * p.M * p.N;
+    }
+  } else {
+    b = xcd_remap(b, a.grid);
+    e = b / tiles;
+    item = b - e * tiles;
+    expert_rows(a.offsets, a.experts, a.rows, e, row0, n);
+    row0 = __builtin_amdgcn_readfirstlane(row0);
+    n = __builtin_amdgcn_readfirstlane(n);
+  }
   if (n == 0 && p.accumulate) return;
   p.K = p.k_per_split = n;
   p.A = shift<T>(p.A, row0 * p.lda);
   p.B0 = shift<T>(p.B0, row0 * p.ldb);
   p.C0 = shift<GT>(p.C0, e * a.w_stride);
   p.C1 = shift<GT>(p.C1, e * a.w_stride);
-  gemm_dma_tile<T, GT, BM, BN, false, false, EPI_STORE, WAVES, true>(p, item - e * tiles, smem);
+  gemm_dma_tile<T, GT, BM, BN, false, false, EPI_STORE_PART, WAVES, true>(p, item, smem);
+}
+
+// The pieces' sums of one expert joined, 16 columns by 16 runs of pieces a workgroup (of 256 threads, or
+// more that do nothing), the runs added in order. red: 256 floats.
+template <typename GT>
+__device__ __forceinline__ void bias_grad_block(const BiasGrad& a, int block, float* red) {
+  const int lane = threadIdx.x & 63, run = threadIdx.x >> 4;
+  const int P = a.db1 ? 2 * a.N : a.N, blocks = (P + 15) / 16;
+  const int e = block / blocks, n = (block % blocks) * 16 + (threadIdx.x & 15);
+  // the expert's first piece: the pieces of the experts before, counted 64 experts at a time
+  int first = 0;
+  for (int base = 0; base < e; base += 64) {
+    int r0, m;
+    const int i = base + lane;
+    expert_rows(a.offsets, a.experts, a.rows, i, r0, m);
+    int v = i < e ? (m + a.step - 1) / a.step : 0;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    first += v;
+  }
+  int row0, m;
+  expert_rows(a.offsets, a.experts, a.rows, e, row0, m);
+  const int pieces = (m + a.step - 1) / a.step;
+  const int b = (int)((int64_t)run * pieces / 16);
+  const int end = min((int)((int64_t)(run + 1) * pieces / 16), a.max_pieces - first);   // offsets may be anything
+  float s = 0.0f;
+  if (n < P && run < 16) {
+#pragma unroll 8
+    for (int i = b; i < end; ++i) s += a.sums[(int64_t)(first + i) * P + n];
+  }
+  if (run < 16) red[threadIdx.x] = s;
+  __syncthreads();
+  if (run != 0 || n >= P) return;
+  s = red[threadIdx.x];
+  for (int w = 1; w < 16; ++w) s += red[w * 16 + threadIdx.x];
+  void* db = n >= a.N ? a.db1 : a.db0;
+  const int64_t at = (int64_t)e * a.N + (n >= a.N ? n - a.N : n);
+  if (a.accumulate) {
+    if (pieces > 0) reinterpret_cast<float*>(db)[at] += s;
+  } else if constexpr (sizeof(GT) == 4) {
+    reinterpret_cast<float*>(db)[at] = s;
+  } else {
+    reinterpret_cast<uint16_t*>(db)[at] = (uint16_t)Bits16<GT>::from_f32(s);
+  }
 }
 
 template <typename T, int BM, int BN, int EPI, int WAVES>
@@ -189,9 +297,16 @@ __global__ __launch_bounds__(64 * WAVES, 1) void expert_fwd_kernel(const ExpertG
 template <typename T, typename GT, int BM, int BN, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 1) void expert_bwd_kernel(const ExpertBwd a) {
   __shared__ __attribute__((aligned(1024))) char smem[expert_lds_bytes<T, BM, BN, WAVES>()];
-  const int b = blockIdx.x;
-  if (b < a.dx.grid) expert_rows_tile<T, BM, BN, false, EPI_STORE, WAVES>(a.dx, b, smem);
-  else expert_grad_tile<T, GT, BM, BN, WAVES>(a.dw, xcd_remap(b - a.dx.grid, a.dw.grid), smem);
+  int b = blockIdx.x;
+  const int first = a.dw_first ? a.dw.grid : a.dx.grid;
+  if (b >= a.dx.grid + a.dw.grid) {
+    bias_grad_block<GT>(a.db, b - a.dx.grid - a.dw.grid, reinterpret_cast<float*>(smem));
+  } else if ((b < first) == (a.dw_first != 0)) {
+    expert_grad_tile<T, GT, BM, BN, WAVES>(a, a.dw_first ? b : b - first, smem);
+  } else {
+    expert_rows_tile<T, BM, BN, false, EPI_STORE_PART, WAVES>(a.dx, a.dw_first ? b - first : b, smem, a.dx_splits, a.dx_kps,
+                                                              a.part_x);
+  }
 }
 
 template <typename T, int BM, int BN, int WAVES>
@@ -205,21 +320,32 @@ hipError_t launch_expert_fwd(int epi, const ExpertGemm& a, hipStream_t s) {
 
 template <typename T, int BM, int BN, int WAVES>
 hipError_t launch_expert_bwd(const ExpertBwd& a, hipStream_t s) {
-  const dim3 grid(a.dx.grid + a.dw.grid), block(64 * WAVES);
-  if (a.dw.g.accumulate) hipLaunchKernelGGL((expert_bwd_kernel<T, float, BM, BN, WAVES>), grid, block, 0, s, a);
+  const dim3 grid(a.dx.grid + a.dw.grid + a.db.grid), block(64 * WAVES);
+  if (a.dw.g.accumulate || a.db.accumulate) hipLaunchKernelGGL((expert_bwd_kernel<T, float, BM, BN, WAVES>), grid, block, 0, s, a);
   else hipLaunchKernelGGL((expert_bwd_kernel<T, T, BM, BN, WAVES>), grid, block, 0, s, a);
   return hipGetLastError();
 }
 
-// The 16-bit experts' products of one type: 8-wave 256 x 256 tiles or 4-wave 128 x 128 ones.
+// The small tiles: 64 x 64, and 64 x 128 (64 gate and 64 up rows) for a gated forward.
+template <typename T> hipError_t launch_expert_fwd_small(int epi, const ExpertGemm& a, hipStream_t s) {
+  if (epi == EPI_LIN_GATED)
+    hipLaunchKernelGGL((expert_fwd_kernel<T, 64, 128, EPI_LIN_GATED, 4>), dim3(a.grid), dim3(256), 0, s, a);
+  else
+    hipLaunchKernelGGL((expert_fwd_kernel<T, 64, 64, EPI_LIN, 4>), dim3(a.grid), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+// The 16-bit experts' products of one type.
 template <typename T> hipError_t expert_fwd16(int epi, TileShape tile, const ExpertGemm& a, hipStream_t s) {
   if (tile == TILE_256x256_W8) return launch_expert_fwd<T, 256, 256, 8>(epi, a, s);
   if (tile == TILE_128x128) return launch_expert_fwd<T, 128, 128, 4>(epi, a, s);
+  if (tile == TILE_64x64) return launch_expert_fwd_small<T>(epi, a, s);
   return hipErrorInvalidValue;
 }
 template <typename T> hipError_t expert_bwd16(TileShape tile, const ExpertBwd& a, hipStream_t s) {
   if (tile == TILE_256x256_W8) return launch_expert_bwd<T, 256, 256, 8>(a, s);
   if (tile == TILE_128x128) return launch_expert_bwd<T, 128, 128, 4>(a, s);
+  if (tile == TILE_64x64) return launch_expert_bwd<T, 64, 64, 4>(a, s);
   return hipErrorInvalidValue;
 }
 

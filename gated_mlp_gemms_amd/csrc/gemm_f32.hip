@@ -6,7 +6,7 @@
 namespace gmlp {
 
 hipError_t run_gemm_f32(Layout layout, int epi, TileShape tile, const GemmArgs& a, int grid, hipStream_t s) {
-  if (tile == TILE_128x128_RING || tile == TILE_64x64_RING) return run_gemm_f32_ring(layout, epi, tile, a, grid, s);
+  if (tile == TILE_128x128_RING || tile == TILE_64x64) return run_gemm_f32_ring(layout, epi, tile, a, grid, s);
   if (tile != TILE_128x128) return hipErrorInvalidValue;
   constexpr int B = 128;
   switch (layout) {

@@ -32,7 +32,7 @@ static hipError_t ring(Layout layout, int epi, const GemmArgs& a, int grid, hipS
 
 hipError_t run_gemm_f32_ring(Layout layout, int epi, TileShape tile, const GemmArgs& a, int grid, hipStream_t s) {
   if (tile == TILE_128x128_RING) return ring<128>(layout, epi, a, grid, s);
-  if (tile == TILE_64x64_RING) return ring<64>(layout, epi, a, grid, s);
+  if (tile == TILE_64x64) return ring<64>(layout, epi, a, grid, s);
   return hipErrorInvalidValue;
 }
 

@@ -285,7 +285,11 @@ __device__ __forceinline__ void epilogue(const GemmArgs& p, f32x16 (&acc)[MI][NI
 #pragma unroll
         for (int r = 0; r < 4; ++r) v[r] = scale * acc[i][j][4 * g + r];
 
-        if constexpr (EPI == EPI_STORE) {
+        if constexpr (EPI == EPI_STORE || EPI == EPI_STORE_PART) {
+          if (EPI == EPI_STORE_PART && p.partial) {
+            Vec4<float>::store(elem_ptr<float>(p.partial, m, p.N, n), v);
+            continue;
+          }
           const bool lo = m < p.c_split;
           void* base = lo ? p.C0 : p.C1;
           const int row = lo ? m : m - p.c_split;

@@ -12,10 +12,11 @@ namespace gmlp {
 enum DType : int { DT_F32 = 0, DT_BF16 = 1, DT_E4M3 = 2, DT_F16 = 3, DT_F8G = 4 };
 enum Layout : int { NT = 0, NN = 1, TN = 2 };   // A K-major/B K-major, A K/B MN, A MN/B MN
 // Tile shapes of the bf16 / e4m3 kernel; _W8 runs the tile with 8 waves (two per SIMD). _RING: the
-// linear layer's and the experts' fp32 tiles, on the 16-bit kernels' DMA ring (64 x 64: 64 x 128 gated).
+// linear layer's and the experts' fp32 tile on the 16-bit kernels' DMA ring; TILE_64x64: theirs for small
+// products, every type (64 x 128 where a tile holds gate and up rows).
 enum TileShape : int {
   TILE_256x256 = 0, TILE_256x128 = 1, TILE_128x128 = 2, TILE_256x256_W8 = 3, TILE_256x128_W8 = 4, TILE_128x128_RING = 5,
-  TILE_64x64_RING = 6, TILE_COUNT = 7
+  TILE_64x64 = 6, TILE_COUNT = 7
 };
 
 // One GEMM launch. `io` is the element type of the epilogue's stored/loaded tensors (for
@@ -63,12 +64,15 @@ inline bool skinny_parts_for(int64_t M, int64_t N, int64_t K) { return M > 8 && 
 hipError_t run_gemm_linear(DType in, int epi, TileShape tile, const GemmArgs& a, int grid, hipStream_t s);
 hipError_t run_gemm_bf16_linear(int epi, TileShape tile, const GemmArgs& a, int grid, hipStream_t s);
 hipError_t run_gemm_f16_linear(int epi, TileShape tile, const GemmArgs& a, int grid, hipStream_t s);
+// 16-bit 64 x 64 tiles, the same products.
+hipError_t run_gemm_small16(DType in, DType io, Layout layout, int epi, const GemmArgs& a, int grid, hipStream_t s);
 // fp32 on the DMA ring: NT with the linear epilogues or partial sums, NN and TN with the store or those.
 hipError_t run_gemm_f32_ring(Layout layout, int epi, TileShape tile, const GemmArgs& a, int grid, hipStream_t s);
 // The same from fp32 partials [splits][M][N] (gated: [splits][M][2N], g then u), summed in order.
 hipError_t run_linear_reduce(DType io, int gated, const float* partial, int splits, const GemmArgs& a, hipStream_t s);
 
-// One product an expert (ExpertGemm). Tiles: TILE_256x256_W8 and TILE_128x128, f32 the _RING ones.
+// One product an expert (ExpertGemm). Tiles: TILE_256x256_W8, TILE_128x128 (f32: its _RING) and
+// TILE_64x64.
 hipError_t run_expert_fwd(DType in, int epi, TileShape tile, const ExpertGemm& a, hipStream_t s);
 hipError_t run_expert_bwd(DType in, TileShape tile, const ExpertBwd& a, hipStream_t s);
 hipError_t run_expert_fwd_bf16(int epi, TileShape tile, const ExpertGemm& a, hipStream_t s);
@@ -77,6 +81,8 @@ hipError_t run_expert_fwd_f32(int epi, TileShape tile, const ExpertGemm& a, hipS
 hipError_t run_expert_bwd_bf16(TileShape tile, const ExpertBwd& a, hipStream_t s);
 hipError_t run_expert_bwd_f16(TileShape tile, const ExpertBwd& a, hipStream_t s);
 hipError_t run_expert_bwd_f32(TileShape tile, const ExpertBwd& a, hipStream_t s);
+// The partial sums of run_expert_bwd added up (nothing without any).
+hipError_t run_expert_join(DType io, const ExpertBwd& a, hipStream_t s);
 // The forward with a few rows an expert, 16-bit (g.N output columns, any rows; grid is unused).
 // Taken up to kExpertFewRows rows an expert on average. 64 experts, 2048 x 1376 gate and up, uneven rows,
 // against 128 x 128 tiles: 96 rows 78 and 96 us, 300 rows 134 and 153, 600 rows 161 and 154, 1000 rows 207 and 158
@@ -97,10 +103,8 @@ inline int64_t dact_pieces(int64_t rows, int64_t N, int64_t experts) {
 }
 hipError_t run_linear_dact(DType io, int gated, int fn, const void* dy, const void* preact, const int* offsets,
                            int experts, int64_t rows, int64_t N, void* dz, float* sums, hipStream_t s);
-// The pieces' sums joined in order: db0 (gated: the first N columns; db1 the others) [experts, N], in
-// `io` or added into fp32 (accumulate).
-hipError_t run_linear_dbias(DType io, int gated, const float* sums, const int* offsets, int experts, int64_t rows,
-                            int64_t N, void* db0, void* db1, int accumulate, hipStream_t s);
+// The pieces' sums joined (BiasGrad, in `io`), as a launch of its own.
+hipError_t run_linear_dbias(DType io, const BiasGrad& a, hipStream_t s);
 
 // ---- router, sort, rows ---------------------------------------------------------------------------
 

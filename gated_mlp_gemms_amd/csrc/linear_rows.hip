@@ -131,48 +131,60 @@ __global__ __launch_bounds__(kThr) void linear_dact_kernel(int fn, const void* _
   if constexpr (GATED) join(su, N);
 }
 
-// db[e][n] = the sum of expert e's pieces, 64 columns x 4 runs of pieces a workgroup.
-template <typename GT, bool GATED>
-__global__ __launch_bounds__(kThr) void linear_dbias_kernel(const float* __restrict__ sums,
-                                                            const int* __restrict__ offsets, int experts, int rows,
-                                                            int N, int step, int max_pieces, void* db0, void* db1,
-                                                            int accumulate) {
-  __shared__ float red[4][64];
-  const int P = GATED ? 2 * N : N, blocks = (P + 63) / 64;
-  const int e = blockIdx.x / blocks, n = (blockIdx.x % blocks) * 64 + (threadIdx.x & 63), q = threadIdx.x >> 6;
-  // the expert's first piece: the pieces of the experts before, counted 64 experts at a time
-  int first = 0;
-  for (int base = 0; base < e; base += 64) {
-    int r0, m;
-    const int i = base + (int)(threadIdx.x & 63);
-    expert_rows(offsets, experts, rows, i, r0, m);
-    int v = i < e ? (m + step - 1) / step : 0;
+template <typename GT>
+__global__ __launch_bounds__(kThr) void linear_dbias_kernel(const BiasGrad a) {
+  __shared__ float red[kThr];
+  bias_grad_block<GT>(a, blockIdx.x, red);
+}
+
+// The experts' partial sums joined (ExpertBwd): workgroups [0, dx_blocks) add up dx's parts (zeros behind the
+// last offset), kJoinBlocks an expert after them the pieces of the weight gradients that have several.
+constexpr int kJoinBlocks = 64;
+
+template <typename T, typename GT>
+__global__ __launch_bounds__(kThr) void expert_join_kernel(const ExpertBwd a, int dx_blocks) {
+  const int b = blockIdx.x;
+  auto add = [](const float* src, int64_t plane, int count) {
+    f32x4 s = *reinterpret_cast<const f32x4*>(src);
+#pragma unroll 4
+    for (int i = 1; i < count; ++i) s += *reinterpret_cast<const f32x4*>(src + i * plane);
+    return s;
+  };
+  if (b < dx_blocks) {
+    const ExpertGemm& g = a.dx;
+    const int kept = g.offsets ? min(max(g.offsets[g.experts], 0), g.rows) : g.rows;
+    const int64_t plane = (int64_t)g.rows * g.g.N, total = plane / 4;
+    for (int64_t i = b * (int64_t)kThr + threadIdx.x; i < total; i += (int64_t)dx_blocks * kThr) {
+      const int64_t at = i * 4;
+      const f32x4 s = at / g.g.N < kept ? add(a.part_x + at, plane, a.dx_splits) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      const float v[4] = {s[0], s[1], s[2], s[3]};
+      Vec4<T>::store(elem_ptr<T>(g.g.C0, 0, 0, at), v);
+    }
+    return;
+  }
+  const ExpertGemm& g = a.dw;
+  const int e = (b - dx_blocks) / kJoinBlocks, part = (b - dx_blocks) % kJoinBlocks;
+  int row0, n;
+  expert_rows(g.offsets, g.experts, g.rows, e, row0, n);
+  if (n <= a.piece_rows) return;
+  const int slot = expert_slots_before(g.offsets, g.experts, g.rows, a.piece_rows, e);
+  const int count = (n + a.piece_rows - 1) / a.piece_rows;
+  if (slot + count > a.max_slots) return;   // offsets may be anything
+  const int64_t plane = (int64_t)g.g.M * g.g.N, total = plane / 4;
+  const float* src = a.part_w + slot * plane;
+  for (int64_t i = part * (int64_t)kThr + threadIdx.x; i < total; i += kJoinBlocks * kThr) {
+    const int64_t at = i * 4, m = at / g.g.N, col = at - m * g.g.N;
+    const f32x4 s = add(src + at, plane, count);
+    float v[4] = {s[0], s[1], s[2], s[3]};
+    const bool lo = m < g.g.c_split;
+    char* dst = elem_ptr<GT>(lo ? g.g.C0 : g.g.C1, lo ? m : m - g.g.c_split, g.g.ldc0, e * g.w_stride + col);
+    if (g.g.accumulate) {
+      float o[4];
+      Vec4<float>::load(dst, o);
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-    first += v;
-  }
-  int row0, m;
-  expert_rows(offsets, experts, rows, e, row0, m);
-  const int pieces = (m + step - 1) / step;
-  const int b = (int)((int64_t)q * pieces / 4);
-  const int end = min((int)((int64_t)(q + 1) * pieces / 4), max_pieces - first);   // offsets may be anything
-  float s = 0.0f;
-  if (n < P) {
-#pragma unroll 8
-    for (int i = b; i < end; ++i) s += sums[(int64_t)(first + i) * P + n];
-  }
-  red[q][threadIdx.x & 63] = s;
-  __syncthreads();
-  if (q != 0 || n >= P) return;
-  s = ((red[0][threadIdx.x] + red[1][threadIdx.x]) + red[2][threadIdx.x]) + red[3][threadIdx.x];
-  void* db = GATED && n >= N ? db1 : db0;
-  const int64_t at = (int64_t)e * N + (GATED && n >= N ? n - N : n);
-  if (accumulate) {
-    if (pieces > 0) reinterpret_cast<float*>(db)[at] += s;
-  } else if constexpr (sizeof(GT) == 4) {
-    reinterpret_cast<float*>(db)[at] = s;
-  } else {
-    reinterpret_cast<uint16_t*>(db)[at] = (uint16_t)Bits16<GT>::from_f32(s);
+      for (int r = 0; r < 4; ++r) v[r] += o[r];
+    }
+    Vec4<GT>::store(dst, v);
   }
 }
 
@@ -208,13 +220,22 @@ hipError_t run_linear_dact(DType io, int gated, int fn, const void* dy, const vo
   });
 }
 
-hipError_t run_linear_dbias(DType io, int gated, const float* sums, const int* offsets, int experts, int64_t rows,
-                            int64_t N, void* db0, void* db1, int accumulate, hipStream_t s) {
-  const int64_t P = gated ? 2 * N : N;
-  const dim3 grid((unsigned)(experts * ((P + 63) / 64)));
-  return by_type(io, gated, [&](auto v, auto g) {
-    hipLaunchKernelGGL((linear_dbias_kernel<decltype(v), decltype(g)::value>), grid, dim3(kThr), 0, s, sums, offsets,
-                       experts, (int)rows, (int)N, dact_rows(rows, N), (int)dact_pieces(rows, N, experts), db0, db1, accumulate);
+hipError_t run_linear_dbias(DType io, const BiasGrad& a, hipStream_t s) {
+  return by_type(a.accumulate ? DT_F32 : io, 0, [&](auto v, auto) {
+    hipLaunchKernelGGL((linear_dbias_kernel<decltype(v)>), dim3(a.grid), dim3(kThr), 0, s, a);
+    return hipGetLastError();
+  });
+}
+
+hipError_t run_expert_join(DType io, const ExpertBwd& a, hipStream_t s) {
+  const int64_t items = a.dx_splits > 1 ? (int64_t)a.dx.rows * a.dx.g.N / 4 : 0;
+  const int dx_blocks = (int)std::min<int64_t>((items + kThr - 1) / kThr, 256 * 16);
+  const int blocks = dx_blocks + (a.piece_rows ? a.dw.experts * kJoinBlocks : 0);
+  if (blocks == 0) return hipSuccess;
+  return by_type(io, a.dw.g.accumulate, [&](auto v, auto acc) {
+    using T = decltype(v);
+    using GT = typename std::conditional<decltype(acc)::value, float, T>::type;
+    hipLaunchKernelGGL((expert_join_kernel<T, GT>), dim3(blocks), dim3(kThr), 0, s, a, dx_blocks);
     return hipGetLastError();
   });
 }

@@ -1271,6 +1271,7 @@ namespace gmlp {
 hipError_t run_gemm(DType in, DType io, Layout layout, int epi, TileShape tile, const GemmArgs& a,
                     int grid, hipStream_t s) {
   if (grid <= 0) return hipSuccess;
+  if (tile == TILE_64x64 && in != DT_F32) return run_gemm_small16(in, io, layout, epi, a, grid, s);
   switch (in) {
     case DT_BF16:
       if (layout == NT) return run_gemm_bf16_nt(io, epi, tile, a, grid, s);

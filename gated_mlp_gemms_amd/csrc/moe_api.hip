@@ -1,6 +1,7 @@
 // C-ABI of the mixture-of-experts operators (moe.h): argument checks, all on the host before any HIP
 // call, the choice of tiles and splits, and the launches.
 #include <algorithm>
+#include <math.h>
 
 #include "host_api.hpp"
 #include "moe.h"
@@ -95,12 +96,24 @@ GemmArgs linear_args(const linear_desc* d) {
   return a;
 }
 
-// plan_gemm, with fp32 on the ring tiles. A 64 x 64 tile's K-step takes a quarter of a 128 x 128 one's:
-// small products, and those whose large tiles leave CUs idle.
+// The tile shapes of the linear layer's and the experts' products. The 16-bit ones' rates are plan_gemm's;
+// 64 x 64: NNN. fp32 (of its own, a sixteenth of the 16-bit peak): 104-127 of 154 TFLOP/s at 128 x 128.
+int linear_tiles(DType in, bool gated, TileInfo (&t)[4]) {
+  if (in == DT_F32) {
+    t[0] = {TILE_128x128_RING, 128, 128, 2, 0.85};
+    t[1] = {TILE_64x64, 64, gated ? 128 : 64, 2, 0.70};
+    return 2;
+  }
+  int n = 0;
+  for (const TileInfo& i : kTiles)
+    if (i.t == TILE_256x256_W8 || i.t == TILE_256x128_W8 || i.t == TILE_128x128) t[n++] = i;
+  t[n++] = {TILE_64x64, 64, gated ? 128 : 64, 2, gated ? 0.26 : 0.20};
+  return n;
+}
+
 Plan plan_linear_gemm(DType in, int64_t M, int64_t N, int64_t K, bool allow_split, bool gated) {
-  if (in != DT_F32) return plan_gemm(in, M, N, K, allow_split, gated);
-  const TileInfo tiles[] = {{TILE_128x128_RING, 128, 128, 2, 0.85}, {TILE_64x64_RING, 64, gated ? 128 : 64, 2, 0.70}};
-  return plan_tiles(tiles, 2, in, M, N, K, allow_split, gated);
+  TileInfo t[4];
+  return plan_tiles(t, linear_tiles(in, gated, t), in, M, N, K, allow_split, gated);
 }
 
 // Forward with one weight: the fused product, or split along K into fp32 partials that
@@ -122,34 +135,73 @@ LinearFwd plan_linear(const linear_desc* d) {
   return f;
 }
 
-// The experts' forward: tiles for many rows an expert, the streaming kernel for few.
+// The experts' products: the streaming kernel for a few rows an expert, else tiles.
 enum ExpertForm { EXPERT_SKINNY, EXPERT_TILES };
 struct ExpertPlan {
   ExpertForm form;
   TileShape tile;
   int bm, bn;
+  double est;            // seconds
+  // backward: parts of dx's K, rows of a weight gradient's piece (0: whole experts) and the partial sums'
+  // slots that those take at most
+  int dx_splits, piece_rows, max_slots;
+  bool dw_first;
 };
+
 // Row tiles of bm rows that M rows of E experts (and the rows behind them) take at most.
 int64_t row_tiles(int64_t M, int64_t E, int64_t bm) { return M / bm + std::min(M, E) + 1; }
 
+// The tile by plan_gemm's time model, every expert ending in half a row tile on average: forward
+// [M, K] -> [M, N], or backward both products ([M, P] -> [M, K], and K over the expert's rows).
 ExpertPlan plan_experts(const linear_desc* d, bool fwd) {
   const DType io = dtype_of(d->dtype);
-  const int64_t M = d->M, E = std::max(d->experts, 1), N = fwd ? d->N : d->K;
   const bool gated = is_gated(d->act);
-  if (io == DT_F32) {
-    // 128 x 128 tiles that leave CUs idle: smaller ones (a K-step of theirs takes a quarter as long)
-    const int64_t tn = (N + (fwd && gated ? 63 : 127)) / (fwd && gated ? 64 : 128);
-    if (row_tiles(M, E, 128) * tn < 512) return {EXPERT_TILES, TILE_64x64_RING, 64, fwd && gated ? 128 : 64};
-    return {EXPERT_TILES, TILE_128x128_RING, 128, 128};
+  const int64_t M = d->M, E = std::max(d->experts, 1), P = gated ? 2 * d->N : d->N;
+  if (fwd && io != DT_F32 && M <= kExpertFewRows * E) return {EXPERT_SKINNY, TILE_128x128, 128, 128, 0.0, 1, 0, 0, false};
+  TileInfo t[4];
+  const int n = linear_tiles(io, fwd && gated, t), bk = bk_of(io);
+  const double per_cu = (io == DT_F32 ? 1.0 / 16.0 : 1.0) * 9.83e12;
+  ExpertPlan best{EXPERT_TILES, TILE_COUNT, 0, 0, 1e300, 1, 0, 0, false};
+  for (int i = 0; i < n; ++i) {
+    if (t[i].t == TILE_256x128_W8) continue;
+    const double step = t[i].slots * 2.0 * t[i].bm * t[i].bn * bk / (t[i].eff * per_cu);   // `slots` tiles' K-step
+    const int64_t bnc = fwd && gated ? t[i].bn / 2 : t[i].bn, slots = 256 * t[i].slots;
+    const int64_t rt = M / t[i].bm + (std::min(M, E) + 1) / 2;
+    const int64_t kx = ((fwd ? d->K : P) + bk - 1) / bk;
+    const int64_t tx = std::max<int64_t>(1, rt) * (((fwd ? d->N : d->K) + bnc - 1) / bnc);
+    ExpertPlan p{EXPERT_TILES, t[i].t, t[i].bm, t[i].bn, 0.0, 1, 0, 0, false};
+    if (fwd) {   // prologue and epilogue: about two K-steps
+      p.est = std::max<int64_t>(1, (tx + slots - 1) / slots) * (kx + 2) * step;
+    } else {
+      const int64_t tw = (P + t[i].bm - 1) / t[i].bm * ((d->K + t[i].bn - 1) / t[i].bn);   // tiles an expert
+      const int64_t kw = (M / E + bk - 1) / bk;
+      const double work = ((double)tx * (kx + 2) + (double)E * tw * (kw + 2)) / slots;   // K-steps a slot
+      // dx in parts while a part is longer than half of what a slot has to do, and takes 8 K-steps
+      while (p.dx_splits < 16 && kx / p.dx_splits > std::max(8.0, work) && kx / (p.dx_splits + 1) >= 8) ++p.dx_splits;
+      // weight gradients over pieces of the rows: with few tiles of half a slot's work, else of all of it
+      // (an expert that most rows go to); at least 8 K-steps
+      const int64_t piece = (int64_t)std::max(8.0, E * tw < 2 * slots ? work / 2 : work) * bk;
+      int64_t kd = std::min<int64_t>((M + bk - 1) / bk, E == 1 ? (M + bk - 1) / bk : 2 * kw);   // longest tile expected
+      if (M >= piece + piece / 2) {
+        p.piece_rows = (int)piece;
+        p.max_slots = (int)std::min<int64_t>(2 * (M / piece) + 1, (int64_t)1 << 30);
+        kd = std::min(kd, piece / bk);
+      }
+      const double longest = std::max((double)kx / p.dx_splits, (double)kd) + 2;
+      p.dw_first = kd > kx / p.dx_splits;
+      p.est = std::max(longest, work + longest / 4) * step;
+      if (p.dx_splits > 1) p.est += ((double)p.dx_splits * 2 + 1) * (double)M * (double)d->K * 4.0 / 6.0e12;
+      if (p.dx_splits > 1 || p.piece_rows) p.est += 4e-6;
+    }
+    if (p.est < best.est * 0.98) best = p;
   }
-  if (fwd && M <= kExpertFewRows * E) return {EXPERT_SKINNY, TILE_128x128, 128, 128};
-  if (M < 256 * E) return {EXPERT_TILES, TILE_128x128, 128, 128};
-  return {EXPERT_TILES, TILE_256x256_W8, 256, 256};
+  return best;
 }
 
 // The backward's launches.
 struct LinearBwd {
-  bool group;          // dx and dW in one launch (one weight, 16-bit)
+  bool small;          // dx, dW and the bias gradient in one launch, as one expert's
+  bool group;          // dx and dW in one launch of 8-wave 256 x 256 tiles (16-bit)
   Plan gdx, gdw;
   RowsPlan dx;
   Plan dw;
@@ -161,7 +213,11 @@ LinearBwd plan_linear_bwd(const linear_desc* d, bool dx, bool dw) {
   if (io == DT_F32) b.dx.main = plan_linear_gemm(io, d->M, d->K, P, true, false);
   else b.dx = plan_rows(io, d->M, d->K, P);
   b.dw = plan_linear_gemm(io, P, d->K, d->M, true, false);
-  if (!dx || !dw || io == DT_F32) return b;
+  // each launch counts for 4 us: small products take fewer
+  const double apart = (dx ? (b.dx.m1 ? b.dx.main.est + b.dx.tail.est : b.dx.main.est) + 4e-6 : 0.0) +
+                       (dw ? b.dw.est + 4e-6 : 0.0);
+  b.small = dx && dw && plan_experts(d, false).est + 4e-6 < 0.97 * apart;
+  if (b.small || !dx || !dw || io == DT_F32) return b;
   b.gdx = plan_gemm(io, d->M, d->K, P, false, false, TILE_256x256_W8);
   b.gdw = plan_gemm(io, P, d->K, d->M, false, false, TILE_256x256_W8);
   const int64_t tiles[2] = {b.gdx.grid, b.gdw.grid}, steps[2] = {(P + 63) / 64, (d->M + 63) / 64};
@@ -170,11 +226,11 @@ LinearBwd plan_linear_bwd(const linear_desc* d, bool dx, bool dw) {
   if (tiles[0] > 32 * 256 || tiles[1] > 32 * 256) return b;   // many rounds: nothing to fill
   const TileInfo& w8 = kTiles[0];
   const double t_group = list_makespan(t2, s2, 2, 1.0) * (2.0 * w8.bm * w8.bn * 64 / (w8.eff * 9.83e12));
-  b.group = t_group < 0.97 * ((b.dx.m1 ? b.dx.main.est + b.dx.tail.est : b.dx.main.est) + b.dw.est);
+  b.group = t_group + 4e-6 < 0.97 * apart;
   return b;
 }
 
-struct LinearWs { size_t dz, sums, partial, total; };
+struct LinearWs { size_t dz, sums, partial, part_w, total; };
 LinearWs linear_ws(const linear_desc* d, int phase) {
   LinearWs w{};
   const int64_t P = is_gated(d->act) ? 2 * d->N : d->N, E = std::max(d->experts, 1);
@@ -186,10 +242,12 @@ LinearWs linear_ws(const linear_desc* d, int phase) {
   } else {
     take(w.dz, d->act == LINEAR_ACT_NONE ? 0 : (size_t)d->M * P * esize(d->dtype));
     take(w.sums, (size_t)dact_pieces(d->M, d->N, E) * P * sizeof(float));
-    if (d->experts == 0 && d->M > 0) {
-      const LinearBwd b = plan_linear_bwd(d, false, false);
-      take(w.partial, std::max(partial_bytes(b.dx, d->M, d->K), partial_bytes(b.dw, P, d->K)));
-    }
+    const LinearBwd b = d->experts || d->M == 0 ? LinearBwd{} : plan_linear_bwd(d, true, true);
+    const ExpertPlan p = plan_experts(d, false);
+    const bool one = d->experts || b.small;
+    take(w.partial, std::max({d->experts || d->M == 0 ? 0 : std::max(partial_bytes(b.dx, d->M, d->K), partial_bytes(b.dw, P, d->K)),
+                              one && p.dx_splits > 1 ? (size_t)p.dx_splits * d->M * d->K * sizeof(float) : 0}));
+    take(w.part_w, one ? (size_t)p.max_slots * P * d->K * sizeof(float) : 0);
   }
   w.total = std::max<size_t>(at, kAlign);
   return w;
@@ -447,9 +505,14 @@ mlp_status linear_bwd(const linear_desc* d, const void* dy, const void* x, const
   if ((need_dz || dbias) && M > 0)
     MLP_TRY(hip_status(run_linear_dact(io, gated, linear_args(d).act, dy, preact, offsets, (int)E, M, N, dz,
                                        dbias ? sums : nullptr, s), "activation gradient"));
-  if (dbias)
-    MLP_TRY(hip_status(run_linear_dbias(io, gated, sums, offsets, (int)E, M, N, dbias, dbias_up, grad_accum, s),
-                       "bias gradient"));
+  BiasGrad db{};
+  if (dbias) {
+    db = {sums, offsets, (int)E, (int)M, (int)N, dact_rows(M, N), (int)dact_pieces(M, N, E), grad_accum, dbias, dbias_up, 0};
+    db.grid = (int)(E * ((P + 15) / 16));
+  }
+  const LinearBwd b = d->experts || M == 0 ? LinearBwd{} : plan_linear_bwd(d, dx != nullptr, dw != nullptr);
+  const bool one = d->experts || M == 0 || b.small;   // (one weight without rows: as one expert without rows)
+  if (dbias && (!one || (!dx && !dw))) MLP_TRY(hip_status(run_linear_dbias(io, db, s), "bias gradient"));
   if (!dx && !dw) return MLP_OK;
 
   GemmArgs gx = linear_args(d);   // dx = dz [W; W_up]
@@ -472,27 +535,41 @@ mlp_status linear_bwd(const linear_desc* d, const void* dy, const void* x, const
   gw.ldc0 = K;
   gw.accumulate = grad_accum;
 
-  if (d->experts || M == 0) {   // (one weight without rows: as one expert without rows)
+  if (one) {
     const ExpertPlan p = plan_experts(d, false);
     ExpertBwd b{};
+    b.db = db;
     gx.N = (int)K;
     gx.K = gx.k_per_split = (int)P;
     gx.tiles_n = (int)((K + p.bn - 1) / p.bn);
     gx.group_m = 8;
     b.dx = expert_gemm(d, gx, offsets);
-    if (dx && M > 0) b.dx.grid = (int)((row_tiles(M, E, p.bm) * gx.tiles_n + 7) / 8 * 8);
+    b.dx_splits = dx ? p.dx_splits : 1;
+    b.dx_kps = b.dx_splits > 1 ? (int)((P + b.dx_splits - 1) / b.dx_splits + bk_of(io) - 1) / bk_of(io) * bk_of(io) : (int)P;
+    if (b.dx_splits > 1) b.dx_splits = (int)((P + b.dx_kps - 1) / b.dx_kps);
+    b.part_x = reinterpret_cast<float*>(base + L.partial);
+    if (dx && M > 0) b.dx.grid = (int)((row_tiles(M, E, p.bm) * gx.tiles_n * b.dx_splits + 7) / 8 * 8);
     gw.M = (int)P;
     gw.N = (int)K;
     gw.tiles_m = (int)((P + p.bm - 1) / p.bm);
     gw.tiles_n = (int)((K + p.bn - 1) / p.bn);
     gw.group_m = std::min(gw.tiles_m, 8);
     b.dw = expert_gemm(d, gw, offsets);
-    if (dw) b.dw.grid = (int)(E * gw.tiles_m * gw.tiles_n);
-    if (b.dx.grid + b.dw.grid == 0) return MLP_OK;
-    return hip_status(run_expert_bwd(io, p.tile, b, s), "experts' gradients");
+    if (dw && M > 0) {
+      b.piece_rows = p.piece_rows;
+      b.max_slots = p.max_slots;
+      b.part_w = reinterpret_cast<float*>(base + L.part_w);
+    }
+    if (dw) b.dw.grid = (int)(((b.piece_rows ? M / b.piece_rows : 0) + E) * gw.tiles_m * gw.tiles_n);
+    if (dw && b.dx.grid && p.dw_first) {
+      b.dw_first = 1;
+      if (b.piece_rows) b.dw.grid = (b.dw.grid + 7) / 8 * 8;
+    }
+    if (b.dx.grid + b.dw.grid + b.db.grid == 0) return MLP_OK;
+    MLP_TRY(hip_status(run_expert_bwd(io, p.tile, b, s), "experts' gradients"));
+    return hip_status(run_expert_join(io, b, s), "experts' gradients (join)");
   }
   void* partial = base + L.partial;
-  const LinearBwd b = plan_linear_bwd(d, dx != nullptr, dw != nullptr);
   if (b.group) {
     GemmGroup g{};
     const bool dx_first = P >= M;   // longest K first
@@ -517,6 +594,7 @@ mlp_status linear_bwd(const linear_desc* d, const void* dy, const void* x, const
 namespace gmlp {
 
 hipError_t run_gemm_linear(DType in, int epi, TileShape tile, const GemmArgs& a, int grid, hipStream_t s) {
+  if (tile == TILE_64x64 && in != DT_F32) return run_gemm_small16(in, in, NT, epi, a, grid, s);
   switch (in) {
     case DT_BF16: return run_gemm_bf16_linear(epi, tile, a, grid, s);
     case DT_F16: return run_gemm_f16_linear(epi, tile, a, grid, s);
