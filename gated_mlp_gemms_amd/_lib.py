@@ -88,6 +88,7 @@ _MOE_SIGNATURES = {
 }
 
 _lib = None
+_bind = None
 
 
 def lib() -> C.CDLL:
@@ -105,6 +106,33 @@ def lib() -> C.CDLL:
             fn.argtypes = args
         _lib = handle
     return _lib
+
+
+# bind.cpp's functions call these, in this order
+_BOUND = ("moe_route", "moe_route_bwd", "moe_sort_workspace_bytes", "moe_sort", "moe_gather", "moe_gather_bwd",
+          "moe_combine", "moe_combine_bwd", "linear_workspace_bytes", "linear_fwd", "linear_bwd")
+
+
+def bind():
+    """The extension that checks tensors and makes moe.h's calls (bind.cpp), tied to the loaded library."""
+    global _bind
+    if _bind is None:
+        import torch
+
+        L = lib()
+        try:
+            from . import _bind as ext
+        except ImportError as e:
+            raise RuntimeError("the _bind extension is missing or does not load: build it with "
+                               "`python -m gated_mlp_gemms_amd.build`") from e
+
+        def workspace(n, device):
+            return torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", device))
+
+        ext.setup(tuple(C.cast(getattr(L, n), C.c_void_p).value for n in _BOUND), MlpError, workspace,
+                  getattr(torch._C, "_cuda_getCurrentRawStream", None))
+        _bind = ext
+    return _bind
 
 
 class MlpError(RuntimeError):

@@ -2,7 +2,8 @@
 
 Usage: ``python -m gated_mlp_gemms_amd.build`` (or ``__graft_entry__.build()``).
 Each source compiles to an object under ``_build/`` in parallel, then one shared library is
-linked next to this file, where the Python binding loads it from.
+linked next to this file, where the Python binding loads it from. ``_bind`` (csrc/bind.cpp, host
+code only) becomes a Python extension next to it.
 """
 from __future__ import annotations
 
@@ -11,12 +12,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgated_mlp.so")
+BIND = os.path.join(PKG, "_bind" + sysconfig.get_config_var("EXT_SUFFIX"))
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
@@ -47,6 +50,23 @@ def _compile(src: str) -> tuple[str, str]:
     return obj, err
 
 
+def _build_bind() -> str:
+    """The Python extension (host code only): csrc/bind.cpp against torch's headers."""
+    import torch
+    from torch.utils.cpp_extension import include_paths, library_paths
+
+    src, tmp = os.path.join(CSRC, "bind.cpp"), BIND + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", os.path.join(ROOT, "include"),
+           "-isystem", sysconfig.get_paths()["include"], *[a for p in include_paths() for a in ("-isystem", p)],
+           src, "-o", tmp, *[a for p in library_paths() for a in ("-L", p)], "-lc10", "-ltorch_cpu", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"compile failed: {' '.join(cmd)}\n{r.stdout}{r.stderr}")
+    shutil.move(tmp, BIND)
+    return BIND
+
+
 def build(jobs: int | None = None, verbose: bool = False) -> str:
     """Compile every HIP source and link the shared library; returns its path."""
     if not os.path.exists(HIPCC):
@@ -54,8 +74,10 @@ def build(jobs: int | None = None, verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = sources()
     jobs = jobs or min(len(srcs), max(1, min(16, os.cpu_count() or 1)))
-    with cf.ThreadPoolExecutor(jobs) as ex:
+    with cf.ThreadPoolExecutor(jobs + 1) as ex:
+        bound = ex.submit(_build_bind)
         results = list(ex.map(_compile, srcs))
+        bound.result()
     for obj, msg in results:
         if verbose and msg.strip():
             print(msg, file=sys.stderr)

@@ -299,3 +299,39 @@ def test_reference_router_gradient_is_a_difference(score, renorm):
 
     h = 1e-6
     assert abs((loss(x + h * v) - loss(x - h * v)) / (2 * h) - (R.route_bwd(x, ids, dw, score, renorm) * v).sum()) < 1e-8
+
+
+# ---- the binding ----------------------------------------------------------------------------------
+
+def test_binding_refuses_what_is_not_a_tensor_or_descriptor():
+    b = _lib.bind()
+    with pytest.raises(TypeError, match="6 arguments expected, not 2"):
+        b.moe_route(t(5, 8), t(5, 2, dtype=I32))
+    with pytest.raises(ValueError, match="weights must be a tensor, not list"):
+        gm.moe_route(t(5, 8), t(5, 2, dtype=I32), [1.0])
+    with pytest.raises(ValueError, match=r"weights must be torch.float32 \[5, 2\], not torch.bfloat16 \[5, 3\]"):
+        gm.moe_route(t(5, 8), t(5, 2, dtype=I32), t(5, 3))
+    with pytest.raises(ValueError, match=r"logits must be contiguous, not of strides \[1, 5\]"):
+        gm.moe_route(t(8, 5).t(), t(5, 2, dtype=I32), t(5, 2, dtype=F32))
+    with pytest.raises(ValueError, match="logits must be on the GPU of the other tensors, not on cpu"):
+        gm.moe_route(t(5, 8), t(5, 2, dtype=I32), t(5, 2, dtype=F32))
+    with pytest.raises(ValueError, match="contiguous"):
+        gm.moe_sort(t(4, 2, dtype=I32).t(), 3, t(4, dtype=I32), t(8, dtype=I32), t(8, dtype=I32))
+    with pytest.raises(ValueError, match="ids must be a tensor"):
+        gm.moe_sort(None, 3, t(4, dtype=I32), t(8, dtype=I32), t(8, dtype=I32))
+    with pytest.raises(TypeError):
+        gm.moe_sort(t(8, dtype=I32), "3", t(4, dtype=I32), t(8, dtype=I32), t(8, dtype=I32))
+    with pytest.raises(ValueError, match="LinearDesc"):
+        gm.linear_fwd(b"x", t(6, 16), t(24, 16), t(6, 24))
+    with pytest.raises(TypeError):
+        gm.linear_fwd(None, t(6, 16), t(24, 16), t(6, 24))
+    with pytest.raises(ValueError, match="x must be contiguous"):
+        gm.linear_fwd(desc(M=6, K=16, N=24, act="none"), t(6, 16).to_sparse(), t(24, 16), t(6, 24))
+
+
+def test_binding_is_required(monkeypatch):
+    monkeypatch.setattr(_lib, "_bind", None)
+    monkeypatch.setitem(__import__("sys").modules, "gated_mlp_gemms_amd._bind", None)
+    monkeypatch.delattr(gm, "_bind", raising=False)
+    with pytest.raises(RuntimeError, match="_bind extension"):
+        gm.moe_route(t(5, 8), t(5, 2, dtype=I32), t(5, 2, dtype=F32))
