@@ -31,49 +31,78 @@ __device__ __forceinline__ void expert_rows(const int* offsets, int experts, int
   n = e <= experts ? end - row0 : 0;
 }
 
+// Inclusive sum over the lanes up to this one: inside 16 lanes by shifted DPP operands, then the last lane of
+// row 0 (and 2) added to the next row, and that of row 1 to the upper half.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);   // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);   // row_bcast:31 into rows 2 and 3
+  return v;
+}
+
+// find_row_piece with C experts a lane: lane l counts experts l C .. l C + C - 1 from C + 1 offsets loaded at once.
+template <int C, int LEAST, typename Want>
+__device__ __forceinline__ bool find_row_piece_of(const int* offsets, int experts, int rows, int step, Want want,
+                                                  RowPiece& out) {
+  const int lane = threadIdx.x & 63, e0 = lane * C;
+  int at[C + 1], pieces[C], sum = 0;
+  if (offsets == nullptr) {   // one expert with every row
+#pragma unroll
+    for (int i = 0; i <= C; ++i) at[i] = e0 + i == 0 ? 0 : rows;
+  } else {
+#pragma unroll
+    for (int i = 0; i <= C; ++i) at[i] = offsets[min(e0 + i, experts)];
+    at[0] = min(max(at[0], 0), rows);
+#pragma unroll
+    for (int i = 1; i <= C; ++i) {   // (whatever the offsets hold: expert_rows)
+      const int from = min(max(at[i], 0), rows);
+      at[i] = e0 + i <= experts ? from : rows;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int n = max(at[i + 1] - at[i], 0);
+    pieces[i] = (n + step - 1) / step;
+    if constexpr (LEAST > 0) pieces[i] = e0 + i < experts ? max(pieces[i], LEAST) : 0;
+    if (e0 + i > experts) pieces[i] = 0;
+    sum += pieces[i];
+  }
+  const int incl = wave_scan(sum);
+  const int k = want(__builtin_amdgcn_readlane(incl, 63));
+  if (k < 0) return false;
+  const uint64_t hit = __ballot(incl > k);
+  if (hit == 0) return false;
+  const int l = __builtin_ctzll(hit);
+  int first = incl - sum, e = e0, row0 = at[0], n = max(at[1] - at[0], 0);   // of the lane's expert that has piece k
+#pragma unroll
+  for (int i = 1; i < C; ++i) {
+    if (first + pieces[i - 1] > k || e != e0 + i - 1) continue;
+    first += pieces[i - 1];
+    e = e0 + i;
+    row0 = at[i];
+    n = max(at[i + 1] - at[i], 0);
+  }
+  out.e = __builtin_amdgcn_readlane(e, l);
+  out.row0 = __builtin_amdgcn_readlane(row0, l);
+  out.rows = __builtin_amdgcn_readlane(n, l);
+  out.first = __builtin_amdgcn_readlane(first, l);
+  out.index = k - out.first;
+  return true;
+}
+
 // Pieces of every expert (the rows behind the last offset included) are numbered in expert order.
-// count(total) -> the number of the piece wanted, or -1. Called by whole waves; every wave of a
+// want(total) -> the number of the piece wanted, or -1. Called by whole waves; every wave of a
 // workgroup gets the same answer, in scalar registers. LEAST: pieces an expert has at least (the rows
-// behind the last offset then have none).
+// behind the last offset then have none). Every tile starts with it, so it is one trip to memory and one scan.
 template <int LEAST = 0, typename Want>
 __device__ __forceinline__ bool find_row_piece(const int* offsets, int experts, int rows, int step, Want want,
                                                RowPiece& out) {
-  const int lane = threadIdx.x & 63;
-  int row0, n, pieces, incl;
-  auto scan = [&](int base) {   // inclusive scan of the pieces of experts base .. base + 63
-    expert_rows(offsets, experts, rows, base + lane, row0, n);
-    pieces = (n + step - 1) / step;
-    if constexpr (LEAST > 0) pieces = base + lane < experts ? max(pieces, LEAST) : 0;
-    incl = pieces;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(incl, o);
-      if (lane >= o) incl += v;
-    }
-  };
-  int total = 0;
-  for (int base = 0; base <= experts; base += 64) {
-    scan(base);
-    total += __builtin_amdgcn_readlane(incl, 63);
-  }
-  const int at = want(total);
-  if (at < 0) return false;
-  int before = 0;
-  for (int base = 0; base <= experts; base += 64) {
-    if (experts >= 64) scan(base);   // else the one scan above is this one
-    const uint64_t hit = __ballot(before + incl > at);
-    if (hit != 0) {
-      const int l = __builtin_ctzll(hit);
-      out.e = base + l;
-      out.row0 = __builtin_amdgcn_readlane(row0, l);
-      out.rows = __builtin_amdgcn_readlane(n, l);
-      out.first = before + __builtin_amdgcn_readlane(incl, l) - __builtin_amdgcn_readlane(pieces, l);
-      out.index = at - out.first;
-      return true;
-    }
-    before += __builtin_amdgcn_readlane(incl, 63);
-  }
-  return false;
+  if (experts < 64) return find_row_piece_of<1, LEAST>(offsets, experts, rows, step, want, out);
+  if (experts < 256) return find_row_piece_of<4, LEAST>(offsets, experts, rows, step, want, out);
+  return find_row_piece_of<17, LEAST>(offsets, experts, rows, step, want, out);
 }
 
 template <typename T> __device__ __forceinline__ const void* shift(const void* p, int64_t elems) {

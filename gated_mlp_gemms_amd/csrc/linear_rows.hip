@@ -138,11 +138,16 @@ __global__ __launch_bounds__(kThr) void linear_dbias_kernel(const BiasGrad a) {
 }
 
 // The experts' partial sums joined (ExpertBwd): workgroups [0, dx_blocks) add up dx's parts (zeros behind the
-// last offset), kJoinBlocks an expert after them the pieces of the weight gradients that have several.
-constexpr int kJoinBlocks = 64;
+// last offset), dw_blocks an expert after them the pieces of the weight gradients that have several. About 4 pieces of
+// 4 columns a thread, fewer for many experts (of which few have pieces): a weight gradient of 4864 x 2048 f16 from
+// 2 pieces, 95 us with 64 workgroups.
+inline int join_blocks(int64_t elems, int experts) {
+  const int64_t want = (elems / 4 + 4 * kThr - 1) / (4 * kThr);
+  return (int)std::min<int64_t>(want, std::max(16, 4096 / experts));
+}
 
 template <typename T, typename GT>
-__global__ __launch_bounds__(kThr) void expert_join_kernel(const ExpertBwd a, int dx_blocks) {
+__global__ __launch_bounds__(kThr) void expert_join_kernel(const ExpertBwd a, int dx_blocks, int dw_blocks) {
   const int b = blockIdx.x;
   auto add = [](const float* src, int64_t plane, int count) {
     f32x4 s = *reinterpret_cast<const f32x4*>(src);
@@ -163,7 +168,7 @@ __global__ __launch_bounds__(kThr) void expert_join_kernel(const ExpertBwd a, in
     return;
   }
   const ExpertGemm& g = a.dw;
-  const int e = (b - dx_blocks) / kJoinBlocks, part = (b - dx_blocks) % kJoinBlocks;
+  const int e = (b - dx_blocks) / dw_blocks, part = (b - dx_blocks) % dw_blocks;
   int row0, n;
   expert_rows(g.offsets, g.experts, g.rows, e, row0, n);
   if (n <= a.piece_rows) return;
@@ -172,7 +177,7 @@ __global__ __launch_bounds__(kThr) void expert_join_kernel(const ExpertBwd a, in
   if (slot + count > a.max_slots) return;   // offsets may be anything
   const int64_t plane = (int64_t)g.g.M * g.g.N, total = plane / 4;
   const float* src = a.part_w + slot * plane;
-  for (int64_t i = part * (int64_t)kThr + threadIdx.x; i < total; i += kJoinBlocks * kThr) {
+  for (int64_t i = part * (int64_t)kThr + threadIdx.x; i < total; i += (int64_t)dw_blocks * kThr) {
     const int64_t at = i * 4, m = at / g.g.N, col = at - m * g.g.N;
     const f32x4 s = add(src + at, plane, count);
     float v[4] = {s[0], s[1], s[2], s[3]};
@@ -230,12 +235,13 @@ hipError_t run_linear_dbias(DType io, const BiasGrad& a, hipStream_t s) {
 hipError_t run_expert_join(DType io, const ExpertBwd& a, hipStream_t s) {
   const int64_t items = a.dx_splits > 1 ? (int64_t)a.dx.rows * a.dx.g.N / 4 : 0;
   const int dx_blocks = (int)std::min<int64_t>((items + kThr - 1) / kThr, 256 * 16);
-  const int blocks = dx_blocks + (a.piece_rows ? a.dw.experts * kJoinBlocks : 0);
+  const int dw_blocks = a.piece_rows ? join_blocks((int64_t)a.dw.g.M * a.dw.g.N, a.dw.experts) : 0;
+  const int blocks = dx_blocks + a.dw.experts * dw_blocks;
   if (blocks == 0) return hipSuccess;
   return by_type(io, a.dw.g.accumulate, [&](auto v, auto acc) {
     using T = decltype(v);
     using GT = typename std::conditional<decltype(acc)::value, float, T>::type;
-    hipLaunchKernelGGL((expert_join_kernel<T, GT>), dim3(blocks), dim3(kThr), 0, s, a, dx_blocks);
+    hipLaunchKernelGGL((expert_join_kernel<T, GT>), dim3(blocks), dim3(kThr), 0, s, a, dx_blocks, dw_blocks);
     return hipGetLastError();
   });
 }

@@ -111,9 +111,61 @@ int linear_tiles(DType in, bool gated, TileInfo (&t)[4]) {
   return n;
 }
 
+// Seconds of a K-step (64 deep, fp32 32) of a tile with few workgroups on the chip, with one on each of the 256
+// CUs, and with every slot taken (all of a CU's slots together), and of what a tile does besides: its first
+// loads and its epilogue. Measured with forced tiles (us): 2000^3 128 x 128 (one a CU) 26.3, 256 x 128 (128 tiles) 33.6,
+// 64 x 64 (two rounds) 38.8; 2000 x 512 x 4096 gated 24.1 / 30.9 / 30.1 / 37.2 (256 x 256, 256 x 128, 128 x 128, 64 x 128);
+// 1000 x 4096 x 512 73 / 47 / 38 / 22.
+struct StepTime { double few, one, full, rest; };
+StepTime step_time(TileShape t, DType in, bool gated) {
+  if (in == DT_F32) return t == TILE_64x64 ? (gated ? StepTime{1.0e-6, 1.2e-6, 2.1e-6, 2e-6} : StepTime{0.55e-6, 0.65e-6, 1.1e-6, 2e-6})
+                                           : StepTime{2.2e-6, 2.3e-6, 4.3e-6, 3e-6};
+  switch (t) {
+    case TILE_256x256_W8: return {1.05e-6, 1.95e-6, 1.95e-6, 4e-6};
+    case TILE_256x128_W8: return {0.66e-6, 1.07e-6, 1.07e-6, 3.5e-6};
+    case TILE_128x128: return {0.50e-6, 0.65e-6, 1.20e-6, 2.5e-6};
+    default: return gated ? StepTime{0.33e-6, 0.55e-6, 0.77e-6, 1.5e-6} : StepTime{0.25e-6, 0.40e-6, 0.52e-6, 1.5e-6};
+  }
+}
+
+// Seconds of `tiles` tiles of `steps` K-steps each.
+double tiles_time(const StepTime& st, int64_t slots, int64_t tiles, int64_t steps) {
+  const int64_t round = 256 * slots, last = tiles % round;
+  double t = (double)(tiles / round) * (st.full * (double)steps + st.rest);
+  if (last > 0) {
+    const double step = last <= 256 ? st.few + (st.one - st.few) * (double)last / 256.0
+                                    : st.one + (st.full - st.one) * (double)(last - 256) / (double)(round - 256);
+    t += step * (double)steps + st.rest;
+  }
+  return t;
+}
+
 Plan plan_linear_gemm(DType in, int64_t M, int64_t N, int64_t K, bool allow_split, bool gated) {
   TileInfo t[4];
-  return plan_tiles(t, linear_tiles(in, gated, t), in, M, N, K, allow_split, gated);
+  const int n = linear_tiles(in, gated, t), bk = bk_of(in);
+  Plan best{};
+  best.est = 1e300;
+  for (int i = 0; i < n; ++i) {
+    const StepTime st = step_time(t[i].t, in, gated);
+    const int64_t units = gated ? t[i].bn / 2 : t[i].bn;
+    const int64_t tm = (M + t[i].bm - 1) / t[i].bm, tn = (N + units - 1) / units;
+    for (int s = 1; s <= (allow_split ? 16 : 1); ++s) {
+      const int64_t kps = ((K + s - 1) / s + bk - 1) / bk * bk;
+      if ((K + kps - 1) / kps != s) continue;
+      double est = tiles_time(st, t[i].slots, tm * tn * s, kps / bk);
+      if (s > 1) est += (2.0 * s * M * N * 4.0 + M * N * 4.0) / 6.0e12 + 4e-6;   // partial sums there and back, a launch
+      if (est >= best.est * 0.98) continue;
+      best.est = est;
+      best.tile = t[i].t;
+      best.splits = s;
+      best.k_per_split = (int)kps;
+      best.tiles_m = (int)tm;
+      best.tiles_n = (int)tn;
+      best.group_m = tn == 3 ? 1 : (int)std::min<int64_t>(tm, 8);   // as plan_tiles
+      best.grid = (int)(tm * tn * s);
+    }
+  }
+  return best;
 }
 
 // Forward with one weight: the fused product, or split along K into fp32 partials that
@@ -151,7 +203,7 @@ struct ExpertPlan {
 // Row tiles of bm rows that M rows of E experts (and the rows behind them) take at most.
 int64_t row_tiles(int64_t M, int64_t E, int64_t bm) { return M / bm + std::min(M, E) + 1; }
 
-// The tile by plan_gemm's time model, every expert ending in half a row tile on average: forward
+// The tile by the time model of step_time, every expert ending in half a row tile on average: forward
 // [M, K] -> [M, N], or backward both products ([M, P] -> [M, K], and K over the expert's rows).
 ExpertPlan plan_experts(const linear_desc* d, bool fwd) {
   const DType io = dtype_of(d->dtype);
@@ -160,18 +212,17 @@ ExpertPlan plan_experts(const linear_desc* d, bool fwd) {
   if (fwd && io != DT_F32 && M <= kExpertFewRows * E) return {EXPERT_SKINNY, TILE_128x128, 128, 128, 0.0, 1, 0, 0, false};
   TileInfo t[4];
   const int n = linear_tiles(io, fwd && gated, t), bk = bk_of(io);
-  const double per_cu = (io == DT_F32 ? 1.0 / 16.0 : 1.0) * 9.83e12;
   ExpertPlan best{EXPERT_TILES, TILE_COUNT, 0, 0, 1e300, 1, 0, 0, false};
   for (int i = 0; i < n; ++i) {
     if (t[i].t == TILE_256x128_W8) continue;
-    const double step = t[i].slots * 2.0 * t[i].bm * t[i].bn * bk / (t[i].eff * per_cu);   // `slots` tiles' K-step
+    const StepTime st = step_time(t[i].t, io, fwd && gated);
     const int64_t bnc = fwd && gated ? t[i].bn / 2 : t[i].bn, slots = 256 * t[i].slots;
-    const int64_t rt = M / t[i].bm + (std::min(M, E) + 1) / 2;
+    const int64_t rt = std::max<int64_t>(1, M / t[i].bm + (std::min(M, E) + 1) / 2);
     const int64_t kx = ((fwd ? d->K : P) + bk - 1) / bk;
-    const int64_t tx = std::max<int64_t>(1, rt) * (((fwd ? d->N : d->K) + bnc - 1) / bnc);
+    const int64_t tx = rt * (((fwd ? d->N : d->K) + bnc - 1) / bnc);
     ExpertPlan p{EXPERT_TILES, t[i].t, t[i].bm, t[i].bn, 0.0, 1, 0, 0, false};
-    if (fwd) {   // prologue and epilogue: about two K-steps
-      p.est = std::max<int64_t>(1, (tx + slots - 1) / slots) * (kx + 2) * step;
+    if (fwd) {
+      p.est = tiles_time(st, t[i].slots, tx, kx);
     } else {
       const int64_t tw = (P + t[i].bm - 1) / t[i].bm * ((d->K + t[i].bn - 1) / t[i].bn);   // tiles an expert
       const int64_t kw = (M / E + bk - 1) / bk;
@@ -187,10 +238,16 @@ ExpertPlan plan_experts(const linear_desc* d, bool fwd) {
         p.max_slots = (int)std::min<int64_t>(2 * (M / piece) + 1, (int64_t)1 << 30);
         kd = std::min(kd, piece / bk);
       }
-      const double longest = std::max((double)kx / p.dx_splits, (double)kd) + 2;
       p.dw_first = kd > kx / p.dx_splits;
-      p.est = std::max(longest, work + longest / 4) * step;
+      // seconds: what a slot does in all, and the longest tile
+      const double items = (double)tx * p.dx_splits + (double)E * tw;
+      const double busy = std::min(1.0, items / slots), step = items <= 256.0 ? st.few + (st.one - st.few) * items / 256.0
+                                                                            : st.one + (st.full - st.one) * busy;
+      const double all = (((double)tx * kx + (double)E * tw * kw) * step + items * st.rest) / slots;
+      const double longest = (double)std::max<int64_t>(kx / p.dx_splits, kd) * step + st.rest;
+      p.est = std::max(longest, all + longest / 4);
       if (p.dx_splits > 1) p.est += ((double)p.dx_splits * 2 + 1) * (double)M * (double)d->K * 4.0 / 6.0e12;
+      if (p.piece_rows && E == 1) p.est += ((double)(M / piece + 1) * 2 + 1) * (double)P * (double)d->K * 4.0 / 6.0e12;
       if (p.dx_splits > 1 || p.piece_rows) p.est += 4e-6;
     }
     if (p.est < best.est * 0.98) best = p;
