@@ -100,6 +100,13 @@ __device__ __forceinline__ void epi_row8(const GemmArgs& p, int m, int n, int sp
       }
       Vec8<float>::store(q, o);
     } else {
+      if constexpr (EPI == EPI_STORE_PART && ElemTraits<IoT>::bytes == 2) {
+        if (p.flags & kFlagStream) {   // (uniform)
+          const u32x4 q = {pack16x2<IoT>(v[0], v[1]), pack16x2<IoT>(v[2], v[3]), pack16x2<IoT>(v[4], v[5]), pack16x2<IoT>(v[6], v[7])};
+          __builtin_nontemporal_store(q, reinterpret_cast<u32x4*>(elem_ptr<IoT>(base, row, p.ldc0, n)));
+          return;
+        }
+      }
       Vec8<IoT>::store(elem_ptr<IoT>(base, row, p.ldc0, n), v);
     }
   } else if constexpr (EPI == EPI_PARTIAL) {
@@ -230,12 +237,13 @@ __device__ __forceinline__ void epi_row16(const GemmArgs& p, int m, int n, const
 template <int WAVES> constexpr int epilogue_rows_per_round() { return WAVES == 8 ? 16 : 32; }
 
 // Bytes of LDS the row-staged epilogue uses (waves x rows per round x padded WN fp32 columns).
-template <int BN, int WAVES, int WGN = 2>
-constexpr int epilogue_lds_bytes() { return WAVES * epilogue_rows_per_round<WAVES>() * ((BN / WGN) * 4 + 16); }
+template <int BN, int WAVES, int WGN = 2, int RR = epilogue_rows_per_round<WAVES>()>   // RR: rows staged per round
+constexpr int epilogue_lds_bytes() { return WAVES * RR * ((BN / WGN) * 4 + 16); }
 
 // acc[i][j]: the MFMA layout of the wave's WM x WN tile (see epilogue()). lds: this
-// workgroup's LDS, at least epilogue_lds_bytes<BN>() bytes, not in use by any wave.
-template <int EPI, typename IoT, int BM, int BN, int MI, int NI, int WAVES, int WGN, typename AccV>
+// workgroup's LDS, at least epilogue_lds_bytes<BN>() bytes (RR rows a wave), not in use by any wave.
+template <int EPI, typename IoT, int BM, int BN, int MI, int NI, int WAVES, int WGN, int RR = epilogue_rows_per_round<WAVES>(),
+          typename AccV>
 __device__ __forceinline__ void epilogue_rows(const GemmArgs& p, AccV (&acc)[MI][NI], int m0, int n0,
                                               int split, int wm, int wn, int lane, int wave, char* lds) {
   constexpr bool GATED = epi_gated(EPI);
@@ -244,7 +252,6 @@ __device__ __forceinline__ void epilogue_rows(const GemmArgs& p, AccV (&acc)[MI]
   constexpr bool B16 = sizeof(AccV) == 4 * sizeof(float);
   constexpr int BLK = B16 ? 16 : 32;
   constexpr int WM = BM / (WAVES / WGN), WN = BN / WGN;
-  constexpr int RR = epilogue_rows_per_round<WAVES>();   // rows staged per round
   constexpr int STRIDE = WN * 4 + 16;                 // padded: rows 16 bytes apart in bank space
   constexpr int UNITS = GATED ? WN / 2 : WN;          // output columns of the wave
   // columns per lane: 16 for the quantizing epilogues (16-byte code stores), else 8

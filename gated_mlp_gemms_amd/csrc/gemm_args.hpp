@@ -60,6 +60,7 @@ struct GemmArgs {
 // weight gradients w_stride, bias_stride and w_stride elements apart. The members' pointers are those
 // of expert 0 and row 0; M (products over rows) or K (weight gradients) is set per expert on the
 // device. tiles_m of a product over rows is unused.
+constexpr int kFlagStream = 4;   // in g.flags: an output that no cache holds until it is read is stored past the caches
 struct ExpertGemm {
   GemmArgs g;
   const int* offsets;
@@ -83,12 +84,15 @@ struct BiasGrad {
 //  * piece_rows: an expert of more rows has its weight gradient summed over pieces of that many, fp32 sums in
 //    part_w [slots][M][N], slots counted over such experts in order, max_slots at most (0: never).
 // run_expert_join adds up either.
+//  * strip_parts > 0: few rows an expert. dx in 64 x 128 tiles; the weight gradients 64 columns of x a workgroup, every
+//    strip_parts-th of the 128-row tiles along dz's columns one after another (expert_grad_strip).
 struct ExpertBwd {
   ExpertGemm dx, dw;
   BiasGrad db;
   int dw_first;
   int dx_splits, dx_kps; float* part_x;
   int piece_rows, max_slots; float* part_w;
+  int strip_parts;
 };
 
 // Up to kGroupMax independent GEMMs run by one launch (gemm_dma_group_kernel): member j covers

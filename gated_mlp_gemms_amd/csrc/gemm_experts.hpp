@@ -230,12 +230,12 @@ __device__ __forceinline__ int expert_slots_before(const int* offsets, int exper
   return __builtin_amdgcn_readfirstlane(slots);
 }
 
-// Tile b of the weight gradients dW_e = dz^T x over expert e's rows, or over a piece of them.
-template <typename T, typename GT, int BM, int BN, int WAVES>
-__device__ __forceinline__ void expert_grad_tile(const ExpertBwd& all, int b, char* smem) {
+// The share of workgroup b of the weight gradients dW_e = dz^T x over expert e's rows, or over a piece of them,
+// `tiles` shares a piece: the product in p and the share's number, or -1.
+template <typename T, typename GT>
+__device__ __forceinline__ int expert_grad_share(const ExpertBwd& all, int b, int tiles, GemmArgs& p) {
   const ExpertGemm& a = all.dw;
-  GemmArgs p = a.g;
-  const int tiles = p.tiles_m * p.tiles_n;
+  p = a.g;
   int e, row0, n, item;
   if (all.piece_rows) {
     RowPiece t;
@@ -246,31 +246,154 @@ __device__ __forceinline__ void expert_grad_tile(const ExpertBwd& all, int b, ch
       tile = xcd_remap(b, count);
       return tile / tiles;
     }, t);
-    if (!found) return;
+    if (!found) return -1;
     e = t.e;
     row0 = t.row0 + t.index * all.piece_rows;
     n = min(t.rows - t.index * all.piece_rows, all.piece_rows);
     item = tile - (t.first + t.index) * tiles;
     if (t.rows > all.piece_rows) {
       const int slot = expert_slots_before(a.offsets, a.experts, a.rows, all.piece_rows, e) + t.index;
-      if (slot >= all.max_slots) return;   // offsets may be anything
+      if (slot >= all.max_slots) return -1;   // offsets may be anything
       p.partial = all.part_w + (int64_t)slot * p.M * p.N;
     }
   } else {
     b = xcd_remap(b, a.grid);
     e = b / tiles;
+    if (e >= a.experts) return -1;
     item = b - e * tiles;
     expert_rows(a.offsets, a.experts, a.rows, e, row0, n);
     row0 = __builtin_amdgcn_readfirstlane(row0);
     n = __builtin_amdgcn_readfirstlane(n);
   }
-  if (n == 0 && p.accumulate) return;
+  if (n == 0 && p.accumulate) return -1;
   p.K = p.k_per_split = n;
   p.A = shift<T>(p.A, row0 * p.lda);
   p.B0 = shift<T>(p.B0, row0 * p.ldb);
   p.C0 = shift<GT>(p.C0, e * a.w_stride);
   p.C1 = shift<GT>(p.C1, e * a.w_stride);
+  return item;
+}
+
+template <typename T, typename GT, int BM, int BN, int WAVES>
+__device__ __forceinline__ void expert_grad_tile(const ExpertBwd& all, int b, char* smem) {
+  GemmArgs p;
+  const int item = expert_grad_share<T, GT>(all, b, all.dw.g.tiles_m * all.dw.g.tiles_n, p);
+  if (item < 0) return;
   gemm_dma_tile<T, GT, BM, BN, false, false, EPI_STORE_PART, WAVES, true>(p, item, smem);
+}
+
+// Weight gradients over few rows: a tile is one or two K-steps, so as workgroups of their own tiles are mostly
+// latency (finding the rows, the first loads, the last stores: 10 us for a pair of 128 x 128 tiles of 57 rows each,
+// 1.7 TB/s of gradient written). Here a workgroup keeps a strip of 128 columns of x and walks the 64-column tiles
+// of dz, the DMAs two steps ahead across tiles, through a ring of three stages (24 KB each; two workgroups a CU); a
+// tile's stores stay in flight over the next steps.
+constexpr int kStripM = kStripTileM, kStripN = kStripTileN, kStripStages = 3;
+template <typename T> constexpr int strip_lds_bytes() { return kStripStages * (kStripM + kStripN) * StepGeo<T>::ROWB; }
+
+template <typename T, typename GT>
+__device__ __forceinline__ void expert_grad_strip(const ExpertBwd& all, int b, char* smem) {
+  constexpr int ES = 2, WAVES = 4, WM = kStripM / 2, WN = kStripN / 2, MI = WM / 32, NI = WN / 32;
+  constexpr int KC = Mma<T>::kChunks, KMMA = 16;
+  using DA = MNTileDma<kStripM, WAVES, false>;
+  using DB = MNTileDma<kStripN, WAVES, false>;
+  constexpr int BK = DA::KROWS, NSUB = BK / KMMA, N_DMA = DA::kInst + DB::kInst;
+  constexpr int A_BYTES = kStripM * StepGeo<T>::ROWB, STAGE = (kStripM + kStripN) * StepGeo<T>::ROWB;
+  static_assert(DB::KROWS == BK && BK * kStripM * ES == A_BYTES, "stage geometry");
+  constexpr int RR = 16;   // rows of the epilogue's staging: it has one stage
+  static_assert(epilogue_lds_bytes<kStripN, WAVES, 2, RR>() <= STAGE, "epilogue staging");
+  // a whole tile's stores a wave makes (16 bytes a lane), which may be in flight when the next step is waited for
+  constexpr int STORES = WM * WN * (int)sizeof(GT) / 1024;
+
+  GemmArgs p;
+  const int parts = all.strip_parts;
+  const int share = expert_grad_share<T, GT>(all, b, all.dw.g.tiles_n * parts, p);
+  if (share < 0) return;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / 2, wn = wave % 2;
+  const int n0 = share / parts * kStripN, part = share % parts;
+  const int count = (p.tiles_m - part + parts - 1) / parts;   // tiles of this workgroup
+  const int nk = (p.K + BK - 1) / BK, steps = count * nk;
+  const int64_t lda = (int64_t)p.lda * ES, ldb = (int64_t)p.ldb * ES;
+
+  DA na;
+  DB nb;
+  nb.init(wave, lane, reinterpret_cast<const char*>(elem_ptr<T>(p.B0, 0, p.ldb, n0)), ldb, 0, p.N - n0);
+  int itile = 0, ik = 0;   // the next step to load
+  auto issue = [&](char* stage) {
+    if (ik == 0) {
+      const int m0 = (part + itile * parts) * kStripM;
+      na.init(wave, lane, reinterpret_cast<const char*>(elem_ptr<T>(p.A, 0, p.lda, m0)), lda, 0, p.M - m0);
+    }
+    na.issue(stage, wave, lane, ik * BK, p.K, ik * BK * lda, INT_MAX, 0);
+    nb.issue(stage + A_BYTES, wave, lane, ik * BK, p.K, ik * BK * ldb, INT_MAX, 0);
+    if (++ik == nk) ik = 0, ++itile;
+  };
+  f32x16 acc[MI][NI];
+  auto clear = [&] {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  };
+  auto store = [&](int t, char* stage) {
+    const int m0 = (part + t * parts) * kStripM;
+    epilogue_rows<EPI_STORE_PART, GT, kStripM, kStripN, MI, NI, WAVES, 2, RR>(p, acc, m0, n0, 0, wm, wn, lane, wave, stage);
+  };
+  clear();
+  if (steps == 0) {   // an expert without rows: zeros
+    for (int t = 0; t < count; ++t) store(t, smem);
+    return;
+  }
+  issue(smem);
+  if (steps > 1) issue(smem + STAGE);
+  int cur = 0, k = 0, t = 0;
+  bool stored = false;   // a whole tile's plain stores were the last thing issued
+  for (int s = 0; s < steps; ++s) {
+    char* stage = smem + cur * STAGE;
+    // this step's DMAs have landed; the next step's, and stores made after them, may be in flight
+    if (s + 1 >= steps) wait_vmcnt<0>();
+    else if (stored) wait_vmcnt<N_DMA + STORES>();
+    else wait_vmcnt<N_DMA>();
+    wait_lgkmcnt0();
+    __builtin_amdgcn_s_barrier();   // (and every wave is done with the stage that is loaded next)
+    if (s + 2 < steps) issue(smem + (cur >= 1 ? cur - 1 : cur + 2) * STAGE);
+    const int sub = min(NSUB, (p.K - k * BK + KMMA - 1) / KMMA);   // rows past the last are zeros
+    auto substep = [&](int q) {
+      u32x4 fa[MI][KC], fb[NI][KC];
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int c = 0; c < KC; ++c) fa[i][c] = DA::read(stage, wm * WM + i * 32, q, lane);
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int c = 0; c < KC; ++c) fb[j][c] = DB::read(stage + A_BYTES, wn * WN + j * 32, q, lane);
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NI; ++j) Mma<T>::mma(fb[j], fa[i], acc[i][j]);
+    };
+    if (sub == NSUB) {   // unrolled, the reads of later substeps go ahead
+#pragma unroll
+      for (int q = 0; q < NSUB; ++q) substep(q);
+    } else {
+      for (int q = 0; q < sub; ++q) substep(q);
+    }
+    stored = false;
+    if (++k == nk) {
+      k = 0;
+      wait_lgkmcnt0();
+      __builtin_amdgcn_s_barrier();   // the stage becomes the epilogue's staging area
+      store(t, stage);
+      const int m0 = (part + t * parts) * kStripM;
+      stored = p.partial == nullptr && !p.accumulate && m0 + kStripM <= p.M && n0 + kStripN <= p.N;
+      clear();
+      ++t;
+    }
+    cur = cur == 2 ? 0 : cur + 1;
+  }
 }
 
 // The pieces' sums of one expert joined, 16 columns by 16 runs of pieces a workgroup (of 256 threads, or
@@ -338,6 +461,28 @@ __global__ __launch_bounds__(64 * WAVES, 1) void expert_bwd_kernel(const ExpertB
   }
 }
 
+// The backward with few rows an expert (ExpertBwd::strip_parts).
+template <typename T, typename GT>
+__global__ __launch_bounds__(256, 2) void expert_bwd_few_kernel(const ExpertBwd a) {
+  constexpr int lds = expert_lds_bytes<T, 64, 128, 4>() > strip_lds_bytes<T>() ? expert_lds_bytes<T, 64, 128, 4>() : strip_lds_bytes<T>();
+  __shared__ __attribute__((aligned(1024))) char smem[lds];
+  int b = blockIdx.x;
+  const int first = a.dw_first ? a.dw.grid : a.dx.grid;
+  if (b >= a.dx.grid + a.dw.grid)
+    bias_grad_block<GT>(a.db, b - a.dx.grid - a.dw.grid, reinterpret_cast<float*>(smem));
+  else if ((b < first) == (a.dw_first != 0))
+    expert_grad_strip<T, GT>(a, a.dw_first ? b : b - first, smem);
+  else
+    expert_rows_tile<T, 64, 128, false, EPI_STORE_PART, 4>(a.dx, a.dw_first ? b - first : b, smem, a.dx_splits, a.dx_kps, a.part_x);
+}
+
+template <typename T> hipError_t launch_expert_bwd_few(const ExpertBwd& a, hipStream_t s) {
+  const dim3 grid(a.dx.grid + a.dw.grid + a.db.grid);
+  if (a.dw.g.accumulate || a.db.accumulate) hipLaunchKernelGGL((expert_bwd_few_kernel<T, float>), grid, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((expert_bwd_few_kernel<T, T>), grid, dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
 template <typename T, int BM, int BN, int WAVES>
 hipError_t launch_expert_fwd(int epi, const ExpertGemm& a, hipStream_t s) {
   if (epi == EPI_LIN_GATED)
@@ -372,6 +517,7 @@ template <typename T> hipError_t expert_fwd16(int epi, TileShape tile, const Exp
   return hipErrorInvalidValue;
 }
 template <typename T> hipError_t expert_bwd16(TileShape tile, const ExpertBwd& a, hipStream_t s) {
+  if (a.strip_parts) return launch_expert_bwd_few<T>(a, s);
   if (tile == TILE_256x256_W8) return launch_expert_bwd<T, 256, 256, 8>(a, s);
   if (tile == TILE_128x128) return launch_expert_bwd<T, 128, 128, 4>(a, s);
   if (tile == TILE_64x64) return launch_expert_bwd<T, 64, 64, 4>(a, s);

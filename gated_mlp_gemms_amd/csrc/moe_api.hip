@@ -198,10 +198,31 @@ struct ExpertPlan {
   // slots that those take at most
   int dx_splits, piece_rows, max_slots;
   bool dw_first;
+  int strip_parts;       // backward, few rows an expert: shares of a strip's weight gradient (ExpertBwd); else 0
 };
 
 // Row tiles of bm rows that M rows of E experts (and the rows behind them) take at most.
 int64_t row_tiles(int64_t M, int64_t E, int64_t bm) { return M / bm + std::min(M, E) + 1; }
+
+// The backward with few rows an expert: dx in 64 x 128 tiles, the weight gradients in strips.
+ExpertPlan plan_experts_few(const linear_desc* d) {
+  const int64_t M = d->M, E = std::max(d->experts, 1), P = is_gated(d->act) ? 2 * d->N : d->N;
+  const int bk = bk_of(dtype_of(d->dtype)), slots = 512;
+  ExpertPlan p{EXPERT_TILES, TILE_128x128, 64, 128, 0.0, 1, 0, 0, false, 0};
+  const int64_t tiles_m = (P + kStripTileM - 1) / kStripTileM, strips = E * ((d->K + kStripTileN - 1) / kStripTileN);
+  p.strip_parts = (int)std::min<int64_t>(tiles_m, std::max<int64_t>(1, 2 * slots / strips));
+  const int64_t kx = (P + bk - 1) / bk, tx = (M / 64 + (std::min(M, E) + 1) / 2) * ((d->K + 127) / 128);
+  const double work = ((double)tx * (kx + 2) + (double)(strips * tiles_m) * ((double)(M / E) / bk + 1)) / slots;
+  while (p.dx_splits < 16 && kx / p.dx_splits > std::max(8.0, work) && kx / (p.dx_splits + 1) >= 8) ++p.dx_splits;
+  const int64_t piece = (int64_t)std::max(8.0, work) * bk;   // for an expert that most rows go to
+  if (M >= piece + piece / 2) {
+    p.piece_rows = (int)piece;
+    p.max_slots = (int)(2 * (M / piece) + 1);
+  }
+  const int es = esize(d->dtype);
+  p.est = 4e-6 + (2.0 * (double)E * P + (double)M) * (double)d->K * es / 5.0e12 + (p.dx_splits > 1 || p.piece_rows ? 4e-6 : 0.0);
+  return p;
+}
 
 // The tile by the time model of step_time, every expert ending in half a row tile on average: forward
 // [M, K] -> [M, N], or backward both products ([M, P] -> [M, K], and K over the expert's rows).
@@ -209,10 +230,11 @@ ExpertPlan plan_experts(const linear_desc* d, bool fwd) {
   const DType io = dtype_of(d->dtype);
   const bool gated = is_gated(d->act);
   const int64_t M = d->M, E = std::max(d->experts, 1), P = gated ? 2 * d->N : d->N;
-  if (fwd && io != DT_F32 && M <= kExpertFewRows * E) return {EXPERT_SKINNY, TILE_128x128, 128, 128, 0.0, 1, 0, 0, false};
+  if (fwd && io != DT_F32 && M <= kExpertFewRows * E) return {EXPERT_SKINNY, TILE_128x128, 128, 128, 0.0, 1, 0, 0, false, 0};
+  if (!fwd && io != DT_F32 && M <= E * (E * P * d->K * 2 < kStreamGradBytes ? kStripRowsSmall : kStripRows)) return plan_experts_few(d);
   TileInfo t[4];
   const int n = linear_tiles(io, fwd && gated, t), bk = bk_of(io);
-  ExpertPlan best{EXPERT_TILES, TILE_COUNT, 0, 0, 1e300, 1, 0, 0, false};
+  ExpertPlan best{EXPERT_TILES, TILE_COUNT, 0, 0, 1e300, 1, 0, 0, false, 0};
   for (int i = 0; i < n; ++i) {
     if (t[i].t == TILE_256x128_W8) continue;
     const StepTime st = step_time(t[i].t, io, fwd && gated);
@@ -220,7 +242,7 @@ ExpertPlan plan_experts(const linear_desc* d, bool fwd) {
     const int64_t rt = std::max<int64_t>(1, M / t[i].bm + (std::min(M, E) + 1) / 2);
     const int64_t kx = ((fwd ? d->K : P) + bk - 1) / bk;
     const int64_t tx = rt * (((fwd ? d->N : d->K) + bnc - 1) / bnc);
-    ExpertPlan p{EXPERT_TILES, t[i].t, t[i].bm, t[i].bn, 0.0, 1, 0, 0, false};
+    ExpertPlan p{EXPERT_TILES, t[i].t, t[i].bm, t[i].bn, 0.0, 1, 0, 0, false, 0};
     if (fwd) {
       p.est = tiles_time(st, t[i].slots, tx, kx);
     } else {
@@ -611,13 +633,20 @@ mlp_status linear_bwd(const linear_desc* d, const void* dy, const void* x, const
     gw.tiles_m = (int)((P + p.bm - 1) / p.bm);
     gw.tiles_n = (int)((K + p.bn - 1) / p.bn);
     gw.group_m = std::min(gw.tiles_m, 8);
+    if (p.strip_parts) {
+      gw.tiles_m = (int)((P + kStripTileM - 1) / kStripTileM);
+      gw.tiles_n = (int)((K + kStripTileN - 1) / kStripTileN);
+      b.strip_parts = p.strip_parts;
+    }
+    if (E * P * K * esize(d->dtype) >= kStreamGradBytes && (!p.strip_parts || K * esize(d->dtype) % 128 == 0)) gw.flags = kFlagStream;
     b.dw = expert_gemm(d, gw, offsets);
     if (dw && M > 0) {
       b.piece_rows = p.piece_rows;
       b.max_slots = p.max_slots;
       b.part_w = reinterpret_cast<float*>(base + L.part_w);
     }
-    if (dw) b.dw.grid = (int)(((b.piece_rows ? M / b.piece_rows : 0) + E) * gw.tiles_m * gw.tiles_n);
+    const int64_t shares = (int64_t)(b.strip_parts ? b.strip_parts : gw.tiles_m) * gw.tiles_n;   // of an expert's weight gradient
+    if (dw) b.dw.grid = (int)(((b.piece_rows ? M / b.piece_rows : 0) + E) * shares);
     if (dw && b.dx.grid && p.dw_first) {
       b.dw_first = 1;
       if (b.piece_rows) b.dw.grid = (b.dw.grid + 7) / 8 * 8;

@@ -598,3 +598,37 @@ def test_linear_backward_in_one_launch(M, K, N, act):
     """Sizes whose dx and dW may share a launch, ragged ones among them."""
     for dt in (torch.bfloat16, torch.float16):
         check_linear(M, K, N, act, dt, bias=False, residual=False)
+
+
+FEW_ROWS = [  # rows an expert, rows behind them, K, N, activations
+    ([3, 0, 31, 64, 65, 1, 0, 100], 5, 264, 456, ("none", "swiglu")),          # whole and part K-steps, several tiles a strip
+    ([2] * 40 + [0] * 5 + [900], 0, 520, 200, ("gelu_tanh", "glu")),           # one expert summed over pieces
+    ([1], 0, 4104, 1288, ("relu", "geglu")), ([7, 12], 0, 1032, 72, ("none", "reglu")),
+    ([130, 250, 200, 60], 9, 136, 392, ("relu_sq", "swiglu")),
+    ([9, 20, 0, 33], 0, 4096, 4096, ("none",)), ([5, 2, 1, 0], 0, 4104, 4096, ("none",)),   # past the caches, or not in whole lines
+    ([200, 90, 140], 0, 4096, 4608, ("none",)),                                # tiles, past the caches
+]
+
+
+@pytest.mark.parametrize("case", FEW_ROWS, ids=lambda c: f"{len(c[0])}x{sum(c[0])}-{c[2]}-{c[3]}")
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_backward_of_few_rows(case, dtype):
+    counts, tail, K, N, acts = case
+    for act in acts:
+        check_linear(sum(counts) + tail, K, N, act, R.DT[dtype], experts=len(counts), offsets=offsets_of(counts))
+        if len(counts) <= 2:
+            check_linear(sum(counts), K, N, act, R.DT[dtype])
+
+
+def test_backward_of_few_rows_is_the_same_again():
+    dt, g = torch.bfloat16, gen(77)
+    for counts, K, N in (([3, 0, 40, 9], 264, 456), ([2] * 40 + [900], 520, 200)):
+        M, E = sum(counts), len(counts)
+        t = make_linear(g, M, K, N, "none", dt, E, False, False)
+        desc, dy, off = gm.make_linear_desc(M, K, N, dtype=dt, experts=E), normal(g, M, N, dtype=dt), offsets_of(counts)
+        runs = []
+        for _ in range(3):
+            dx, dw = poison(M, K, dtype=dt), poison(E, N, K, dtype=dt)
+            gm.linear_bwd(desc, dy, t["x"], t["w"], offsets=off, dx=dx, dw=dw)
+            runs.append((dx, dw))
+        assert all(torch.equal(runs[0][i], r[i]) for r in runs[1:] for i in range(2))
