@@ -109,11 +109,9 @@ __device__ __forceinline__ void load_scores(const void* logits, int64_t row, int
 // reduction; fp32 scores take a second one for the expert.
 // 16384 tokens x 128 scores, k = 8: bound by the rounds' instructions (reading the scores takes 1 us).
 template <typename T, int L, int C>
-__global__ __launch_bounds__(kRouteThreads) void route_kernel(const void* __restrict__ logits, int64_t tokens, int E,
-                                                              int k, int sigmoid, int renorm, int* __restrict__ ids,
-                                                              float* __restrict__ weights) {
+__device__ __forceinline__ void route_token(const void* __restrict__ logits, int64_t t, int64_t tokens, int E, int k,
+                                            int sigmoid, int renorm, int* __restrict__ ids, float* __restrict__ weights) {
   const int lane = threadIdx.x & (L - 1);
-  const int64_t t = (int64_t)blockIdx.x * (kRouteThreads / L) + threadIdx.x / L;
   const bool live = t < tokens;
   constexpr bool PACKED = sizeof(T) == 2;
   float x[C];
@@ -181,6 +179,14 @@ __global__ __launch_bounds__(kRouteThreads) void route_kernel(const void* __rest
     weights[t * k + lane] = w;
   }
 }
+template <typename T, int L, int C>
+__global__ __launch_bounds__(kRouteThreads) void route_kernel(const void* __restrict__ logits, int64_t tokens, int E,
+                                                              int k, int sigmoid, int renorm, int* __restrict__ ids,
+                                                              float* __restrict__ weights) {
+  constexpr int R = kRouteThreads / L;
+  for (int64_t t0 = (int64_t)blockIdx.x * R; t0 < tokens; t0 += (int64_t)gridDim.x * R)
+    route_token<T, L, C>(logits, t0 + threadIdx.x / L, tokens, E, k, sigmoid, renorm, ids, weights);
+}
 
 // f(id, coefficient) of choice I, I + 1, .. k - 1, which lane I of the group holds. Lane I of 16 reaches its
 // row as a DPP operand (row broadcast); wider groups shuffle.
@@ -202,13 +208,10 @@ __device__ __forceinline__ void each_choice(int k, int id, float coef, F f) {
 //   softmax:               dx_e = [e chosen] w g - p_e m, p over every expert;
 //   sigmoid, renormalised: dx_i = w_i (1 - q_i) (g_i - m);   sigmoid: q_i (1 - q_i) g_i.
 template <typename T, int L, int C>
-__global__ __launch_bounds__(kRouteThreads) void route_bwd_kernel(const void* __restrict__ logits,
-                                                                  const int* __restrict__ ids,
-                                                                  const float* __restrict__ dweights, int64_t tokens,
-                                                                  int E, int k, int sigmoid, int renorm,
-                                                                  void* __restrict__ dlogits) {
+__device__ __forceinline__ void route_token_bwd(const void* __restrict__ logits, const int* __restrict__ ids,
+                                                const float* __restrict__ dweights, int64_t t, int64_t tokens, int E,
+                                                int k, int sigmoid, int renorm, void* __restrict__ dlogits) {
   const int lane = threadIdx.x & (L - 1);
-  const int64_t t = (int64_t)blockIdx.x * (kRouteThreads / L) + threadIdx.x / L;
   const bool live = t < tokens;
   int id = -1;
   float g = 0.0f, s = -INFINITY;
@@ -286,6 +289,16 @@ __global__ __launch_bounds__(kRouteThreads) void route_bwd_kernel(const void* __
     const int e = lane * C + j;
     if (e < E) store1<T>(dlogits, t * E + e, d[j]);
   }
+}
+template <typename T, int L, int C>
+__global__ __launch_bounds__(kRouteThreads) void route_bwd_kernel(const void* __restrict__ logits,
+                                                                  const int* __restrict__ ids,
+                                                                  const float* __restrict__ dweights, int64_t tokens,
+                                                                  int E, int k, int sigmoid, int renorm,
+                                                                  void* __restrict__ dlogits) {
+  constexpr int R = kRouteThreads / L;
+  for (int64_t t0 = (int64_t)blockIdx.x * R; t0 < tokens; t0 += (int64_t)gridDim.x * R)
+    route_token_bwd<T, L, C>(logits, ids, dweights, t0 + threadIdx.x / L, tokens, E, k, sigmoid, renorm, dlogits);
 }
 
 // f(L, C) for the lanes a token and scores a lane that E takes.
@@ -421,7 +434,10 @@ inline int row_shift(int64_t pieces) {
   while (sh < 8 && (int64_t)(1 << sh) < pieces) ++sh;
   return sh;
 }
-inline int64_t row_grid(int64_t rows, int sh) { return (rows + (kRowThreads >> sh) - 1) / (kRowThreads >> sh); }
+// Workgroups for `items` items, `per` a workgroup: at most 2^20, which then take several (2^32 threads are more
+// than a launch can have).
+inline unsigned item_grid(int64_t items, int64_t per) { return (unsigned)std::min<int64_t>((items + per - 1) / per, 1 << 20); }
+inline unsigned row_grid(int64_t rows, int sh) { return item_grid(rows, kRowThreads >> sh); }
 
 template <typename T> struct Piece {   // 16 bytes of a row
   static constexpr int N = 16 / (int)sizeof(T);
@@ -467,13 +483,15 @@ __global__ __launch_bounds__(kRowThreads) void gather_kernel(const u32x4* __rest
                                                              const int* __restrict__ slot_of,
                                                              const int* __restrict__ offsets, int n, int E, int k,
                                                              int pieces, int sh, u32x4* __restrict__ xs) {
-  const int r = blockIdx.x * (kRowThreads >> sh) + (threadIdx.x >> sh);
-  if (r >= n) return;
-  const int slot = slot_of[r];
-  const bool kept = r < offsets[E] && (uint32_t)slot < (uint32_t)n;
-  const u32x4* src = x + (int64_t)(kept ? slot / k : 0) * pieces;
-  u32x4* dst = xs + (int64_t)r * pieces;
-  for (int c = threadIdx.x & ((1 << sh) - 1); c < pieces; c += 1 << sh) store_piece<NT>(dst + c, kept ? src[c] : u32x4{0u, 0u, 0u, 0u});
+  const int per = kRowThreads >> sh;
+  for (int r = blockIdx.x * per + (threadIdx.x >> sh); r < n; r += gridDim.x * per) {
+    const int slot = slot_of[r];
+    const bool kept = r < offsets[E] && (uint32_t)slot < (uint32_t)n;
+    const u32x4* src = x + (int64_t)(kept ? slot / k : 0) * pieces;
+    u32x4* dst = xs + (int64_t)r * pieces;
+    for (int c = threadIdx.x & ((1 << sh) - 1); c < pieces; c += 1 << sh)
+      store_piece<NT>(dst + c, kept ? src[c] : u32x4{0u, 0u, 0u, 0u});
+  }
 }
 
 // out[t] = residual[t] + sum_j weights[t][j] ys[row_of[t k + j]] over the kept rows (weights NULL: 1,
@@ -487,41 +505,41 @@ __global__ __launch_bounds__(kRowThreads) void combine_kernel(const u32x4* __res
                                                               int tokens, int E, int k, int pieces, int sh,
                                                               u32x4* out) {
   constexpr int N = Piece<T>::N;
-  const int t = blockIdx.x * (kRowThreads >> sh) + (threadIdx.x >> sh);
-  if (t >= tokens) return;
-  const int kept = min(offsets[E], tokens * k);
-  for (int c = threadIdx.x & ((1 << sh) - 1); c < pieces; c += 1 << sh) {
-    float acc[N];
-#pragma unroll
-    for (int q = 0; q < N; ++q) acc[q] = 0.0f;
-    for (int j0 = 0; j0 < k; j0 += J) {
-      u32x4 v[J];
-      float w[J];
-      bool ok[J];
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        const int64_t slot = (int64_t)t * k + j0 + j;
-        const int row = j0 + j < k ? row_of[slot] : -1;
-        ok[j] = row >= 0 && row < kept;
-        w[j] = ok[j] && weights != nullptr ? weights[slot] : 1.0f;
-        v[j] = ok[j] ? load_piece<NT>(ys + (int64_t)row * pieces + c) : u32x4{0u, 0u, 0u, 0u};
+  const int per = kRowThreads >> sh, kept = min(offsets[E], tokens * k);
+  for (int t = blockIdx.x * per + (threadIdx.x >> sh); t < tokens; t += gridDim.x * per) {
+    for (int c = threadIdx.x & ((1 << sh) - 1); c < pieces; c += 1 << sh) {
+      float acc[N];
+  #pragma unroll
+      for (int q = 0; q < N; ++q) acc[q] = 0.0f;
+      for (int j0 = 0; j0 < k; j0 += J) {
+        u32x4 v[J];
+        float w[J];
+        bool ok[J];
+  #pragma unroll
+        for (int j = 0; j < J; ++j) {
+          const int64_t slot = (int64_t)t * k + j0 + j;
+          const int row = j0 + j < k ? row_of[slot] : -1;
+          ok[j] = row >= 0 && row < kept;
+          w[j] = ok[j] && weights != nullptr ? weights[slot] : 1.0f;
+          v[j] = ok[j] ? load_piece<NT>(ys + (int64_t)row * pieces + c) : u32x4{0u, 0u, 0u, 0u};
+        }
+  #pragma unroll
+        for (int j = 0; j < J; ++j) {
+          if (!ok[j]) continue;
+          float f[N];
+          Piece<T>::unpack(v[j], f);
+  #pragma unroll
+          for (int q = 0; q < N; ++q) acc[q] = __builtin_fmaf(w[j], f[q], acc[q]);
+        }
       }
-#pragma unroll
-      for (int j = 0; j < J; ++j) {
-        if (!ok[j]) continue;
+      if (residual != nullptr) {
         float f[N];
-        Piece<T>::unpack(v[j], f);
-#pragma unroll
-        for (int q = 0; q < N; ++q) acc[q] = __builtin_fmaf(w[j], f[q], acc[q]);
+        Piece<T>::unpack(residual[(int64_t)t * pieces + c], f);
+  #pragma unroll
+        for (int q = 0; q < N; ++q) acc[q] += f[q];
       }
+      store_piece<NT>(out + (int64_t)t * pieces + c, Piece<T>::pack(acc));
     }
-    if (residual != nullptr) {
-      float f[N];
-      Piece<T>::unpack(residual[(int64_t)t * pieces + c], f);
-#pragma unroll
-      for (int q = 0; q < N; ++q) acc[q] += f[q];
-    }
-    store_piece<NT>(out + (int64_t)t * pieces + c, Piece<T>::pack(acc));
   }
 }
 
@@ -537,34 +555,34 @@ __global__ __launch_bounds__(kRowThreads) void combine_bwd_kernel(const u32x4* _
                                                                   float* __restrict__ dweights) {
   constexpr int N = Piece<T>::N;
   const int lane = threadIdx.x & 63;
-  const int r = blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6);
-  if (r >= n) return;
-  const int slot = slot_of[r];
-  const bool known = (uint32_t)slot < (uint32_t)n, kept = known && r < offsets[E];
-  u32x4* dst = dys + (int64_t)r * pieces;
-  float dot = 0.0f;
-  if (kept) {
-    const float w = weights[slot];
-    const u32x4* g = dout + (int64_t)(slot / k) * pieces;
-    const u32x4* y = ys + (int64_t)r * pieces;
-#pragma unroll 4
-    for (int c = lane; c < pieces; c += 64) {
-      float gv[N], yv[N], o[N];
-      Piece<T>::unpack(g[c], gv);
-      Piece<T>::unpack(load_piece<NT>(y + c), yv);
-#pragma unroll
-      for (int q = 0; q < N; ++q) {
-        dot = __builtin_fmaf(gv[q], yv[q], dot);
-        o[q] = w * gv[q];
+  for (int r = blockIdx.x * (kRowThreads / 64) + (threadIdx.x >> 6); r < n; r += gridDim.x * (kRowThreads / 64)) {
+    const int slot = slot_of[r];
+    const bool known = (uint32_t)slot < (uint32_t)n, kept = known && r < offsets[E];
+    u32x4* dst = dys + (int64_t)r * pieces;
+    float dot = 0.0f;
+    if (kept) {
+      const float w = weights[slot];
+      const u32x4* g = dout + (int64_t)(slot / k) * pieces;
+      const u32x4* y = ys + (int64_t)r * pieces;
+  #pragma unroll 4
+      for (int c = lane; c < pieces; c += 64) {
+        float gv[N], yv[N], o[N];
+        Piece<T>::unpack(g[c], gv);
+        Piece<T>::unpack(load_piece<NT>(y + c), yv);
+  #pragma unroll
+        for (int q = 0; q < N; ++q) {
+          dot = __builtin_fmaf(gv[q], yv[q], dot);
+          o[q] = w * gv[q];
+        }
+        store_piece<NT>(dst + c, Piece<T>::pack(o));
       }
-      store_piece<NT>(dst + c, Piece<T>::pack(o));
+  #pragma unroll
+      for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o);
+    } else {
+      for (int c = lane; c < pieces; c += 64) dst[c] = u32x4{0u, 0u, 0u, 0u};
     }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) dot += __shfl_xor(dot, o);
-  } else {
-    for (int c = lane; c < pieces; c += 64) dst[c] = u32x4{0u, 0u, 0u, 0u};
+    if (known && lane == 0) dweights[slot] = dot;
   }
-  if (known && lane == 0) dweights[slot] = dot;
 }
 
 // f() with the element type of `dt` as its argument.
@@ -588,7 +606,7 @@ hipError_t run_moe_route(DType dt, const void* logits, int64_t T, int E, int k, 
   return by_type(dt, [&](auto v) {
     return route_shape(E, [&](auto l, auto c) {
       constexpr int L = decltype(l)::value, C = decltype(c)::value, R = kRouteThreads / L;
-      hipLaunchKernelGGL((route_kernel<decltype(v), L, C>), dim3((unsigned)((T + R - 1) / R)), dim3(kRouteThreads), 0, s,
+      hipLaunchKernelGGL((route_kernel<decltype(v), L, C>), dim3(item_grid(T, R)), dim3(kRouteThreads), 0, s,
                          logits, T, E, k, sigmoid, renorm, ids, weights);
       return hipGetLastError();
     });
@@ -600,7 +618,7 @@ hipError_t run_moe_route_bwd(DType dt, const void* logits, const int* ids, const
   return by_type(dt, [&](auto v) {
     return route_shape(E, [&](auto l, auto c) {
       constexpr int L = decltype(l)::value, C = decltype(c)::value, R = kRouteThreads / L;
-      hipLaunchKernelGGL((route_bwd_kernel<decltype(v), L, C>), dim3((unsigned)((T + R - 1) / R)), dim3(kRouteThreads), 0,
+      hipLaunchKernelGGL((route_bwd_kernel<decltype(v), L, C>), dim3(item_grid(T, R)), dim3(kRouteThreads), 0,
                          s, logits, ids, dweights, T, E, k, sigmoid, renorm, dlogits);
       return hipGetLastError();
     });
@@ -637,7 +655,7 @@ hipError_t run_moe_gather(const void* x, const int* slot_of, const int* offsets,
                           void* xs, hipStream_t s) {
   const int sh = row_shift(pieces);
   return by_stream(n, pieces, [&](auto nt) {
-    hipLaunchKernelGGL((gather_kernel<decltype(nt)::value>), dim3((unsigned)row_grid(n, sh)), dim3(kRowThreads), 0, s,
+    hipLaunchKernelGGL((gather_kernel<decltype(nt)::value>), dim3(row_grid(n, sh)), dim3(kRowThreads), 0, s,
                        static_cast<const u32x4*>(x), slot_of, offsets, n, E, k, pieces, sh, static_cast<u32x4*>(xs));
     return hipGetLastError();
   });
@@ -650,7 +668,7 @@ hipError_t run_moe_combine(DType dt, const void* ys, const float* weights, const
     auto launch = [&](auto j) {   // J: rows of a token in flight at once
       return by_stream((int64_t)T * k, pieces, [&](auto nt) {
         hipLaunchKernelGGL((combine_kernel<decltype(v), decltype(j)::value, decltype(nt)::value>),
-                           dim3((unsigned)row_grid(T, sh)), dim3(kRowThreads), 0, s, static_cast<const u32x4*>(ys),
+                           dim3(row_grid(T, sh)), dim3(kRowThreads), 0, s, static_cast<const u32x4*>(ys),
                            weights, row_of, offsets, static_cast<const u32x4*>(residual), T, E, k, pieces, sh,
                            static_cast<u32x4*>(out));
         return hipGetLastError();
@@ -667,7 +685,7 @@ hipError_t run_moe_combine_bwd(DType dt, const void* dout, const void* ys, const
                                hipStream_t s) {
   return by_type(dt, [&](auto v) {
     return by_stream(n, pieces, [&](auto nt) {
-      hipLaunchKernelGGL((combine_bwd_kernel<decltype(v), decltype(nt)::value>), dim3((unsigned)((n + 3) / 4)),
+      hipLaunchKernelGGL((combine_bwd_kernel<decltype(v), decltype(nt)::value>), dim3(item_grid(n, kRowThreads / 64)),
                          dim3(kRowThreads), 0, s, static_cast<const u32x4*>(dout), static_cast<const u32x4*>(ys),
                          weights, slot_of, offsets, n, E, k, pieces, static_cast<u32x4*>(dys), dweights);
       return hipGetLastError();

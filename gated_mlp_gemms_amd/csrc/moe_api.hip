@@ -75,7 +75,7 @@ mlp_status check_linear(const linear_desc* d) {
   if (d->experts < 0) return fail(MLP_ERR_INVALID_ARG, "experts = %d must be >= 0", d->experts);
   if (d->experts > 0) MLP_TRY(check_experts(d->experts));
   const int64_t P = is_gated(d->act) ? 2 * d->N : d->N, E = std::max(d->experts, 1), lim = (int64_t)1 << 37;
-  if (d->M > kRowLimit) return fail(MLP_ERR_UNSUPPORTED, "M is above 2^30");
+  if (d->M > kRowLimit / 2) return fail(MLP_ERR_UNSUPPORTED, "M is above 2^29");
   if (d->K >= (int64_t)1 << 25 || d->N >= (int64_t)1 << 25 || P >= (int64_t)1 << 25)
     return fail(MLP_ERR_UNSUPPORTED, "a leading dimension (K, N, or 2N gated) is 2^25 elements or more");
   if (d->M > lim / P || d->M > lim / d->K || E * P > lim / d->K)

@@ -97,7 +97,7 @@ mlp_status moe_combine_bwd(const void* dout, const void* ys, const float* weight
 #define LINEAR_ACT_NONE (-1)
 
 typedef struct linear_desc {
-  int64_t M;        /* rows of x (experts: all rows, dropped ones behind offsets[E] included) */
+  int64_t M;        /* rows of x (experts: all rows, dropped ones behind offsets[E] included), <= 2^29 */
   int64_t K;        /* width of x */
   int64_t N;        /* width of y */
   int32_t act;      /* mlp_act or LINEAR_ACT_NONE */

@@ -632,3 +632,54 @@ def test_backward_of_few_rows_is_the_same_again():
             gm.linear_bwd(desc, dy, t["x"], t["w"], offsets=off, dx=dx, dw=dw)
             runs.append((dx, dw))
         assert all(torch.equal(runs[0][i], r[i]) for r in runs[1:] for i in range(2))
+
+
+@pytest.mark.parametrize("act,score,bias,experts", [("swiglu", "softmax", False, 8), ("relu_sq", "sigmoid", True, 8),
+                                                    ("geglu", "softmax", True, 8), ("swiglu", "sigmoid", True, 7)])
+def test_runner_against_double(act, score, bias, experts):
+    """The layer's runner, fp32, against autograd of the formula in float64 on the CPU."""
+    from gated_mlp_gemms_amd.moe_runner import MoeRunner, moe_tensors
+
+    size = dict(act=act, dtype="f32", tokens=45, width=32, hidden=40, experts=experts)
+    t = moe_tensors(seed=5, bias=bias, **size)
+    r = MoeRunner(choices=3, score=score, tensors=t, **size)
+    r.step()
+    infer = MoeRunner(choices=3, score=score, tensors=t, train=False, **size)
+    assert torch.equal(infer.forward_infer(), r.out)
+    leaf = {k: v.double().cpu().requires_grad_() for k, v in t.items() if k != "dout"}
+    gated, ids = act in R.GATED, r.ids.long().cpu()
+    x, w1, w2 = leaf["x"], leaf["w_gate" if gated else "w1"], leaf["w_down" if gated else "w2"]
+    p = x @ leaf["router"].T
+    p = torch.softmax(p, 1) if score == "softmax" else torch.sigmoid(p)
+    w = p.gather(1, ids)
+    w = w / w.sum(1, keepdim=True)
+    out = x
+    for j in range(3):
+        e = ids[:, j]
+        g = (w1[e] @ x[:, :, None])[:, :, 0] + (leaf["b_gate" if gated else "b1"][e] if bias else 0)
+        if gated:
+            u = (leaf["w_up"][e] @ x[:, :, None])[:, :, 0] + (leaf["b_up"][e] if bias else 0)
+            a = (torch.nn.functional.silu(g) if act == "swiglu" else torch.nn.functional.gelu(g, approximate="tanh")) * u
+        else:
+            a = torch.relu(g) ** 2
+        out = out + w[:, j:j + 1] * ((w2[e] @ a[:, :, None])[:, :, 0] + (leaf["b_down" if gated else "b2"][e] if bias else 0))
+    names = ["x", "router", "w_gate" if gated else "w1", "w_down" if gated else "w2"] + (["w_up"] if gated else [])
+    keys = ["dx", "d_router", "dw1", "dw2"] + (["dw_up"] if gated else [])
+    if bias:
+        names += ["b_gate" if gated else "b1", "b_down" if gated else "b2"] + (["b_up"] if gated else [])
+        keys += ["db1", "db2"] + (["db_up"] if gated else [])
+    grads = torch.autograd.grad((out * t["dout"].double().cpu()).sum(), [leaf[n] for n in names])
+    # as test_layer_gradients_against_double_and_differences
+    R.check("out", r.out.cpu(), out.detach(), torch.full_like(out, 2000 * R.U32 * out.abs().max().item()).detach())
+    assert sorted(r.grads()) == sorted(keys)
+    for k, b in zip(keys, grads):
+        R.check(k, r.grads()[k].cpu(), b, torch.full_like(b, 2000 * R.U32 * b.abs().max().item()))
+
+
+def test_runner_command(capsys):
+    from gated_mlp_gemms_amd import moe_runner
+
+    moe_runner.main(["--tokens", "64", "--width", "64", "--hidden", "72", "--experts", "4", "--choices", "2", "--steps", "2",
+                     "--decode-tokens", "3"])
+    text = capsys.readouterr().out
+    assert "training step, 64 tokens" in text and "in a graph, 3 tokens" in text

@@ -335,3 +335,8 @@ def test_binding_is_required(monkeypatch):
     monkeypatch.delattr(gm, "_bind", raising=False)
     with pytest.raises(RuntimeError, match="_bind extension"):
         gm.moe_route(t(5, 8), t(5, 2, dtype=I32), t(5, 2, dtype=F32))
+
+
+def test_rows_beyond_a_launch_are_refused():
+    assert fwd(desc(M=(1 << 29) + 8, K=8, N=8)) == MLP_ERR_UNSUPPORTED and "2^29" in err()
+    assert gm.linear_workspace_bytes(desc(M=1 << 29, K=8, N=8, act="none"), "bwd") >= 256
