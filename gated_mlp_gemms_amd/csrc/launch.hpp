@@ -85,8 +85,8 @@ hipError_t run_expert_bwd_f32(TileShape tile, const ExpertBwd& a, hipStream_t s)
 // kStripTileN of x. Taken up to kStripRows rows an expert on average, for weight gradients that caches hold
 // (kStreamGradBytes) up to kStripRowsSmall. Both products, against the tiles (us): 1711 rows of 113 experts (6080 x 152) 147
 // and 197, 97 of 60 (4992 x 704) 212 and 243, 4096 of 32 (2048 x 1376) 110 and 95; caches hold: 5 of 3 (4456 x 464) 15 and 23,
-// 576 of 3 (1952 x 672) 18 and 23, 4000 of 16 (512 x 1024) 37 and 44.
-constexpr int kStripTileM = 64, kStripTileN = 128, kStripRows = 32, kStripRowsSmall = 256;
+// 576 of 3 (1952 x 672) 19 and 23, 4000 of 16 (512 x 1024) 37 and 31.
+constexpr int kStripTileM = 64, kStripTileN = 128, kStripRows = 32, kStripRowsSmall = 200;
 // Weight gradients from this size on are stored past the caches (16-bit; in strips only with rows of whole 128-byte
 // lines: a strip's store of part of a line goes to memory on its own). Both products of 4096 rows of 32 experts of
 // 2048 x 1376: 127 -> 95 us.

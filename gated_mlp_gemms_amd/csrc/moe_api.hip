@@ -204,6 +204,9 @@ struct ExpertPlan {
 // Row tiles of bm rows that M rows of E experts (and the rows behind them) take at most.
 int64_t row_tiles(int64_t M, int64_t E, int64_t bm) { return M / bm + std::min(M, E) + 1; }
 
+// K-steps that are not worth another launch to join them (about 0.3 us each of a product with CUs to spare, against 5 us).
+constexpr double kJoinSteps = 20.0;
+
 // The backward with few rows an expert: dx in 64 x 128 tiles, the weight gradients in strips.
 ExpertPlan plan_experts_few(const linear_desc* d) {
   const int64_t M = d->M, E = std::max(d->experts, 1), P = is_gated(d->act) ? 2 * d->N : d->N;
@@ -213,8 +216,8 @@ ExpertPlan plan_experts_few(const linear_desc* d) {
   p.strip_parts = (int)std::min<int64_t>(tiles_m, std::max<int64_t>(1, 2 * slots / strips));
   const int64_t kx = (P + bk - 1) / bk, tx = (M / 64 + (std::min(M, E) + 1) / 2) * ((d->K + 127) / 128);
   const double work = ((double)tx * (kx + 2) + (double)(strips * tiles_m) * ((double)(M / E) / bk + 1)) / slots;
-  while (p.dx_splits < 16 && kx / p.dx_splits > std::max(8.0, work) && kx / (p.dx_splits + 1) >= 8) ++p.dx_splits;
-  const int64_t piece = (int64_t)std::max(8.0, work) * bk;   // for an expert that most rows go to
+  while (p.dx_splits < 16 && kx / p.dx_splits > std::max(kJoinSteps, work) && kx / (p.dx_splits + 1) >= 8) ++p.dx_splits;
+  const int64_t piece = (int64_t)std::max(kJoinSteps, work) * bk;   // for an expert that most rows go to
   if (M >= piece + piece / 2) {
     p.piece_rows = (int)piece;
     p.max_slots = (int)(2 * (M / piece) + 1);
@@ -250,10 +253,11 @@ ExpertPlan plan_experts(const linear_desc* d, bool fwd) {
       const int64_t kw = (M / E + bk - 1) / bk;
       const double work = ((double)tx * (kx + 2) + (double)E * tw * (kw + 2)) / slots;   // K-steps a slot
       // dx in parts while a part is longer than half of what a slot has to do, and takes 8 K-steps
-      while (p.dx_splits < 16 && kx / p.dx_splits > std::max(8.0, work) && kx / (p.dx_splits + 1) >= 8) ++p.dx_splits;
+      const double least = io == DT_F32 ? 8.0 : kJoinSteps;
+      while (p.dx_splits < 16 && kx / p.dx_splits > std::max(least, work) && kx / (p.dx_splits + 1) >= 8) ++p.dx_splits;
       // weight gradients over pieces of the rows: with few tiles of half a slot's work, else of all of it
-      // (an expert that most rows go to); at least 8 K-steps
-      const int64_t piece = (int64_t)std::max(8.0, E * tw < 2 * slots ? work / 2 : work) * bk;
+      // (an expert that most rows go to)
+      const int64_t piece = (int64_t)std::max(least, E * tw < 2 * slots ? work / 2 : work) * bk;
       int64_t kd = std::min<int64_t>((M + bk - 1) / bk, E == 1 ? (M + bk - 1) / bk : 2 * kw);   // longest tile expected
       if (M >= piece + piece / 2) {
         p.piece_rows = (int)piece;
