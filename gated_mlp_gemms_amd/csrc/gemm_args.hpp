@@ -60,7 +60,8 @@ struct GemmArgs {
 // weight gradients w_stride, bias_stride and w_stride elements apart. The members' pointers are those
 // of expert 0 and row 0; M (products over rows) or K (weight gradients) is set per expert on the
 // device. tiles_m of a product over rows is unused.
-constexpr int kFlagStream = 4;   // in g.flags: an output that no cache holds until it is read is stored past the caches
+// In g.flags: an output that no cache holds until it is read is stored past the caches; so are its runs of zeros.
+constexpr int kFlagStream = 4, kFlagLarge = 8;
 struct ExpertGemm {
   GemmArgs g;
   const int* offsets;
@@ -70,13 +71,14 @@ struct ExpertGemm {
   int split_tail;   // products over rows in 256-row tiles: a last round of at most half the CUs runs as halves
 };
 // The bias gradients from the column sums of pieces of at most `step` rows (run_linear_dact): db0
-// [experts, N], and db1 for the other N columns of a gated layer; written, or added into fp32.
+// [experts, N], and db1 for the other N columns of a gated layer; written, or added into fp32. runs (1, 4, 16): parts of
+// an expert's pieces that are summed beside one another.
 struct BiasGrad {
   const float* sums;
   const int* offsets;
   int experts, rows, N, step, max_pieces, accumulate;
   void* db0; void* db1;
-  int grid;
+  int grid, runs;
 };
 // The backward's two products and the bias gradient in one launch: the workgroups of dx and of dW (dw_first:
 // the other way round), then the bias gradient's.

@@ -230,8 +230,22 @@ __device__ __forceinline__ int expert_slots_before(const int* offsets, int exper
   return __builtin_amdgcn_readfirstlane(slots);
 }
 
+// Zeros into share `item` of `tiles` of the weight gradient(s) of an expert without rows: in order of memory, whatever
+// the tiles are (2 rows, 50 experts of 648 x 2576 gated: the launch 134 -> 107 us).
+template <typename GT>
+__device__ __forceinline__ void zero_share(const GemmArgs& p, int64_t elems, int item, int tiles) {
+  const int64_t pieces = elems * (int64_t)sizeof(GT) / 16, all = p.C1 != nullptr ? 2 * pieces : pieces;
+  const int64_t beg = all * item / tiles, end = all * (item + 1) / tiles;
+  const u32x4 zero = {0u, 0u, 0u, 0u};
+  for (int64_t i = beg + threadIdx.x; i < end; i += blockDim.x) {
+    u32x4* q = reinterpret_cast<u32x4*>(i < pieces ? p.C0 : p.C1) + (i < pieces ? i : i - pieces);
+    if (p.flags & kFlagLarge) __builtin_nontemporal_store(zero, q);
+    else *q = zero;
+  }
+}
+
 // The share of workgroup b of the weight gradients dW_e = dz^T x over expert e's rows, or over a piece of them,
-// `tiles` shares a piece: the product in p and the share's number, or -1.
+// `tiles` shares a piece: the product in p and the share's number, or -1. p.K = 0: the share is one of zeros.
 template <typename T, typename GT>
 __device__ __forceinline__ int expert_grad_share(const ExpertBwd& all, int b, int tiles, GemmArgs& p) {
   const ExpertGemm& a = all.dw;
@@ -266,19 +280,24 @@ __device__ __forceinline__ int expert_grad_share(const ExpertBwd& all, int b, in
     n = __builtin_amdgcn_readfirstlane(n);
   }
   if (n == 0 && p.accumulate) return -1;
+  p.C0 = shift<GT>(p.C0, e * a.w_stride);
+  p.C1 = shift<GT>(p.C1, e * a.w_stride);
   p.K = p.k_per_split = n;
   p.A = shift<T>(p.A, row0 * p.lda);
   p.B0 = shift<T>(p.B0, row0 * p.ldb);
-  p.C0 = shift<GT>(p.C0, e * a.w_stride);
-  p.C1 = shift<GT>(p.C1, e * a.w_stride);
   return item;
 }
 
 template <typename T, typename GT, int BM, int BN, int WAVES>
 __device__ __forceinline__ void expert_grad_tile(const ExpertBwd& all, int b, char* smem) {
   GemmArgs p;
-  const int item = expert_grad_share<T, GT>(all, b, all.dw.g.tiles_m * all.dw.g.tiles_n, p);
+  const int tiles = all.dw.g.tiles_m * all.dw.g.tiles_n;
+  const int item = expert_grad_share<T, GT>(all, b, tiles, p);
   if (item < 0) return;
+  if (p.K == 0) {
+    zero_share<GT>(p, all.dw.w_stride, item, tiles);
+    return;
+  }
   gemm_dma_tile<T, GT, BM, BN, false, false, EPI_STORE_PART, WAVES, true>(p, item, smem);
 }
 
@@ -308,6 +327,10 @@ __device__ __forceinline__ void expert_grad_strip(const ExpertBwd& all, int b, c
   const int parts = all.strip_parts;
   const int share = expert_grad_share<T, GT>(all, b, all.dw.g.tiles_n * parts, p);
   if (share < 0) return;
+  if (p.K == 0) {
+    zero_share<GT>(p, all.dw.w_stride, share, all.dw.g.tiles_n * parts);
+    return;
+  }
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / 2, wn = wave % 2;
   const int n0 = share / parts * kStripN, part = share % parts;
@@ -342,10 +365,6 @@ __device__ __forceinline__ void expert_grad_strip(const ExpertBwd& all, int b, c
     epilogue_rows<EPI_STORE_PART, GT, kStripM, kStripN, MI, NI, WAVES, 2, RR>(p, acc, m0, n0, 0, wm, wn, lane, wave, stage);
   };
   clear();
-  if (steps == 0) {   // an expert without rows: zeros
-    for (int t = 0; t < count; ++t) store(t, smem);
-    return;
-  }
   issue(smem);
   if (steps > 1) issue(smem + STAGE);
   int cur = 0, k = 0, t = 0;
@@ -396,13 +415,16 @@ __device__ __forceinline__ void expert_grad_strip(const ExpertBwd& all, int b, c
   }
 }
 
-// The pieces' sums of one expert joined, 16 columns by 16 runs of pieces a workgroup (of 256 threads, or
-// more that do nothing), the runs added in order. red: 256 floats.
+// The pieces' sums of one expert joined, 256 / runs columns by `runs` runs of pieces a workgroup (of 256 threads, or
+// more that do nothing), the runs added in order. red: 256 floats. Few pieces an expert take one run: these
+// workgroups share the launch's LDS size, one or two a CU, so there should be few (32 experts of 2752 columns as 5504
+// workgroups of 16 columns: the backward's launch 986 us, 943 with 352 of 256).
 template <typename GT>
 __device__ __forceinline__ void bias_grad_block(const BiasGrad& a, int block, float* red) {
-  const int lane = threadIdx.x & 63, run = threadIdx.x >> 4;
-  const int P = a.db1 ? 2 * a.N : a.N, blocks = (P + 15) / 16;
-  const int e = block / blocks, n = (block % blocks) * 16 + (threadIdx.x & 15);
+  const int runs = a.runs, cols = 256 / runs;   // powers of two
+  const int lane = threadIdx.x & 63, run = threadIdx.x / cols;
+  const int P = a.db1 ? 2 * a.N : a.N, blocks = (P + cols - 1) / cols;
+  const int e = block / blocks, n = (block % blocks) * cols + (threadIdx.x & (cols - 1));
   // the expert's first piece: the pieces of the experts before, counted 64 experts at a time
   int first = 0;
   for (int base = 0; base < e; base += 64) {
@@ -417,18 +439,19 @@ __device__ __forceinline__ void bias_grad_block(const BiasGrad& a, int block, fl
   int row0, m;
   expert_rows(a.offsets, a.experts, a.rows, e, row0, m);
   const int pieces = (m + a.step - 1) / a.step;
-  const int b = (int)((int64_t)run * pieces / 16);
-  const int end = min((int)((int64_t)(run + 1) * pieces / 16), a.max_pieces - first);   // offsets may be anything
+  const int b = (int)((int64_t)run * pieces / runs);
+  const int end = min((int)((int64_t)(run + 1) * pieces / runs), a.max_pieces - first);   // offsets may be anything
   float s = 0.0f;
-  if (n < P && run < 16) {
+  if (n < P && run < runs) {
 #pragma unroll 8
     for (int i = b; i < end; ++i) s += a.sums[(int64_t)(first + i) * P + n];
   }
-  if (run < 16) red[threadIdx.x] = s;
-  __syncthreads();
+  if (runs > 1) {
+    if (run < runs) red[threadIdx.x] = s;
+    __syncthreads();
+  }
   if (run != 0 || n >= P) return;
-  s = red[threadIdx.x];
-  for (int w = 1; w < 16; ++w) s += red[w * 16 + threadIdx.x];
+  for (int w = 1; w < runs; ++w) s += red[w * cols + threadIdx.x];
   void* db = n >= a.N ? a.db1 : a.db0;
   const int64_t at = (int64_t)e * a.N + (n >= a.N ? n - a.N : n);
   if (a.accumulate) {

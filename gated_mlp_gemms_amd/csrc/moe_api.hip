@@ -590,8 +590,10 @@ mlp_status linear_bwd(const linear_desc* d, const void* dy, const void* x, const
                                        dbias ? sums : nullptr, s), "activation gradient"));
   BiasGrad db{};
   if (dbias) {
-    db = {sums, offsets, (int)E, (int)M, (int)N, dact_rows(M, N), (int)dact_pieces(M, N, E), grad_accum, dbias, dbias_up, 0};
-    db.grid = (int)(E * ((P + 15) / 16));
+    db = {sums, offsets, (int)E, (int)M, (int)N, dact_rows(M, N), (int)dact_pieces(M, N, E), grad_accum, dbias, dbias_up, 0, 1};
+    const int64_t pieces = M / E / dact_rows(M, N);   // of an expert
+    db.runs = pieces <= 16 ? 1 : pieces <= 64 ? 4 : 16;
+    db.grid = (int)(E * ((P + 256 / db.runs - 1) / (256 / db.runs)));
   }
   const LinearBwd b = d->experts || M == 0 ? LinearBwd{} : plan_linear_bwd(d, dx != nullptr, dw != nullptr);
   const bool one = d->experts || M == 0 || b.small;   // (one weight without rows: as one expert without rows)
@@ -642,7 +644,8 @@ mlp_status linear_bwd(const linear_desc* d, const void* dy, const void* x, const
       gw.tiles_n = (int)((K + kStripTileN - 1) / kStripTileN);
       b.strip_parts = p.strip_parts;
     }
-    if (E * P * K * esize(d->dtype) >= kStreamGradBytes && (!p.strip_parts || K * esize(d->dtype) % 128 == 0)) gw.flags = kFlagStream;
+    if (E * P * K * esize(d->dtype) >= kStreamGradBytes)
+      gw.flags = kFlagLarge | (!p.strip_parts || K * esize(d->dtype) % 128 == 0 ? kFlagStream : 0);
     b.dw = expert_gemm(d, gw, offsets);
     if (dw && M > 0) {
       b.piece_rows = p.piece_rows;
