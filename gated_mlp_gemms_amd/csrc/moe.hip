@@ -428,18 +428,11 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int* __r
 
 constexpr int kRowThreads = 256;
 
-// A row of `pieces` 16-byte pieces is walked by 2^sh threads; kRowThreads >> sh rows a workgroup. From a wave a
-// row on: the number of threads that leaves the fewest turns idle in at most 3 walks. Combine and gather's gradient (us),
-// 256 threads and this: 12000 rows of 325 pieces 17.6 / 15.0 and 16.2 / 13.9; five walks of 128 for 625 pieces would cost
-// 43.5 / 41.4 against three of 256 35.7 / 33.8.
+// A row of `pieces` 16-byte pieces is walked by 2^sh threads; kRowThreads >> sh rows a workgroup. (Fewer threads a row
+// where they would leave fewer turns idle: 5003 tokens of 259 pieces there and back 108 -> 115 us.)
 inline int row_shift(int64_t pieces) {
   int sh = 0;
   while (sh < 8 && (int64_t)(1 << sh) < pieces) ++sh;
-  int64_t least = (((pieces - 1) >> sh) + 1) << sh;
-  for (int t = sh - 1; t >= 6 && pieces <= (int64_t)3 << t; --t) {
-    const int64_t turns = (((pieces - 1) >> t) + 1) << t;
-    if (turns < least) least = turns, sh = t;
-  }
   return sh;
 }
 // Workgroups for `items` items, `per` a workgroup: at most 2^20, which then take several (2^32 threads are more

@@ -97,7 +97,7 @@ GemmArgs linear_args(const linear_desc* d) {
 }
 
 // The tile shapes of the linear layer's and the experts' products. The 16-bit ones' rates are plan_gemm's;
-// 64 x 64: NNN. fp32 (of its own, a sixteenth of the 16-bit peak): 104-127 of 154 TFLOP/s at 128 x 128.
+// 64 x 64: as measured in step_time. fp32 (of its own, a sixteenth of the 16-bit peak): 104-127 of 154 TFLOP/s at 128 x 128.
 int linear_tiles(DType in, bool gated, TileInfo (&t)[4]) {
   if (in == DT_F32) {
     t[0] = {TILE_128x128_RING, 128, 128, 2, 0.85};
