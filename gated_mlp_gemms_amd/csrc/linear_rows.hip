@@ -138,11 +138,11 @@ __global__ __launch_bounds__(kThr) void linear_dbias_kernel(const BiasGrad a) {
 }
 
 // The experts' partial sums joined (ExpertBwd): workgroups [0, dx_blocks) add up dx's parts (zeros behind the
-// last offset), dw_blocks an expert after them the pieces of the weight gradients that have several. About 4 pieces of
-// 4 columns a thread, fewer for many experts (of which few have pieces): a weight gradient of 4864 x 2048 f16 from
-// 2 pieces, 95 us with 64 workgroups.
+// last offset), dw_blocks an expert after them the pieces of the weight gradients that have several. 4 columns a
+// thread, more for many experts (of which few have pieces): a weight gradient of 4864 x 2048 f16 from 2 pieces took 95 us
+// with 64 workgroups, one of 320 x 252 from 62 pieces 27 us with 20.
 inline int join_blocks(int64_t elems, int experts) {
-  const int64_t want = (elems / 4 + 4 * kThr - 1) / (4 * kThr);
+  const int64_t want = (elems / 4 + kThr - 1) / kThr;
   return (int)std::min<int64_t>(want, std::max(16, 4096 / experts));
 }
 
