@@ -683,3 +683,34 @@ def test_runner_command(capsys):
                      "--decode-tokens", "3"])
     text = capsys.readouterr().out
     assert "training step, 64 tokens" in text and "in a graph, 3 tokens" in text
+
+
+def test_calls_on_a_stream_that_is_passed():
+    """A torch stream and its handle as the `stream` argument: the same bits as on the current one."""
+    g, dt = gen(31), torch.bfloat16
+    T, E, k, d = 33, 8, 2, 72
+    x, logits = normal(g, T, d, dtype=dt), normal(g, T, E)
+    w, b = normal(g, E, d, d, scale=0.1, dtype=dt), normal(g, E, d, dtype=dt)
+    desc = gm.make_linear_desc(T * k, d, d, act="relu", dtype=dt, experts=E)
+    side = torch.cuda.Stream()
+
+    def run(stream):
+        ids, wt = poison(T, k, dtype=torch.int32), poison(T, k, dtype=torch.float32)
+        off, row, slot = (poison(n, dtype=torch.int32) for n in (E + 1, T * k, T * k))
+        xs, y, out, pre = (poison(n, d, dtype=dt) for n in (T * k, T * k, T, T * k))
+        dw, db, dx = poison(E, d, d, dtype=dt), poison(E, d, dtype=dt), poison(T * k, d, dtype=dt)
+        ws = [torch.zeros(gm.linear_workspace_bytes(desc, p), dtype=torch.uint8, device=DEV) for p in ("fwd", "bwd")]
+        sw = torch.zeros(gm.moe_sort_workspace_bytes(T * k, E), dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        gm.moe_route(logits, ids, wt, stream=stream)
+        gm.moe_sort(ids, E, off, row, slot, workspace=sw, stream=stream)
+        gm.moe_gather(x, slot, off, xs, stream=stream)
+        gm.linear_fwd(desc, xs, w, y, bias=b, offsets=off, preact=pre, workspace=ws[0], stream=stream)
+        gm.moe_combine(y, wt, row, off, out, residual=x, stream=stream)
+        gm.linear_bwd(desc, y, xs, w, preact=pre, offsets=off, dx=dx, dw=dw, dbias=db, workspace=ws[1], stream=stream)
+        torch.cuda.synchronize()
+        return ids, wt, off, row, slot, xs, y, out, dx, dw, db
+
+    first = run(None)
+    for stream in (side, side.cuda_stream):
+        assert all(torch.equal(a, c) for a, c in zip(first, run(stream)))
