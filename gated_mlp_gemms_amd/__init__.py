@@ -19,7 +19,7 @@ from ._lib import (  # noqa: F401
     MLP_ACT_SWIGLU, MLP_BF16, MLP_BWD_DW_DOWN_WITH_DACT, MLP_BWD_GROUPED, MLP_F16, MLP_F32, MLP_FP8_E4M3,
     MLP_FP8_E5M2, MLP_GATE_INSIDE, MLP_GATE_OUTSIDE,
     MLP_NOALLOC_SCRATCH_BYTES, MLP_PHASE_BWD, MLP_PHASE_FWD, MLP_PHASE_FWD_INFER, MlpDesc, MlpError, MlpFp8, check,
-    lib,
+    lib, workspace_on,
 )
 from ._lib import (  # noqa: F401
     LINEAR_ACT_NONE, LINEAR_BWD, LINEAR_FWD, MOE_MAX_CHOICES, MOE_MAX_EXPERTS, MOE_SIGMOID, MOE_SOFTMAX, LinearDesc,
@@ -71,26 +71,28 @@ def workspace_bytes(desc: MlpDesc, phase: str) -> int:
     return int(n)
 
 
-def _workspace(desc, phase, workspace, device):
+def _workspace(desc, phase, workspace, device, stream):
     if workspace is not None:
         return workspace, workspace.numel() * workspace.element_size()
     n = workspace_bytes(desc, phase)
-    return torch.empty(n, dtype=torch.uint8, device=device), n
+    return workspace_on(n, device.index, stream), n
 
 
 def mlp_fwd(desc, x, w_gate, w_up, w_down, out, saved_preact=None, fp8=None, workspace=None, stream=None):
-    ws, nws = _workspace(desc, "fwd", workspace, out.device)
+    s = _stream(stream)
+    ws, nws = _workspace(desc, "fwd", workspace, out.device, s)
     st = lib().mlp_fwd(C.byref(desc), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(out),
                        _ptr(saved_preact), C.byref(fp8) if fp8 is not None else None, _ptr(ws), nws,
-                       _stream(stream))
+                       s)
     check(st, "mlp_fwd")
     return out
 
 
 def mlp_fwd_infer(desc, x, w_gate, w_up, w_down, out, fp8=None, workspace=None, stream=None):
-    ws, nws = _workspace(desc, "fwd_infer", workspace, out.device)
+    s = _stream(stream)
+    ws, nws = _workspace(desc, "fwd_infer", workspace, out.device, s)
     st = lib().mlp_fwd_infer(C.byref(desc), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(out),
-                             C.byref(fp8) if fp8 is not None else None, _ptr(ws), nws, _stream(stream))
+                             C.byref(fp8) if fp8 is not None else None, _ptr(ws), nws, s)
     check(st, "mlp_fwd_infer")
     return out
 
@@ -106,11 +108,12 @@ def mlp_fwd_infer_noalloc(desc, x, w_gate, w_up, w_down, out, fp8=None, stream=N
 
 def mlp_bwd(desc, dout, x, w_gate, w_up, w_down, saved_preact=None, dpreact=None, dx=None, dw_gate=None,
             dw_up=None, dw_down=None, grad_accum=False, fp8=None, workspace=None, stream=None):
-    ws, nws = _workspace(desc, "bwd", workspace, dout.device)
+    s = _stream(stream)
+    ws, nws = _workspace(desc, "bwd", workspace, dout.device, s)
     st = lib().mlp_bwd(C.byref(desc), _ptr(dout), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
                        _ptr(saved_preact), _ptr(dpreact), _ptr(dx), _ptr(dw_gate), _ptr(dw_up), _ptr(dw_down),
                        int(bool(grad_accum)), C.byref(fp8) if fp8 is not None else None, _ptr(ws), nws,
-                       _stream(stream))
+                       s)
     check(st, "mlp_bwd")
 
 
@@ -121,10 +124,11 @@ def mlp_quantize_workspace_bytes() -> int:
 def mlp_quantize_e4m3(src, dst, scale, workspace=None, stream=None):
     """Per-tensor e4m3 quantization of ``src`` (f32/bf16/f16) into ``dst`` (uint8 or float8_e4m3fn)
     and the fp32 device scalar ``scale``."""
+    s = _stream(stream)
     if workspace is None:
-        workspace = torch.empty(mlp_quantize_workspace_bytes(), dtype=torch.uint8, device=src.device)
+        workspace = workspace_on(mlp_quantize_workspace_bytes(), src.device.index, s)
     st = lib().mlp_quantize_e4m3(_ptr(src), _DTYPES[src.dtype], src.numel(), _ptr(dst), _ptr(scale),
-                                 _ptr(workspace), workspace.numel(), _stream(stream))
+                                 _ptr(workspace), workspace.numel(), s)
     check(st, "mlp_quantize_e4m3")
 
 

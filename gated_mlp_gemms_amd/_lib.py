@@ -113,6 +113,25 @@ _BOUND = ("moe_route", "moe_route_bwd", "moe_sort_workspace_bytes", "moe_sort", 
           "moe_combine", "moe_combine_bwd", "linear_workspace_bytes", "linear_fwd", "linear_bwd")
 
 
+def raw_stream(device: int) -> int:
+    """The handle of the stream that torch's current one is on GPU `device`."""
+    import torch
+
+    return torch._C._cuda_getCurrentRawStream(device)
+
+
+def workspace_on(n: int, device: int, stream: int):
+    """`n` bytes for one call on the stream of handle `stream`, dropped once the call has been made. The allocator hands
+    a block on in the order of the stream that it was allocated on, so the block is allocated on the call's."""
+    import torch
+
+    where = torch.device("cuda", device)
+    if stream == raw_stream(device):
+        return torch.empty(n, dtype=torch.uint8, device=where)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=where)):
+        return torch.empty(n, dtype=torch.uint8, device=where)
+
+
 def bind():
     """The extension that checks tensors and makes moe.h's calls (bind.cpp), tied to the loaded library."""
     global _bind
@@ -126,10 +145,8 @@ def bind():
             raise RuntimeError("the _bind extension is missing or does not load: build it with "
                                "`python -m gated_mlp_gemms_amd.build`") from e
 
-        def workspace(n, device):
-            return torch.empty(n, dtype=torch.uint8, device=torch.device("cuda", device))
-
-        ext.setup(tuple(C.cast(getattr(L, n), C.c_void_p).value for n in _BOUND), MlpError, workspace,
+        ext.setup(tuple(C.cast(getattr(L, n), C.c_void_p).value for n in _BOUND), MlpError,
+                  lambda n, device, stream: workspace_on(n, device, stream),
                   getattr(torch._C, "_cuda_getCurrentRawStream", None))
         _bind = ext
     return _bind

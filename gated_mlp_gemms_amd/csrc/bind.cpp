@@ -151,13 +151,14 @@ void* stream_of(PyObject* o, int dev) {
   return s;
 }
 
-// The caller's workspace, or a new one of need() bytes that lives until the call has been made (torch's
-// allocator hands its memory on in stream order).
+// The caller's workspace, or a new one of need() bytes that lives until the call has been made: torch's
+// allocator hands it on in the order of the stream it was allocated on, which is the call's.
 class Workspace {
  public:
-  template <typename Need> Workspace(PyObject* o, int dev, Need need) {
+  template <typename Need> Workspace(PyObject* o, int dev, void* stream, Need need) {
     if (o == Py_None) {
-      own_ = PyObject_CallFunction(py_workspace, "Ki", (unsigned long long)need(), dev);
+      own_ = PyObject_CallFunction(py_workspace, "KiK", (unsigned long long)need(), dev,
+                                   (unsigned long long)reinterpret_cast<uintptr_t>(stream));
       if (own_ == nullptr) throw PyFailed{};
       o = own_;
     }
@@ -267,8 +268,8 @@ void sort(PyObject* const* a) {
   auto* row_of = arg.as<int32_t>(a[3], "row_of", kI32, {n});
   auto* slot_of = arg.as<int32_t>(a[4], "slot_of", kI32, {n});
   const int dev = arg.device();
-  const Workspace ws(a[5], dev, [&] { return needed(lib.sort_bytes(n, E), "moe_sort_workspace_bytes"); });
   void* s = stream_of(a[6], dev);
+  const Workspace ws(a[5], dev, s, [&] { return needed(lib.sort_bytes(n, E), "moe_sort_workspace_bytes"); });
   call(dev, "moe_sort", [&] { return lib.sort(ids, n, E, offsets, row_of, slot_of, ws.ptr, ws.bytes, s); });
 }
 
@@ -394,8 +395,8 @@ void fwd(PyObject* const* a) {
   void* y = arg(a[3], "y", q.dt, {M, N});
   void* preact = arg.opt(a[9], "preact", q.dt, {M, q.P});
   const int dev = arg.device();
-  const Workspace ws(a[10], dev, [&] { return needed(lib.linear_bytes(&q.d, LINEAR_FWD), "linear_workspace_bytes"); });
   void* s = stream_of(a[11], dev);
+  const Workspace ws(a[10], dev, s, [&] { return needed(lib.linear_bytes(&q.d, LINEAR_FWD), "linear_workspace_bytes"); });
   call(dev, "linear_fwd",
        [&] { return lib.fwd(&q.d, x, w, w_up, bias, bias_up, res, offsets, y, preact, ws.ptr, ws.bytes, s); });
 }
@@ -419,14 +420,14 @@ void bwd(PyObject* const* a) {
   void* dbias = arg.opt(a[10], "dbias", gt, q.bias());
   void* dbias_up = arg.opt(a[11], "dbias_up", gt, q.bias());
   const int dev = arg.device();
-  const Workspace ws(a[13], dev, [&] { return needed(lib.linear_bytes(&q.d, LINEAR_BWD), "linear_workspace_bytes"); });
   void* s = stream_of(a[14], dev);
+  const Workspace ws(a[13], dev, s, [&] { return needed(lib.linear_bytes(&q.d, LINEAR_BWD), "linear_workspace_bytes"); });
   call(dev, "linear_bwd", [&] {
     return lib.bwd(&q.d, dy, x, w, w_up, preact, offsets, dx, dw, dw_up, dbias, dbias_up, accum, ws.ptr, ws.bytes, s);
   });
 }
 
-// addresses of the library's entry points in Entry's order, MlpError, workspace(bytes, device), raw_stream(device)
+// addresses of the library's entry points in Entry's order, MlpError, workspace(bytes, device, stream), raw_stream(device)
 PyObject* setup(PyObject*, PyObject* args) {
   PyObject *at, *error, *workspace, *raw_stream;
   if (!PyArg_ParseTuple(args, "O!OOO", &PyTuple_Type, &at, &error, &workspace, &raw_stream)) return nullptr;

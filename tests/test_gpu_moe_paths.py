@@ -1,0 +1,49 @@
+"""GPU tests of the mixture-of-experts operators on the paths that their main tests do not take."""
+import pytest
+import torch
+
+import gated_mlp_gemms_amd as gm
+from gpu_helpers import announce
+from test_gpu_moe import DEV, gen, normal, poison
+
+pytestmark = pytest.mark.gpu
+
+
+# ---- streams ------------------------------------------------------------------------------------
+
+def test_workspaces_of_calls_on_a_stream_that_is_passed():
+    """Without a workspace, on a stream that is not torch's current one: the same bits, and the memory that the
+    call allocates belongs to its stream."""
+    g, dt = gen(32), torch.bfloat16
+    T, E, k, d, h = 2100, 6, 3, 264, 520
+    n = T * k
+    ids = torch.rand(T, E, device=DEV, generator=g).topk(k, dim=1)[1].to(torch.int32)
+    x, dy, w, b = normal(g, n, d, dtype=dt), normal(g, n, h, dtype=dt), normal(g, E, h, d, scale=0.05, dtype=dt), normal(g, E, h, dtype=dt)
+    experts = gm.make_linear_desc(n, d, h, act="gelu_tanh", dtype=dt, experts=E)
+    deep = gm.make_linear_desc(130, 8200, 264, dtype=dt)        # split along K into partial sums
+    xd, wd = normal(g, 130, 8200, dtype=dt), normal(g, 264, 8200, scale=0.01, dtype=dt)
+    mlp = gm.make_desc(300, d, h, act="swiglu", dtype=dt)
+    xm, wg, wu, wo = normal(g, 300, d, dtype=dt), w[0].contiguous(), w[1].contiguous(), normal(g, d, h, scale=0.05, dtype=dt)
+    assert n > 4096 and gm.linear_workspace_bytes(deep, "fwd") > 256   # (the sort counts in its workspace)
+
+    def run(stream):
+        off, row, slot = (poison(m, dtype=torch.int32) for m in (E + 1, n, n))
+        y, pre, yd, ym = (poison(*s, dtype=dt) for s in ((n, h), (n, h), (130, 264), (300, d)))
+        dx, dw, db = poison(n, d, dtype=dt), poison(E, h, d, dtype=dt), poison(E, h, dtype=dt)
+        torch.cuda.synchronize()
+        gm.moe_sort(ids, E, off, row, slot, stream=stream)
+        gm.linear_fwd(experts, x, w, y, bias=b, offsets=off, preact=pre, stream=stream)
+        gm.linear_bwd(experts, dy, x, w, preact=pre, offsets=off, dx=dx, dw=dw, dbias=db, stream=stream)
+        gm.linear_fwd(deep, xd, wd, yd, stream=stream)
+        gm.mlp_fwd_infer(mlp, xm, wg, wu, wo, ym, stream=stream)
+        torch.cuda.synchronize()
+        return off, row, slot, y, pre, dx, dw, db, yd, ym
+
+    first = run(None)
+    for handle in (False, True):
+        side = torch.cuda.Stream()
+        assert side.cuda_stream != torch.cuda.current_stream().cuda_stream
+        announce(f"workspaces on {side}")
+        assert all(torch.equal(a, c) for a, c in zip(first, run(side.cuda_stream if handle else side)))
+        held = sum(s["total_size"] for s in torch.cuda.memory_snapshot() if s["stream"] == side.cuda_stream)
+        assert held >= gm.linear_workspace_bytes(experts, "bwd")
