@@ -3,8 +3,10 @@ import pytest
 import torch
 
 import gated_mlp_gemms_amd as gm
+import moe_paths as P
+import moe_reference as R
 from gpu_helpers import announce
-from test_gpu_moe import DEV, gen, normal, poison
+from test_gpu_moe import DEV, check_linear, gen, normal, offsets_of, poison
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +49,12 @@ def test_workspaces_of_calls_on_a_stream_that_is_passed():
         assert all(torch.equal(a, c) for a, c in zip(first, run(side.cuda_stream if handle else side)))
         held = sum(s["total_size"] for s in torch.cuda.memory_snapshot() if s["stream"] == side.cuda_stream)
         assert held >= gm.linear_workspace_bytes(experts, "bwd")
+
+
+# ---- every kernel of the products ---------------------------------------------------------------
+
+@pytest.mark.parametrize("p", P.PATHS, ids=lambda p: f"{p.M}x{p.K}x{p.N}-{p.act}-{p.dtype}-{len(p.counts or ())}")
+def test_products(p):
+    """Forward and backward, with bias and residual."""
+    counts = p.counts and list(p.counts)
+    check_linear(p.M, p.K, p.N, p.act, R.DT[p.dtype], experts=len(counts or ()), offsets=offsets_of(counts) if counts else None)
