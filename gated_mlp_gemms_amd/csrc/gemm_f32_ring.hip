@@ -10,7 +10,9 @@ static hipError_t ring(Layout layout, int epi, const GemmArgs& a, int grid, hipS
     case NT:
       switch (epi) {
         case EPI_LIN: return launch_gemm_dma<float, float, B, B, true, true, EPI_LIN>(a, grid, s);
-        case EPI_LIN_GATED: return launch_gemm_dma<float, float, B, 128, true, true, EPI_LIN_GATED>(a, grid, s);
+        case EPI_LIN_GATED:   // 64 rows only (linear_tiles)
+          if constexpr (B == 64) return launch_gemm_dma<float, float, 64, 128, true, true, EPI_LIN_GATED>(a, grid, s);
+          return hipErrorInvalidValue;
         case EPI_PARTIAL: return launch_gemm_dma<float, float, B, B, true, true, EPI_PARTIAL>(a, grid, s);
         default: return hipErrorInvalidValue;
       }

@@ -98,13 +98,14 @@ GemmArgs linear_args(const linear_desc* d) {
 
 // The tile shapes of the linear layer's and the experts' products. The 16-bit ones' rates are plan_gemm's;
 // 64 x 64: as measured in step_time. fp32 (of its own, a sixteenth of the 16-bit peak): 104-127 of 154 TFLOP/s at 128 x 128.
+// A gated fp32 tile has 64 units in either shape, and by step_time the one of 64 rows is faster at every size.
 int linear_tiles(DType in, bool gated, TileInfo (&t)[4]) {
-  if (in == DT_F32) {
-    t[0] = {TILE_128x128_RING, 128, 128, 2, 0.85};
-    t[1] = {TILE_64x64, 64, gated ? 128 : 64, 2, 0.70};
-    return 2;
-  }
   int n = 0;
+  if (in == DT_F32) {
+    if (!gated) t[n++] = {TILE_128x128_RING, 128, 128, 2, 0.85};
+    t[n++] = {TILE_64x64, 64, gated ? 128 : 64, 2, 0.70};
+    return n;
+  }
   for (const TileInfo& i : kTiles)
     if (i.t == TILE_256x256_W8 || i.t == TILE_256x128_W8 || i.t == TILE_128x128) t[n++] = i;
   t[n++] = {TILE_64x64, 64, gated ? 128 : 64, 2, gated ? 0.26 : 0.20};
