@@ -203,6 +203,14 @@ __device__ __forceinline__ void each_choice(int k, int id, float coef, F f) {
   }
 }
 
+// The sigmoid of s and its complement, both to a few roundings of themselves: 1 - q from a rounded q cancels, and is 0
+// from s = 17.4 on.
+struct Sigmoid { float q, rest; };
+__device__ __forceinline__ Sigmoid sigmoid_of(float s) {
+  const float t = expf(-fabsf(s)), r = 1.0f / (1.0f + t);
+  return s < 0.0f ? Sigmoid{t * r, r} : Sigmoid{r, t * r};
+}
+
 // The gradient, same lanes. With w the weights and m = sum_i g_i w_i:
 //   softmax, renormalised: a softmax of the chosen alone, dx_i = w_i (g_i - m) at the chosen ones;
 //   softmax:               dx_e = [e chosen] w g - p_e m, p over every expert;
@@ -229,14 +237,15 @@ __device__ __forceinline__ void route_token_bwd(const void* __restrict__ logits,
   for (int j = 0; j < C; ++j) d[j] = 0.0f;
   float coef = 0.0f;
   if (sigmoid) {
-    const float q = chosen ? 1.0f / (1.0f + expf(-s)) : 0.0f;
+    Sigmoid p = sigmoid_of(s);
+    p.q = chosen ? p.q : 0.0f;
     if (renorm) {
-      const float total = group_sum<L>(q);
-      const float w = total == 0.0f ? 0.0f : q / total;
+      const float total = group_sum<L>(p.q);
+      const float w = total == 0.0f ? 0.0f : p.q / total;
       const float mean = group_sum<L>(g * w);
-      coef = w * (1.0f - q) * (g - mean);
+      coef = w * p.rest * (g - mean);
     } else {
-      coef = q * (1.0f - q) * g;
+      coef = p.q * p.rest * g;
     }
   } else if (renorm) {
     const float top = key_score(group_max<L>(chosen ? score_key(s) : score_key(-INFINITY)));

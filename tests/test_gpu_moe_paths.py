@@ -51,6 +51,46 @@ def test_workspaces_of_calls_on_a_stream_that_is_passed():
         assert held >= gm.linear_workspace_bytes(experts, "bwd")
 
 
+# ---- router -------------------------------------------------------------------------------------
+
+def route_both(x, k, renorm, g):
+    """ids, weights, dweights and dlogits of a sigmoid router."""
+    T, E = x.shape
+    ids, w, dw = poison(T, k, dtype=torch.int32), poison(T, k, dtype=torch.float32), normal(g, T, k)
+    dl = poison(T, E, dtype=x.dtype)
+    gm.moe_route(x, ids, w, score="sigmoid", renorm=renorm)
+    gm.moe_route_bwd(x, ids, dw, dl, score="sigmoid", renorm=renorm)
+    return ids.long(), w, dw, dl
+
+
+def sigmoid_reference(x, ids, dw, renorm):
+    """In float64, from the logarithms so that nothing underflows or cancels: weights, dlogits at the chosen experts and
+    what the latter's error counts by (|w| (1 - q) times the terms of g - mean; unnormalised: the value)."""
+    s, g = x.double().gather(1, ids), dw.double()
+    logq, rest = torch.nn.functional.logsigmoid(s), torch.sigmoid(-s)
+    if not renorm:
+        return logq.exp(), logq.exp() * rest * g, (logq.exp() * rest * g).abs()
+    w = torch.softmax(logq, dim=1)
+    mean = (g * w).sum(dim=1, keepdim=True)
+    return w, w * rest * (g - mean), w * rest * (g.abs() + (g.abs() * w).sum(dim=1, keepdim=True))
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+def test_sigmoid_gradient_far_from_zero(renorm):
+    """Scores up to 30, whose sigmoids are 1 in fp32 and their gradients are not 0: the error is a few roundings of the
+    value itself. The exponential is off by 2 half steps at most, 1 + t, its reciprocal, two products and the last
+    by one each: 8; a normalised weight adds its total's (k + 8) and a quotient's, twice (in w and in the mean)."""
+    k = 8
+    for dt in R.DT.values():
+        announce(f"sigmoid gradient renorm={renorm} {dt}")
+        g = gen(60)
+        x = (torch.linspace(-30, 30, 320, device=DEV)[torch.randperm(320, device=DEV, generator=g)]).reshape(8, 40).to(dt)
+        ids, w, dw, dl = route_both(x, k, renorm, g)
+        rw, rd, mag = sigmoid_reference(x, ids, dw, renorm)
+        n = 8 + 2 * (k + 10) if renorm else 8
+        R.check("dlogits", dl.gather(1, ids), rd, n * R.U32 * mag + R.half_step(dt) * rd.abs() + R.floor_of(dt))
+
+
 # ---- every kernel of the products ---------------------------------------------------------------
 
 @pytest.mark.parametrize("p", P.PATHS, ids=lambda p: f"{p.M}x{p.K}x{p.N}-{p.act}-{p.dtype}-{len(p.counts or ())}")
