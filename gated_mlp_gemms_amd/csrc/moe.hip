@@ -76,6 +76,24 @@ template <typename T> __device__ __forceinline__ float packed_score(uint32_t m) 
 
 constexpr int kRouteThreads = 256;
 
+// The sigmoid of s and its complement, both to a few roundings of themselves: 1 - q from a rounded q cancels, and is 0
+// from s = 17.4 on.
+struct Sigmoid { float q, rest; };
+__device__ __forceinline__ Sigmoid sigmoid_of(float s) {
+  const float t = expf(-fabsf(s)), r = 1.0f / (1.0f + t);
+  return s < 0.0f ? Sigmoid{t * r, r} : Sigmoid{r, t * r};
+}
+
+// Sigmoids divided by their sum over L lanes (`mine`: of those that take part; top: their largest score), as the
+// exponentials that they are below 0, scaled by the largest: sigmoids themselves run out of range at -88, where
+// their ratios are as they are elsewhere. Below -104 the largest counts as 0 (2^-150), and all weights are 0.
+template <int L> __device__ __forceinline__ float sigmoid_share(float s, bool mine, float top) {
+  const float shift = fminf(top, 0.0f);
+  const float v = s < 0.0f ? expf(s - shift) / (1.0f + expf(s)) : sigmoid_of(s).q;
+  const float w = mine ? v : 0.0f, total = group_sum<L>(w);
+  return top < -104.0f ? 0.0f : w / total;
+}
+
 template <typename T, int C> struct ScorePart {   // C scores as one aligned piece
   static constexpr int B = C * (int)sizeof(T);
   struct alignas(B < 4 ? 4 : B < 16 ? B : 16) type { uint32_t w[(B + 3) / 4]; };
@@ -156,11 +174,8 @@ __device__ __forceinline__ void route_token(const void* __restrict__ logits, int
   const bool mine = lane < k;
   float w = 0.0f;
   if (sigmoid) {
-    w = mine ? 1.0f / (1.0f + expf(-my_score)) : 0.0f;
-    if (renorm) {
-      const float total = group_sum<L>(w);
-      w = total == 0.0f ? 0.0f : w / total;
-    }
+    if (renorm) w = sigmoid_share<L>(my_score, mine, top);
+    else w = mine ? sigmoid_of(my_score).q : 0.0f;
   } else if (top == -INFINITY) {   // every score is -inf: no expert has a probability
     w = 0.0f;
   } else {
@@ -203,14 +218,6 @@ __device__ __forceinline__ void each_choice(int k, int id, float coef, F f) {
   }
 }
 
-// The sigmoid of s and its complement, both to a few roundings of themselves: 1 - q from a rounded q cancels, and is 0
-// from s = 17.4 on.
-struct Sigmoid { float q, rest; };
-__device__ __forceinline__ Sigmoid sigmoid_of(float s) {
-  const float t = expf(-fabsf(s)), r = 1.0f / (1.0f + t);
-  return s < 0.0f ? Sigmoid{t * r, r} : Sigmoid{r, t * r};
-}
-
 // The gradient, same lanes. With w the weights and m = sum_i g_i w_i:
 //   softmax, renormalised: a softmax of the chosen alone, dx_i = w_i (g_i - m) at the chosen ones;
 //   softmax:               dx_e = [e chosen] w g - p_e m, p over every expert;
@@ -237,15 +244,14 @@ __device__ __forceinline__ void route_token_bwd(const void* __restrict__ logits,
   for (int j = 0; j < C; ++j) d[j] = 0.0f;
   float coef = 0.0f;
   if (sigmoid) {
-    Sigmoid p = sigmoid_of(s);
-    p.q = chosen ? p.q : 0.0f;
+    const Sigmoid p = sigmoid_of(s);
     if (renorm) {
-      const float total = group_sum<L>(p.q);
-      const float w = total == 0.0f ? 0.0f : p.q / total;
+      const float top = key_score(group_max<L>(chosen ? score_key(s) : score_key(-INFINITY)));
+      const float w = sigmoid_share<L>(s, chosen, top);
       const float mean = group_sum<L>(g * w);
       coef = w * p.rest * (g - mean);
     } else {
-      coef = p.q * p.rest * g;
+      coef = chosen ? p.q * p.rest * g : 0.0f;
     }
   } else if (renorm) {
     const float top = key_score(group_max<L>(chosen ? score_key(s) : score_key(-INFINITY)));

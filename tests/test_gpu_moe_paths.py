@@ -91,6 +91,36 @@ def test_sigmoid_gradient_far_from_zero(renorm):
         R.check("dlogits", dl.gather(1, ids), rd, n * R.U32 * mag + R.half_step(dt) * rd.abs() + R.floor_of(dt))
 
 
+def test_sigmoid_weights_of_low_scores():
+    """Scores whose sigmoids leave fp32's range (below -88): normalised, they are the weights of any other scores; the
+    sigmoid itself is as near as fp32 has it. The bound counts as above, the exponential of a difference of scores a
+    half step of the difference more."""
+    k = 6
+    for dt in (torch.float32, torch.bfloat16):
+        announce(f"sigmoid weights of low scores {dt}")
+        g = gen(61)
+        low = -20.0 - 83.0 * torch.rand(40, 24, device=DEV, generator=g)
+        low[0], low[1], low[2, 5:] = -95.0, -103.0, -200.0
+        low[3] = torch.linspace(-102, -88, 24, device=DEV)
+        low[4, 0] = 3.0                                    # a score of ordinary size among them
+        x = low.to(dt)
+        ids, w, dw, dl = route_both(x, k, True, g)
+        rw, rd, mag = sigmoid_reference(x, ids, dw, True)
+        s = x.double().gather(1, ids)
+        n = 2 * (k + 18) + 2 * (s[:, :1] - s)
+        tiny = 2 * torch.finfo(torch.float32).smallest_normal      # weights below fp32's range, and what they enter
+        R.check("weights", w, rw, n * R.U32 * rw + tiny)
+        R.check("dlogits", dl.gather(1, ids), rd,
+                n * R.U32 * mag + tiny * (1 + dw.abs().max().item()) * k + R.half_step(dt) * rd.abs() + R.floor_of(dt))
+        x[:] = -105.0                                      # below 2^-150 all of them count as 0
+        _, w, _, dl = route_both(x, k, True, g)
+        assert not w.any() and not dl.any()
+        x[:] = torch.linspace(-100, -70, 24, device=DEV)
+        ids, w, _, _ = route_both(x, k, False, g)
+        ref = torch.sigmoid(x.double().gather(1, ids))
+        R.check("weights", w, ref, 8 * R.U32 * ref + 2 * R.floor_of(torch.float32))
+
+
 # ---- every kernel of the products ---------------------------------------------------------------
 
 @pytest.mark.parametrize("p", P.PATHS, ids=lambda p: f"{p.M}x{p.K}x{p.N}-{p.act}-{p.dtype}-{len(p.counts or ())}")
