@@ -310,6 +310,13 @@ __device__ __forceinline__ void linear_fn_grad(int fn, const float (&z)[N], floa
       f[r] = z[r] * s;
       df[r] = s * (1.0f + z[r] * (1.0f - s) * (2.0f * kGeluC * (1.0f + 3.0f * kGeluK * (z[r] * z[r]))));
     }
+  } else if (fn == FN_SIGMOID) {   // for z > 0, 1 - s of a rounded s cancels: 1 - s = s exp(-z)
+#pragma unroll
+    for (int r = 0; r < N; ++r) {
+      const float e = __expf(-z[r]), s = __builtin_amdgcn_rcpf(1.0f + e);
+      f[r] = s;
+      df[r] = s * (z[r] > 0.0f ? s * e : 1.0f - s);
+    }
   } else {
     act_fn_grad<N>(fn, z, f, df);
   }

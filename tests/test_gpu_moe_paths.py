@@ -121,6 +121,33 @@ def test_sigmoid_weights_of_low_scores():
         R.check("weights", w, ref, 8 * R.U32 * ref + 2 * R.floor_of(torch.float32))
 
 
+# ---- activations --------------------------------------------------------------------------------
+
+def slopes(act, z, u=1.0):
+    """f'(z) and, gated, f(z) as linear_bwd forms them, in fp32: the bias gradients of one row against dy = 1."""
+    N, dt, gated = z.numel(), z.dtype, act in R.GATED
+    desc = gm.make_linear_desc(1, 8, N, act=act, dtype=dt)
+    pre = (torch.cat([z, torch.full_like(z, u)]) if gated else z).reshape(1, -1).contiguous()
+    x, w, dy = (torch.ones(*s, dtype=dt, device=DEV) for s in ((1, 8), (N, 8), (1, N)))
+    db, du = torch.zeros(N, device=DEV), torch.zeros(N, device=DEV)
+    gm.linear_bwd(desc, dy, x, w, w_up=w if gated else None, preact=pre, dbias=db, dbias_up=du if gated else None,
+                  grad_accum=True)
+    return db, du
+
+
+@pytest.mark.parametrize("dtype", list(R.DT))
+def test_glu_gradient_far_from_zero(dtype):
+    """Gates up to 80, where the sigmoid is 1 in fp32 and its gradient is not 0. Its exponential is off by |z| + 2 half
+    steps (fp32's argument), 1 + e, the reciprocal (2), two products by 6 in all; each counts in s, in s and in e."""
+    z = torch.linspace(-80, 80, 400, device=DEV).to(R.DT[dtype])
+    df, f = slopes("glu", z)
+    s = torch.sigmoid(z.double())
+    ref = s * torch.sigmoid(-z.double())
+    n = 3 * (z.double().abs() + 8)
+    R.check("f", f, s, n * R.U32 * s)
+    R.check("df", df, ref, n * R.U32 * ref)
+
+
 # ---- every kernel of the products ---------------------------------------------------------------
 
 @pytest.mark.parametrize("p", P.PATHS, ids=lambda p: f"{p.M}x{p.K}x{p.N}-{p.act}-{p.dtype}-{len(p.counts or ())}")
