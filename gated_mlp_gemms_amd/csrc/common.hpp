@@ -307,8 +307,9 @@ __device__ __forceinline__ void linear_fn_grad(int fn, const float (&z)[N], floa
 #pragma unroll
     for (int r = 0; r < N; ++r) {
       const float s = gelu_gate(z[r]);
+      const float c = __builtin_amdgcn_fmed3f(z[r], -16.0f, 16.0f);   // beyond, s or 1 - s is 0, and z z may overflow
       f[r] = z[r] * s;
-      df[r] = s * (1.0f + z[r] * (1.0f - s) * (2.0f * kGeluC * (1.0f + 3.0f * kGeluK * (z[r] * z[r]))));
+      df[r] = s * (1.0f + c * (1.0f - s) * (2.0f * kGeluC * (1.0f + 3.0f * kGeluK * (c * c))));
     }
   } else if (fn == FN_SIGMOID) {   // for z > 0, 1 - s of a rounded s cancels: 1 - s = s exp(-z)
 #pragma unroll

@@ -148,6 +148,16 @@ def test_glu_gradient_far_from_zero(dtype):
     R.check("df", df, ref, n * R.U32 * ref)
 
 
+@pytest.mark.parametrize("act", [a for a in R.ACTS if a != "none"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_slopes_of_large_values(act, dtype):
+    """From 1e5 to 1e38 every f' has reached its limit: 1, 0 or, of relu^2, 2 z."""
+    z = torch.tensor([s * 10.0 ** e for e in (5, 7, 9, 13, 17, 18, 19, 20, 25, 30, 33, 38) for s in (1, -1)], device=DEV).to(R.DT[dtype])
+    df, _ = slopes(act, z)
+    up = {"glu": 0.0, "relu_sq": 2 * z.float().clamp(min=0)}.get(act, (z > 0).float())
+    assert torch.equal(df, torch.broadcast_to(torch.as_tensor(up, device=DEV), df.shape))
+
+
 # ---- every kernel of the products ---------------------------------------------------------------
 
 @pytest.mark.parametrize("p", P.PATHS, ids=lambda p: f"{p.M}x{p.K}x{p.N}-{p.act}-{p.dtype}-{len(p.counts or ())}")
