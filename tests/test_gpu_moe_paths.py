@@ -158,6 +158,25 @@ def test_slopes_of_large_values(act, dtype):
     assert torch.equal(df, torch.broadcast_to(torch.as_tensor(up, device=DEV), df.shape))
 
 
+@pytest.mark.parametrize("act", R.ACTS)
+@pytest.mark.parametrize("M", [3, 100, 700])     # streamed, and in small and large tiles
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_nan_comes_through(act, M, dtype):
+    """A NaN in one row of x makes that row of y NaN, of every activation, and no other."""
+    dt, g, gated = R.DT[dtype], gen(62), act in R.GATED
+    K, N = 72, 1032
+    x, w, u = normal(g, M, K, dtype=dt), normal(g, N, K, dtype=dt), normal(g, N, K, dtype=dt) if gated else None
+    x[1, 5] = float("nan")
+    for experts, off in ((0, None), (1, offsets_of([M]))):
+        desc = gm.make_linear_desc(M, K, N, act=act, dtype=dt, experts=experts)
+        lead = (lambda t: t[None] if experts and t is not None else t)
+        y, pre = torch.zeros(M, N, dtype=dt, device=DEV), torch.zeros(M, 2 * N if gated else N, dtype=dt, device=DEV)
+        gm.linear_fwd(desc, x, lead(w), y, w_up=lead(u), offsets=off, preact=pre)
+        assert torch.isnan(y[1]).all() and torch.isnan(pre[1]).all()
+        rest = torch.arange(M, device=DEV) != 1
+        assert torch.isfinite(y[rest]).all() and torch.isfinite(pre[rest]).all()
+
+
 # ---- every kernel of the products ---------------------------------------------------------------
 
 @pytest.mark.parametrize("p", P.PATHS, ids=lambda p: f"{p.M}x{p.K}x{p.N}-{p.act}-{p.dtype}-{len(p.counts or ())}")
