@@ -184,3 +184,30 @@ def test_products(p):
     """Forward and backward, with bias and residual."""
     counts = p.counts and list(p.counts)
     check_linear(p.M, p.K, p.N, p.act, R.DT[p.dtype], experts=len(counts or ()), offsets=offsets_of(counts) if counts else None)
+
+
+@pytest.mark.parametrize("p", [p for p in P.PATHS if p.counts], ids=lambda p: f"{p.M}x{p.K}x{p.N}-{p.act}-{p.dtype}-{len(p.counts)}")
+def test_an_experts_nan_stays_its_own(p):
+    """Rows of one expert that are NaN reach no other expert's rows or gradients."""
+    dt, g, gated, E = R.DT[p.dtype], gen(63), p.act in R.GATED, len(p.counts)
+    announce(f"an expert's NaN {p}")
+    off = offsets_of(list(p.counts))
+    x, w, dy = normal(g, p.M, p.K, dtype=dt), normal(g, E, p.N, p.K, scale=0.05, dtype=dt), normal(g, p.M, p.N, dtype=dt)
+    u = normal(g, E, p.N, p.K, scale=0.05, dtype=dt) if gated else None
+    bad = max(e for e in range(E - 1) if p.counts[e])      # one with an expert behind it
+    lo, hi = int(off[bad]), int(off[bad + 1])
+    x[lo:hi], dy[lo:hi] = float("nan"), float("nan")
+    desc = gm.make_linear_desc(p.M, p.K, p.N, act=p.act, dtype=dt, experts=E)
+    y, pre, dx = (poison(p.M, n, dtype=dt) for n in (p.N, 2 * p.N if gated else p.N, p.K))
+    gm.linear_fwd(desc, x, w, y, w_up=u, offsets=off, preact=pre)
+    dw, db = poison(E, p.N, p.K, dtype=dt), poison(E, p.N, dtype=dt)
+    dwu, dbu = (torch.zeros_like(dw), torch.zeros_like(db)) if gated else (None, None)
+    gm.linear_bwd(desc, dy, x, w, w_up=u, preact=None if p.act == "none" else pre, offsets=off, dx=dx, dw=dw, dw_up=dwu,
+                  dbias=db, dbias_up=dbu)
+    rows = torch.ones(p.M, dtype=torch.bool, device=DEV)
+    rows[lo:hi] = False
+    for t in (y, pre, dx):
+        assert torch.isfinite(t[rows]).all() and torch.isnan(t[lo:hi]).any()
+    others = torch.arange(E, device=DEV) != bad
+    for t in filter(lambda t: t is not None, (dw, dwu, db, dbu)):
+        assert torch.isfinite(t[others]).all() and torch.isnan(t[bad]).any()
