@@ -67,6 +67,7 @@ __device__ __forceinline__ bool find_row_piece_of(const int* offsets, int expert
     const int n = max(at[i + 1] - at[i], 0);
     pieces[i] = (n + step - 1) / step;
     if constexpr (LEAST > 0) pieces[i] = e0 + i < experts ? max(pieces[i], LEAST) : 0;
+    if constexpr (LEAST < 0) pieces[i] = e0 + i < experts ? max(pieces[i] - 1, 0) : 0;
     if (e0 + i > experts) pieces[i] = 0;
     sum += pieces[i];
   }
@@ -96,12 +97,14 @@ __device__ __forceinline__ bool find_row_piece_of(const int* offsets, int expert
 // Pieces of every expert (the rows behind the last offset included) are numbered in expert order.
 // want(total) -> the number of the piece wanted, or -1. Called by whole waves; every wave of a
 // workgroup gets the same answer, in scalar registers. LEAST: pieces an expert has at least (the rows
-// behind the last offset then have none). Every tile starts with it, so it is one trip to memory and one scan.
+// behind the last offset then have none); -1: every expert's pieces but its first are numbered (its second is piece 0
+// of it, and the rows behind the last offset have none). Every tile starts with it, so it is one trip to memory and
+// one scan.
 template <int LEAST = 0, typename Want>
 __device__ __forceinline__ bool find_row_piece(const int* offsets, int experts, int rows, int step, Want want,
                                                RowPiece& out) {
   if (experts < 64) return find_row_piece_of<1, LEAST>(offsets, experts, rows, step, want, out);
-  if (experts < 256) return find_row_piece_of<4, LEAST>(offsets, experts, rows, step, want, out);
+  if (experts < 320) return find_row_piece_of<5, LEAST>(offsets, experts, rows, step, want, out);
   return find_row_piece_of<17, LEAST>(offsets, experts, rows, step, want, out);
 }
 

@@ -93,10 +93,10 @@ constexpr int kStripTileM = 64, kStripTileN = 128, kStripRows = 32, kStripRowsSm
 constexpr int64_t kStreamGradBytes = 100 << 20;
 // The partial sums of run_expert_bwd added up (nothing without any).
 hipError_t run_expert_join(DType io, const ExpertBwd& a, hipStream_t s);
-// The forward with a few rows an expert, 16-bit (g.N output columns, any rows; grid is unused).
-// Taken up to kExpertFewRows rows an expert on average. 64 experts, 2048 x 1376 gate and up, uneven rows,
-// against 128 x 128 tiles: 96 rows 78 and 96 us, 300 rows 134 and 153, 600 rows 161 and 154, 1000 rows 207 and 158
-// (an expert's weights are streamed again for every 16 of its rows).
+// The forward with a few rows an expert, 16-bit (g.N output columns, any rows; grid: runs of column blocks).
+// Taken up to kExpertFewRows rows an expert on average (an expert's weights are streamed again for every 16 of its rows).
+// Uneven rows, against the tiles that the plan takes above (us): 64 experts of 2048 x 1376 gate and up, 96 rows 76 and 88,
+// 256 129 and 145, 512 150 and 127, 768 173 and 126; 8 of 2048 x 5504 gate and up, 64 rows 75 and 80, 96 83 and 81.
 constexpr int kExpertFewRows = 8;
 hipError_t run_skinny_experts(DType in, int epi, const ExpertGemm& a, hipStream_t s);
 

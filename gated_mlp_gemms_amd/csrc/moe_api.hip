@@ -532,7 +532,10 @@ mlp_status linear_fwd(const linear_desc* d, const void* x, const void* w, const 
     a.N = (int)N;
     a.K = a.k_per_split = (int)K;
     ExpertGemm e = expert_gemm(d, a, offsets);
-    if (p.form == EXPERT_SKINNY) return hip_status(run_skinny_experts(io, epi, e, s), "experts' products (few rows)");
+    if (p.form == EXPERT_SKINNY) {
+      e.grid = (int)(d->experts + 1 + (M - 1) / 16);   // runs of column blocks
+      return hip_status(run_skinny_experts(io, epi, e, s), "experts' products (few rows)");
+    }
     const int64_t bn = gated ? p.bn / 2 : p.bn;
     e.g.tiles_n = (int)((N + bn - 1) / bn);
     e.g.group_m = 8;

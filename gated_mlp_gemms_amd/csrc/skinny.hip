@@ -392,12 +392,17 @@ hipError_t skinny_epi(int epi, const GemmArgs& a, hipStream_t s) {
   }
 }
 
-// The experts' products with a few rows an expert: workgroup b takes column block b % blocks of expert
-// b / blocks and streams its weights once for every 16 of the expert's rows (once, for most), K over its
-// waves as above; experts without rows cost their workgroups one look at the offsets. The workgroups
-// of "expert" `experts` fill the rows behind the last offset.
+// The experts' products with a few rows an expert: workgroup b takes column block b % blocks of up to 16 rows of one expert
+// and streams the expert's weights once, K over its waves as above. The first experts + 1 runs of blocks have the first 16
+// rows of each expert (one without rows costs its workgroups one look at the offsets) and all rows behind the last offset,
+// which are filled; the runs behind them have the further rows of experts that have more, 16 a run (as many runs as the
+// rows could need: most look at the offsets and end). 1000 rows of 128 experts, 2048 x 1376 gate and up: 267 us evenly
+// spread, 124 where all go to one expert (366 as turns of that expert's first workgroups).
+// Two waves a SIMD for the gated body, three for the other: what the compiler makes of the registers without the
+// attribute, three and five, streams slower (64 experts, 96 rows evenly 125 us against 122; 500 rows 145 against 137).
 template <typename T, int EPI, int WAVES, int NBUF>
-__global__ __launch_bounds__(64 * WAVES) void skinny_experts_kernel(const ExpertGemm a) {
+__global__ __launch_bounds__(64 * WAVES) __attribute__((amdgpu_waves_per_eu(epi_gated(EPI) ? 2 : 3, epi_gated(EPI) ? 2 : 3)))
+void skinny_experts_kernel(const ExpertGemm a) {
   constexpr bool GATED = epi_gated(EPI);
   constexpr int NB = GATED ? 2 : 1;
   __shared__ f32x4 red[WAVES][NB][64];
@@ -405,15 +410,25 @@ __global__ __launch_bounds__(64 * WAVES) void skinny_experts_kernel(const Expert
   const int r = lane & 15, q = lane >> 4;
   GemmArgs p = a.g;
   const int blocks = (p.N + 15) / 16;
-  const int e = blockIdx.x / blocks, n = (blockIdx.x % blocks) * 16 + r;
-  int row0, rows;
-  expert_rows(a.offsets, a.experts, a.rows, e, row0, rows);
-  row0 = __builtin_amdgcn_readfirstlane(row0);
-  rows = __builtin_amdgcn_readfirstlane(rows);
+  const int run = blockIdx.x / blocks, n = (blockIdx.x % blocks) * 16 + r;
   const bool row_ok = n < p.N;
+  int e = run, row0, M;
+  if (run <= a.experts) {
+    expert_rows(a.offsets, a.experts, a.rows, e, row0, M);
+    row0 = __builtin_amdgcn_readfirstlane(row0);
+    M = __builtin_amdgcn_readfirstlane(M);
+    if (M == 0) return;
+  } else {
+    const int want = run - a.experts - 1;
+    RowPiece t;
+    if (!find_row_piece<-1>(a.offsets, a.experts, a.rows, 16, [&](int total) { return want < total ? want : -1; }, t)) return;
+    e = t.e;
+    row0 = t.row0 + (t.index + 1) * 16;
+    M = t.rows - (t.index + 1) * 16;
+  }
   if (e == a.experts) {
     if (!row_ok) return;
-    for (int m = row0 + wave * 4 + q; m < row0 + rows; m += 4 * WAVES) {
+    for (int m = row0 + wave * 4 + q; m < row0 + M; m += 4 * WAVES) {
       if (p.flags & 1) {
         *reinterpret_cast<uint16_t*>(elem_ptr<T>(p.aux, m, p.ld_aux, n)) = 0;
         if (GATED) *reinterpret_cast<uint16_t*>(elem_ptr<T>(p.aux, m, p.ld_aux, p.half + n)) = 0;
@@ -423,8 +438,7 @@ __global__ __launch_bounds__(64 * WAVES) void skinny_experts_kernel(const Expert
     }
     return;
   }
-  p.bias0 = shift<T>(p.bias0, e * a.bias_stride);
-  p.bias1 = shift<T>(p.bias1, e * a.bias_stride);
+  M = min(M, 16);
   const int64_t wrow0 = e * a.w_stride + (int64_t)(row_ok ? n : 0) * p.ldb;
   const char* wrow[NB];
   wrow[0] = reinterpret_cast<const char*>(shift<T>(p.B0, wrow0));
@@ -432,76 +446,72 @@ __global__ __launch_bounds__(64 * WAVES) void skinny_experts_kernel(const Expert
   const int nblk = (p.K + kKBlock - 1) / kKBlock;
   const int b0 = wave * nblk / WAVES, nb = (wave + 1) * nblk / WAVES - b0;
 
-  for (int m0 = 0; m0 < rows; m0 += 16) {
-    const int M = min(16, rows - m0);   // token rows of this pass
-    const bool tok_ok = r < M;
-    const char* xrow = reinterpret_cast<const char*>(elem_ptr<T>(p.A, row0 + m0 + (tok_ok ? r : 0), p.lda, 0));
-    u32x4 xa[NBUF][4], wa[NBUF][NB][4];
-    auto load = [&](int b, int s) {
+  const bool tok_ok = r < M;
+  const char* xrow = reinterpret_cast<const char*>(elem_ptr<T>(p.A, row0 + (tok_ok ? r : 0), p.lda, 0));
+  u32x4 xa[NBUF][4], wa[NBUF][NB][4];
+  auto load = [&](int b, int s) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int k = b * kKBlock + c * 32 + q * 8;
-        const bool k_ok = k < p.K;
-        const int64_t off = (int64_t)k * (int64_t)sizeof(T);
+    for (int c = 0; c < 4; ++c) {
+      const int k = b * kKBlock + c * 32 + q * 8;
+      const bool k_ok = k < p.K;
+      const int64_t off = (int64_t)k * (int64_t)sizeof(T);
 #pragma unroll
-        for (int m = 0; m < NB; ++m)
-          wa[s][m][c] = (row_ok && k_ok) ? *reinterpret_cast<const u32x4*>(wrow[m] + off) : u32x4{0u, 0u, 0u, 0u};
-        xa[s][c] = (tok_ok && k_ok) ? *reinterpret_cast<const u32x4*>(xrow + off) : u32x4{0u, 0u, 0u, 0u};
-      }
-    };
-    f32x4 acc[NB];
-#pragma unroll
-    for (int m = 0; m < NB; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    auto compute = [&](int s) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int m = 0; m < NB; ++m) Mma16<T>::mma(xa[s][c], wa[s][m][c], acc[m]);
-    };
-#pragma unroll
-    for (int j = 0; j < NBUF - 1; ++j)
-      if (j < nb) load(b0 + j, j);
-    int i = 0;
-    for (; i + NBUF <= nb; i += NBUF) {
-#pragma unroll
-      for (int j = 0; j < NBUF; ++j) {
-        if (i + j + NBUF - 1 < nb) load(b0 + i + j + NBUF - 1, (j + NBUF - 1) % NBUF);
-        compute(j);
-      }
+      for (int m = 0; m < NB; ++m)
+        wa[s][m][c] = (row_ok && k_ok) ? *reinterpret_cast<const u32x4*>(wrow[m] + off) : u32x4{0u, 0u, 0u, 0u};
+      xa[s][c] = (tok_ok && k_ok) ? *reinterpret_cast<const u32x4*>(xrow + off) : u32x4{0u, 0u, 0u, 0u};
     }
+  };
+  f32x4 acc[NB];
 #pragma unroll
-    for (int j = 0; j < NBUF; ++j)
-      if (i + j < nb) compute(j);
+  for (int m = 0; m < NB; ++m) acc[m] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  auto compute = [&](int s) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+      for (int m = 0; m < NB; ++m) Mma16<T>::mma(xa[s][c], wa[s][m][c], acc[m]);
+  };
+#pragma unroll
+  for (int j = 0; j < NBUF - 1; ++j)
+    if (j < nb) load(b0 + j, j);
+  int i = 0;
+  for (; i + NBUF <= nb; i += NBUF) {
+#pragma unroll
+    for (int j = 0; j < NBUF; ++j) {
+      if (i + j + NBUF - 1 < nb) load(b0 + i + j + NBUF - 1, (j + NBUF - 1) % NBUF);
+      compute(j);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < NBUF; ++j)
+    if (i + j < nb) compute(j);
 
-    if (m0 > 0) __syncthreads();   // the first wave has read the last pass's sums
 #pragma unroll
-    for (int m = 0; m < NB; ++m) red[wave][m][lane] = acc[m];
-    __syncthreads();
-    if (wave == 0 && row_ok) {
-      f32x4 s0 = red[0][0][lane], s1 = red[0][NB - 1][lane];
+  for (int m = 0; m < NB; ++m) red[wave][m][lane] = acc[m];
+  __syncthreads();
+  if (wave == 0 && row_ok) {
+    f32x4 s0 = red[0][0][lane], s1 = red[0][NB - 1][lane];
 #pragma unroll
-      for (int w = 1; w < WAVES; ++w) {
-        s0 += red[w][0][lane];
-        if constexpr (GATED) s1 += red[w][1][lane];
-      }
-      float v[4] = {s0[0], s0[1], s0[2], s0[3]}, u[4] = {s1[0], s1[1], s1[2], s1[3]};
-      GemmArgs c = p;   // this pass's rows
-      const int64_t at = row0 + m0;
-      c.C0 = shift<T>(p.C0, at * p.ldc0);
-      c.aux = shift<T>(p.aux, at * p.ld_aux);
-      c.res = shift<T>(p.res, at * p.ld_res);
-      linear_finish<T, EPI>(c, M, q, n, v, u);
+    for (int w = 1; w < WAVES; ++w) {
+      s0 += red[w][0][lane];
+      if constexpr (GATED) s1 += red[w][1][lane];
     }
+    float v[4] = {s0[0], s0[1], s0[2], s0[3]}, u[4] = {s1[0], s1[1], s1[2], s1[3]};
+    GemmArgs c = p;   // these rows, of this expert
+    const int64_t at = row0;
+    c.C0 = shift<T>(p.C0, at * p.ldc0);
+    c.aux = shift<T>(p.aux, at * p.ld_aux);
+    c.res = shift<T>(p.res, at * p.ld_res);
+    c.bias0 = shift<T>(p.bias0, e * a.bias_stride);
+    c.bias1 = shift<T>(p.bias1, e * a.bias_stride);
+    linear_finish<T, EPI>(c, M, q, n, v, u);
   }
 }
 
 template <typename T, int EPI>
 hipError_t launch_skinny_experts(const ExpertGemm& a, hipStream_t s) {
-  const int64_t blocks = (int64_t)(a.experts + 1) * ((a.g.N + 15) / 16);
-  // Four waves, two buffers of loads: with three the gated body takes all registers, one wave a SIMD (96
-  // rows, 36 of 64 experts live, 2048 x 1376 gate and up: 110 us, against 78 us = 5.2 TB/s of weights);
-  // eight waves a workgroup are slower there (104 us) and no faster with few workgroups (4 rows of 2
-  // experts, 4096 x 512: 9.5 against 9.0 us).
+  const int64_t blocks = a.grid * (int64_t)((a.g.N + 15) / 16);
+  // Four waves, two buffers of loads: three are slower for the gated body (96 rows of 64 experts, unevenly, 2048 x
+  // 1376 gate and up: 68 us against 66) and even for the other; 66 us are 6.1 TB/s of the 36 live experts' weights.
   hipLaunchKernelGGL((skinny_experts_kernel<T, EPI, 4, 2>), dim3((unsigned)blocks), dim3(256), 0, s, a);
   return hipGetLastError();
 }

@@ -186,6 +186,23 @@ def test_products(p):
     check_linear(p.M, p.K, p.N, p.act, R.DT[p.dtype], experts=len(counts or ()), offsets=offsets_of(counts) if counts else None)
 
 
+# streaming (at most 8 rows an expert on average), experts of more than 16 rows among them
+CROWDED = [  # rows an expert, rows behind them, K, N
+    ([0, 0, 64, 0, 0, 0, 0, 0], 0, 264, 136), ([61, 0, 0, 0, 0, 0, 0, 0], 3, 136, 40), ([0] * 7 + [17], 30, 520, 24),
+    ([16, 33, 1, 40, 0, 15, 0, 0, 0, 0, 0, 0, 0, 0, 0, 17], 5, 2056, 72), ([1] * 60 + [130] + [0] * 39 + [200], 40, 136, 264),
+    ([0] * 200 + [900, 16, 17, 0, 32, 33] + [2] * 114, 50, 72, 40), ([0] * 1023 + [1500], 1, 40, 24),
+]
+
+
+@pytest.mark.parametrize("case", CROWDED, ids=lambda c: f"{len(c[0])}x{sum(c[0])}-{c[2]}-{c[3]}")
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_streamed_experts_of_many_rows(case, dtype):
+    counts, tail, K, N = case
+    assert sum(counts) + tail <= 8 * len(counts)
+    for act in ("none", "swiglu"):
+        check_linear(sum(counts) + tail, K, N, act, R.DT[dtype], experts=len(counts), offsets=offsets_of(counts))
+
+
 @pytest.mark.parametrize("p", [p for p in P.PATHS if p.counts], ids=lambda p: f"{p.M}x{p.K}x{p.N}-{p.act}-{p.dtype}-{len(p.counts)}")
 def test_an_experts_nan_stays_its_own(p):
     """Rows of one expert that are NaN reach no other expert's rows or gradients."""
