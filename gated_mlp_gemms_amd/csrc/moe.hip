@@ -478,10 +478,13 @@ template <typename T> struct Piece {   // 16 bytes of a row
 };
 
 // Rows that no cache will hold until they are read again are streamed (NT: non-temporal loads of the
-// rows read once, non-temporal stores): from 100 MB of sorted rows on. Bound by HBM. 49152 rows of 2048 bf16
-// (201 MB): gather 67 -> 55 us (4.2 TB/s), combine 55 -> 45 (5.9), its gradient 93 -> 86 (5.0), gather's 50 -> 41 (5.7);
-// 15009 rows of 1036 fp32 (62 MB): gather's gradient 17 -> 20 us, the others even.
-constexpr int64_t kStreamBytes = 100 << 20;
+// rows read once, non-temporal stores): from 32 MiB of sorted rows on. Bound by HBM. Gather, combine and both gradients
+// one after another, rows in caches and streamed (us): 6 rows of 2048 bf16 a token, 20 MB 31.7 and 32.5, 30 MB 46 and 41,
+// 45 MB 65 and 56, 104 MB 151 and 124, 200 MB 267 and 222 (gather 68 -> 54, combine 54 -> 43, its gradient 88 -> 84,
+// gather's 49 -> 40); 3 rows of 1036 fp32, 20 MB 37.5 and 38.4, 45 MB 77 and 71, 62 MB 98 and 92. The two products between
+// gather and combine of a layer do not miss the rows: 2048 x 1376, 4 a token, with them 20 MB 121 and 121, 45 MB 216 and
+// 208, 104 MB 388 and 395, 150 MB 554 and 552; 2048 x 256, 6 a token, 20 MB 53 and 55, 62 MB 118 and 105, 150 MB 250 and 230.
+constexpr int64_t kStreamBytes = 32 << 20;
 inline bool stream_rows(int64_t rows, int pieces) { return rows * pieces * 16 >= kStreamBytes; }
 
 template <bool NT> __device__ __forceinline__ u32x4 load_piece(const u32x4* p) {

@@ -177,6 +177,39 @@ def test_nan_comes_through(act, M, dtype):
         assert torch.isfinite(y[rest]).all() and torch.isfinite(pre[rest]).all()
 
 
+# ---- rows ---------------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("T,d,dtype", [(2100, 4096, "bf16"), (1500, 4096, "f16"), (2200, 2060, "f32")])
+def test_streamed_rows_equal_rows_in_caches(T, d, dtype):
+    """From 32 MiB of sorted rows on they are streamed: the same values as of the tokens in eight parts, which are not."""
+    g, dt, E, k, parts = gen(22), R.DT[dtype], 24, 3, 8
+    n, size = T * k, torch.empty(0, dtype=dt).element_size()
+    assert n * d * size >= 32 << 20 and -(-T // parts) * k * d * size < 16 << 20
+    ids = torch.rand(T, E, device=DEV, generator=g).topk(k, dim=1)[1].to(torch.int32)
+    ids[torch.rand(T, k, device=DEV, generator=g) < 0.1] = -1
+    x, dout, w = normal(g, T, d, dtype=dt), normal(g, T, d, dtype=dt), torch.rand(T, k, device=DEV, generator=g)
+    each = normal(g, n, d, dtype=dt)               # a row of ys for each slot
+
+    def layer(a, b):
+        m = (b - a) * k
+        off, row, slot = (poison(c, dtype=torch.int32) for c in (E + 1, m, m))
+        gm.moe_sort(ids[a:b].contiguous(), E, off, row, slot)
+        ys = each[a * k:b * k][slot.long()]
+        xs, out, dys, dw, dx = (poison(*s, dtype=t) for s, t in (
+            ((m, d), dt), ((b - a, d), dt), ((m, d), dt), ((b - a, k), torch.float32), ((b - a, d), dt)))
+        gm.moe_gather(x[a:b].contiguous(), slot, off, xs)
+        gm.moe_combine(ys, w[a:b].contiguous(), row, off, out, residual=x[a:b].contiguous())
+        gm.moe_combine_bwd(dout[a:b].contiguous(), ys, w[a:b].contiguous(), row, slot, off, dys, dw)
+        gm.moe_gather_bwd(ys, row, off, dx)
+        at = row.long()                            # by slot again
+        return xs[at], out, dys[at], dw, dx
+
+    cuts = [T * i // parts for i in range(parts + 1)]
+    whole, pieces = layer(0, T), [layer(a, b) for a, b in zip(cuts, cuts[1:])]
+    for i, t in enumerate(whole):
+        assert torch.equal(t, torch.cat([p[i] for p in pieces])), i
+
+
 # ---- every kernel of the products ---------------------------------------------------------------
 
 @pytest.mark.parametrize("p", P.PATHS, ids=lambda p: f"{p.M}x{p.K}x{p.N}-{p.act}-{p.dtype}-{len(p.counts or ())}")
