@@ -88,8 +88,12 @@ hipError_t run_expert_bwd_f32(TileShape tile, const ExpertBwd& a, hipStream_t s)
 // 576 of 3 (1952 x 672) 19 and 23, 4000 of 16 (512 x 1024) 37 and 31.
 constexpr int kStripTileM = 64, kStripTileN = 128, kStripRows = 32, kStripRowsSmall = 200;
 // Weight gradients from this size on are stored past the caches (16-bit; in strips only with rows of whole 128-byte
-// lines: a strip's store of part of a line goes to memory on its own). Both products of 4096 rows of 32 experts of
-// 2048 x 1376: 127 -> 95 us.
+// lines: a strip's store of part of a line goes to memory on its own). Both products, into caches and past them (us), 24
+// rows an expert of 2048 x 1376 gate and up: gradients of 50 MB 40 and 37, 90 MB 65 and 54, 110 MB 78 and 72, 180 MB 114
+// and 106; 400 rows: 50 MB 77 and 69, 110 MB 139 and 137, 180 MB 229 and 225. A reader right after the call would rather
+// find them in the caches (24 rows, the gradients scaled by a pass of its own: 50 MB 57 and 58, 90 MB 90 and 95, 110 MB
+// 109 and 114, 180 MB 163 and 175); a training step reads them when the other layers' have passed, and the larger they
+// are the less of them a cache has kept.
 constexpr int64_t kStreamGradBytes = 100 << 20;
 // The partial sums of run_expert_bwd added up (nothing without any).
 hipError_t run_expert_join(DType io, const ExpertBwd& a, hipStream_t s);
