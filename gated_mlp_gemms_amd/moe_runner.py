@@ -1,5 +1,7 @@
 """Device buffers for one mixture-of-experts layer and the calls of its training step and its inference
-forward, as ``runner.py`` holds them for the MLP. It only marshals: every step runs in the library's kernels.
+forward, as ``runner.py`` holds them for the MLP. Every operator runs in the library's kernels; torch only adds ``dout``
+to the router's part of dx and copies the columns of a router whose number of experts is not a multiple of a 16-byte
+row's (8, fp32 4).
 
     out = x + sum over a token's k experts of weight (act(x W_gate^T) x W_up^T) W_down^T
 
@@ -13,7 +15,7 @@ import torch
 
 from . import GATED_ACTS
 from .moe import (linear_bwd, linear_fwd, linear_workspace_bytes, make_linear_desc, moe_combine, moe_combine_bwd,
-                  moe_gather, moe_gather_bwd, moe_route, moe_route_bwd, moe_sort, moe_sort_workspace_bytes)
+                  moe_gather, moe_route, moe_route_bwd, moe_sort, moe_sort_workspace_bytes)
 
 
 class MoeRunner:
@@ -60,7 +62,8 @@ class MoeRunner:
             self.dout = t["dout"]
             self.preact = new(n, 2 * h if gated else h)
             self.dys, self.dweights, self.da, self.dxs = new(n, d), new(T, k, of=f32), new(n, h), new(n, d)
-            self.dlogits, self.dx_rows, self.dx_router, self.dx = new(T, E), new(T, d), new(T, d), new(T, d)
+            self.dlogits, self.dx_router, self.dx = new(T, E), new(T, d), new(T, d)
+            self.ones = new(T, k, of=f32).fill_(1.0)   # the weights of the experts' rows in dx
             like = lambda v: torch.empty_like(v) if v is not None else None   # noqa: E731
             self.wide_dlogits = self.dlogits
             self.d_router, self.dw1, self.dw_up, self.dw2 = like(self.router), like(self.w1), like(self.w_up), like(self.w2)
@@ -98,7 +101,6 @@ class MoeRunner:
                    dbias=self.db2, workspace=self.ws)
         linear_bwd(self.up_desc, self.da, self.xs, self.w1, w_up=self.w_up, preact=self.preact, offsets=self.offsets,
                    dx=self.dxs, dw=self.dw1, dw_up=self.dw_up, dbias=self.db1, dbias_up=self.db_up, workspace=self.ws)
-        moe_gather_bwd(self.dxs, self.row_of, self.offsets, self.dx_rows)
         moe_route_bwd(self.logits, self.ids, self.dweights, self.dlogits, score=self.score, renorm=self.renorm)
         if self.wide_dlogits is not self.dlogits:
             self.wide_dlogits[:, : self.experts].copy_(self.dlogits)
@@ -106,8 +108,9 @@ class MoeRunner:
                    workspace=self.ws)
         if self.wide_d_router is not self.d_router:
             self.d_router.copy_(self.wide_d_router[: self.experts])
-        torch.add(self.dx_rows, self.dx_router, out=self.dx)
-        self.dx.add_(self.dout)
+        # summed in fp32 and rounded once; the router's part has been rounded, and with dout's once more
+        torch.add(self.dx_router, self.dout, out=self.dx)
+        moe_combine(self.dxs, self.ones, self.row_of, self.offsets, self.dx, residual=self.dx)
 
     def step(self):
         self.forward()

@@ -261,3 +261,20 @@ def test_an_experts_nan_stays_its_own(p):
     others = torch.arange(E, device=DEV) != bad
     for t in filter(lambda t: t is not None, (dw, dwu, db, dbu)):
         assert torch.isfinite(t[others]).all() and torch.isnan(t[bad]).any()
+
+
+# ---- the layer's runner -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("experts", [8, 7])
+def test_runner_sums_dx_in_fp32(experts):
+    """dx of a 16-bit layer: the experts' rows summed in fp32 onto dout plus the router's part, and rounded once."""
+    from gated_mlp_gemms_amd.moe_runner import MoeRunner, moe_tensors
+
+    size = dict(act="swiglu", dtype="bf16", tokens=70, width=136, hidden=72, experts=experts)
+    r = MoeRunner(choices=5, tensors=moe_tensors(seed=7, **size), **size)
+    r.step()
+    base = (r.dx_router.float() + r.dout.float()).bfloat16().float()
+    row, acc = r.row_of.long().reshape(70, 5), torch.zeros(70, 136, device=DEV)
+    for j in range(5):
+        acc = acc + r.dxs.float()[row[:, j]]
+    assert torch.equal(r.dx, (acc + base).bfloat16())
