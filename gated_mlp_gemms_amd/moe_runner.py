@@ -5,7 +5,7 @@ row's (8, fp32 4).
 
     out = x + sum over a token's k experts of weight (act(x W_gate^T) x W_up^T) W_down^T
 
-(the residual stream x goes into the combine). As a command it times one layer::
+(the residual stream x goes into the combine; where x is a norm of it, the stream is a tensor of its own). As a command it times one layer::
 
     python -m gated_mlp_gemms_amd.moe_runner --tokens 4096 --width 2048 --hidden 1376 --experts 32 --choices 4
 """
@@ -21,7 +21,8 @@ from .moe import (linear_bwd, linear_fwd, linear_workspace_bytes, make_linear_de
 class MoeRunner:
     """``tokens`` rows of ``width`` through ``experts`` experts of ``hidden`` units, ``choices`` a token.
     ``tensors``: x, dout [tokens, width]; router [experts, width]; w_gate, w_up (gated) or w1
-    [experts, hidden, width]; w_down or w2 [experts, width, hidden]; optional b_gate, b_up or b1, b_down or b2.
+    [experts, hidden, width]; w_down or w2 [experts, width, hidden]; optional b_gate, b_up or b1, b_down or b2; optional
+    residual [tokens, width], added to the output in x's place: its gradient is dout, which dx then leaves out.
     ``train`` False holds no more than ``forward_infer`` needs."""
 
     def __init__(self, *, act, dtype, tokens, width, hidden, experts, choices, tensors, score="softmax", renorm=True,
@@ -33,7 +34,7 @@ class MoeRunner:
         T, d, h, E, k = int(tokens), int(width), int(hidden), int(experts), int(choices)
         n = T * k
         self.train, self.score, self.renorm, self.experts, self.dtype = train, score, renorm, E, dt
-        self.x, self.router = t["x"], t["router"]
+        self.x, self.router, self.residual = t["x"], t["router"], t.get("residual", t["x"])
         self.w1, self.w_up, self.w2 = t["w_gate" if gated else "w1"], t.get("w_up"), t["w_down" if gated else "w2"]
         self.b1, self.b_up, self.b2 = t.get("b_gate" if gated else "b1"), t.get("b_up"), t.get("b_down" if gated else "b2")
 
@@ -84,7 +85,7 @@ class MoeRunner:
         linear_fwd(self.up_desc, self.xs, self.w1, self.a, w_up=self.w_up, bias=self.b1, bias_up=self.b_up,
                    offsets=self.offsets, preact=preact, workspace=self.ws)
         linear_fwd(self.down_desc, self.a, self.w2, self.ys, bias=self.b2, offsets=self.offsets, workspace=self.ws)
-        moe_combine(self.ys, self.weights, self.row_of, self.offsets, self.out, residual=self.x)
+        moe_combine(self.ys, self.weights, self.row_of, self.offsets, self.out, residual=self.residual)
         return self.out
 
     def forward(self):
@@ -94,8 +95,8 @@ class MoeRunner:
         return self._forward(None)
 
     def backward(self):
-        """Every gradient of :meth:`forward` against ``dout``; ``dx`` is the sum of the residual's, the experts'
-        rows' and the router's."""
+        """Every gradient of :meth:`forward` against ``dout``; ``dx`` is the sum of the experts' rows', the router's
+        and, where x is the residual, dout."""
         moe_combine_bwd(self.dout, self.ys, self.weights, self.row_of, self.slot_of, self.offsets, self.dys, self.dweights)
         linear_bwd(self.down_desc, self.dys, self.a, self.w2, offsets=self.offsets, dx=self.da, dw=self.dw2,
                    dbias=self.db2, workspace=self.ws)
@@ -109,8 +110,10 @@ class MoeRunner:
         if self.wide_d_router is not self.d_router:
             self.d_router.copy_(self.wide_d_router[: self.experts])
         # summed in fp32 and rounded once; the router's part has been rounded, and with dout's once more
-        torch.add(self.dx_router, self.dout, out=self.dx)
-        moe_combine(self.dxs, self.ones, self.row_of, self.offsets, self.dx, residual=self.dx)
+        rest = self.dx_router
+        if self.residual is self.x:
+            rest = torch.add(self.dx_router, self.dout, out=self.dx)
+        moe_combine(self.dxs, self.ones, self.row_of, self.offsets, self.dx, residual=rest)
 
     def step(self):
         self.forward()

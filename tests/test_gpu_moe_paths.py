@@ -278,3 +278,33 @@ def test_runner_sums_dx_in_fp32(experts):
     for j in range(5):
         acc = acc + r.dxs.float()[row[:, j]]
     assert torch.equal(r.dx, (acc + base).bfloat16())
+
+
+def test_runner_with_a_residual_of_its_own():
+    """A norm in front: x is the norm of the stream h, which the output is added to. fp32, against autograd of the formula
+    in float64 on the CPU, through the norm; the bound is test_gpu_moe.py's, for one more product's depth."""
+    from gated_mlp_gemms_amd.moe_runner import MoeRunner, moe_tensors
+
+    size = dict(act="swiglu", dtype="f32", tokens=45, width=32, hidden=40, experts=8)
+    t, h = moe_tensors(seed=8, **size), normal(gen(9), 45, 32)
+    norm = lambda h: h / (h.square().mean(dim=1, keepdim=True) + 1e-5).sqrt()   # noqa: E731
+    t.update(x=norm(h.double()).float(), residual=h)
+    r = MoeRunner(choices=3, tensors=t, **size)
+    r.step()
+    leaf = {k: t[k].double().cpu().requires_grad_() for k in ("residual", "router", "w_gate", "w_up", "w_down")}
+    x, ids = norm(leaf["residual"]), r.ids.long().cpu()
+    x.retain_grad()
+    w = torch.softmax((x @ leaf["router"].T).gather(1, ids), dim=1)
+    out = leaf["residual"]
+    for j in range(3):
+        e = ids[:, j]
+        g, u = ((leaf[n][e] @ x[:, :, None])[:, :, 0] for n in ("w_gate", "w_up"))
+        out = out + w[:, j:j + 1] * (leaf["w_down"][e] @ (torch.nn.functional.silu(g) * u)[:, :, None])[:, :, 0]
+    (out * t["dout"].double().cpu()).sum().backward()
+    grads = r.grads()
+    pairs = [("out", r.out, out.detach()), ("dx", grads["dx"], x.grad), ("d_router", grads["d_router"], leaf["router"].grad),
+             ("dw1", grads["dw1"], leaf["w_gate"].grad), ("dw_up", grads["dw_up"], leaf["w_up"].grad),
+             ("dw2", grads["dw2"], leaf["w_down"].grad)]
+    for name, a, b in pairs:
+        R.check(name, a.cpu(), b, torch.full_like(b, 2400 * R.U32 * b.abs().max().item()))
+    assert torch.equal(MoeRunner(choices=3, tensors=t, train=False, **size).forward_infer(), r.out)
