@@ -86,8 +86,8 @@ struct BiasGrad {
 //  * piece_rows: an expert of more rows has its weight gradient summed over pieces of that many, fp32 sums in
 //    part_w [slots][M][N], slots counted over such experts in order, max_slots at most (0: never).
 // run_expert_join adds up either.
-//  * strip_parts > 0: few rows an expert. dx in 64 x 128 tiles; the weight gradients 64 columns of x a workgroup, every
-//    strip_parts-th of the 128-row tiles along dz's columns one after another (expert_grad_strip).
+//  * strip_parts > 0: few rows an expert. dx in 64 x 128 tiles; the weight gradients 128 columns of x a workgroup
+//    (kStripTileN), every strip_parts-th of the 64-column tiles of dz (kStripTileM) one after another (expert_grad_strip).
 struct ExpertBwd {
   ExpertGemm dx, dw;
   BiasGrad db;

@@ -370,7 +370,7 @@ __global__ __launch_bounds__(kSortThreads) void sort_place_kernel(const int* __r
   __syncthreads();
 
   // thread b: bin b's count over every chunk and over the chunks before this one
-  const int bin = tid;   // nb <= kSortThreads + 1; the bin past the last thread is done by thread 0
+  const int bin = tid;   // nb <= kSortThreads + 1; the bin past the last thread is done by that thread, which holds the scan's total
   auto totals = [&](int b, int& all, int& before) {
     all = before = 0;
     if (b >= nb) return;

@@ -43,7 +43,10 @@ class MoeRunner:
 
         i32, f32 = torch.int32, torch.float32
         self.logits, self.ids, self.weights = new(T, E), new(T, k, of=i32), new(T, k, of=f32)
-        # a linear layer's rows are 16-byte aligned: for another number of experts the router's product has
+        # The logits have the layer's type, as every tensor of a linear layer does: of 16 bits, a score is off by half a
+        # step of that type, so near ties between experts may fall either way. moe_route takes fp32 scores from
+        # wherever a program has them.
+        # A linear layer's rows are 16-byte aligned: for another number of experts the router's product has
         # columns of zero weights behind, which its logits leave out
         q = 4 if dt == torch.float32 else 8
         Er = (E + q - 1) // q * q

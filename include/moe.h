@@ -46,7 +46,7 @@ typedef enum moe_score { MOE_SOFTMAX = 0, MOE_SIGMOID = 1 } moe_score;
  * logits [T, E] in dtype (f32, bf16, f16), scores of -inf allowed: such an expert is chosen last,
  * with weight 0; where every chosen probability is 0 all weights are 0 (never 0 / 0). A sigmoid counts as 0
  * below a score of -104 (2^-150); above, normalised weights are exact ratios also where the sigmoids
- * themselves are below fp32's range.
+ * themselves are below fp32's range. A score of +inf has sigmoid 1; softmax over one is NaN.
  * 1 <= E <= MOE_MAX_EXPERTS, 1 <= k <= min(E, MOE_MAX_CHOICES).
  */
 mlp_status moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t k, int score, int renorm,

@@ -219,6 +219,17 @@ def test_products(p):
     check_linear(p.M, p.K, p.N, p.act, R.DT[p.dtype], experts=len(counts or ()), offsets=offsets_of(counts) if counts else None)
 
 
+@pytest.mark.parametrize("E", [256, 319, 320, 321])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_numbers_of_experts_around_the_searchs(E, dtype):
+    """The search for a workgroup's rows holds 1, 5 or 17 experts a lane: up to 63, up to 319, above."""
+    g = torch.Generator().manual_seed(E)
+    for most in (3, 20):
+        counts = [int(c) for c in torch.randint(0, most, (E - 2,), generator=g)] + [0, 5]
+        check_linear(sum(counts) + 3, 40, 24, "swiglu", R.DT[dtype], experts=E, offsets=offsets_of(counts))
+        check_linear(sum(counts), 40, 24, "none", R.DT[dtype], experts=E, offsets=offsets_of(counts))
+
+
 # streaming (at most 8 rows an expert on average), experts of more than 16 rows among them
 CROWDED = [  # rows an expert, rows behind them, K, N
     ([0, 0, 64, 0, 0, 0, 0, 0], 0, 264, 136), ([61, 0, 0, 0, 0, 0, 0, 0], 3, 136, 40), ([0] * 7 + [17], 30, 520, 24),
