@@ -292,49 +292,67 @@ __device__ __forceinline__ void gated_act_grad(int fn, float gm, int inside, con
 __device__ __forceinline__ float gelu_gate(float z) {
   return sigmoidf_(2.0f * kGeluC * (z + kGeluK * (z * z) * z));
 }
-// A maximum with 0 would turn a NaN into 0 and hide it; this keeps it.
-__device__ __forceinline__ float linear_relu(float z) { return z <= 0.0f ? 0.0f : z; }
+// The larger of z and 0; a NaN stays one (fmaxf would turn it into 0 and hide it).
+__device__ __forceinline__ float linear_relu(float z) { return __builtin_elementwise_maximum(z, 0.0f); }
 template <int N>
 __device__ __forceinline__ void linear_fn(int fn, const float (&z)[N], float (&f)[N]) {
-  if (fn == FN_GELU_TANH) {
+  switch (fn) {
+    case FN_SILU:
 #pragma unroll
-    for (int r = 0; r < N; ++r) f[r] = z[r] * gelu_gate(z[r]);
-  } else if (fn == FN_RELU || fn == FN_RELU_SQ) {
+      for (int r = 0; r < N; ++r) f[r] = z[r] * sigmoidf_(z[r]);
+      break;
+    case FN_GELU_TANH:
 #pragma unroll
-    for (int r = 0; r < N; ++r) {
-      const float t = linear_relu(z[r]);
-      f[r] = fn == FN_RELU ? t : t * t;
-    }
-  } else {
-    act_fn<N>(fn, z, f);
+      for (int r = 0; r < N; ++r) f[r] = z[r] * gelu_gate(z[r]);
+      break;
+    case FN_RELU:
+#pragma unroll
+      for (int r = 0; r < N; ++r) f[r] = linear_relu(z[r]);
+      break;
+    case FN_SIGMOID:
+#pragma unroll
+      for (int r = 0; r < N; ++r) f[r] = sigmoidf_(z[r]);
+      break;
+    default:   // FN_RELU_SQ
+#pragma unroll
+      for (int r = 0; r < N; ++r) { const float t = linear_relu(z[r]); f[r] = t * t; }
   }
 }
 template <int N>
 __device__ __forceinline__ void linear_fn_grad(int fn, const float (&z)[N], float (&f)[N], float (&df)[N]) {
-  if (fn == FN_GELU_TANH) {
+  switch (fn) {
+    case FN_SILU:
 #pragma unroll
-    for (int r = 0; r < N; ++r) {
-      const float s = gelu_gate(z[r]);
-      const float c = __builtin_amdgcn_fmed3f(z[r], -16.0f, 16.0f);   // beyond, s or 1 - s is 0, and z z may overflow
-      f[r] = z[r] * s;
-      df[r] = s * (1.0f + c * (1.0f - s) * (2.0f * kGeluC * (1.0f + 3.0f * kGeluK * (c * c))));
-    }
-  } else if (fn == FN_RELU || fn == FN_RELU_SQ) {
+      for (int r = 0; r < N; ++r) {
+        const float s = sigmoidf_(z[r]);
+        f[r] = z[r] * s;
+        df[r] = s * (1.0f + z[r] * (1.0f - s));
+      }
+      break;
+    case FN_GELU_TANH:
 #pragma unroll
-    for (int r = 0; r < N; ++r) {
-      const float t = linear_relu(z[r]);
-      f[r] = fn == FN_RELU ? t : t * t;
-      df[r] = fn == FN_RELU ? (z[r] > 0.0f ? 1.0f : 0.0f) : 2.0f * t;
-    }
-  } else if (fn == FN_SIGMOID) {   // for z > 0, 1 - s of a rounded s cancels: 1 - s = s exp(-z)
+      for (int r = 0; r < N; ++r) {
+        const float s = gelu_gate(z[r]);
+        const float c = __builtin_amdgcn_fmed3f(z[r], -16.0f, 16.0f);   // beyond, s or 1 - s is 0, and z z may overflow
+        f[r] = z[r] * s;
+        df[r] = s * (1.0f + c * (1.0f - s) * (2.0f * kGeluC * (1.0f + 3.0f * kGeluK * (c * c))));
+      }
+      break;
+    case FN_RELU:
 #pragma unroll
-    for (int r = 0; r < N; ++r) {
-      const float e = __expf(-z[r]), s = __builtin_amdgcn_rcpf(1.0f + e);
-      f[r] = s;
-      df[r] = s * (z[r] > 0.0f ? s * e : 1.0f - s);
-    }
-  } else {
-    act_fn_grad<N>(fn, z, f, df);
+      for (int r = 0; r < N; ++r) { f[r] = linear_relu(z[r]); df[r] = z[r] > 0.0f ? 1.0f : 0.0f; }
+      break;
+    case FN_SIGMOID:   // for z > 0, 1 - s of a rounded s cancels: 1 - s = s exp(-z)
+#pragma unroll
+      for (int r = 0; r < N; ++r) {
+        const float e = __expf(-z[r]), s = __builtin_amdgcn_rcpf(1.0f + e);
+        f[r] = s;
+        df[r] = s * (z[r] > 0.0f ? s * e : 1.0f - s);
+      }
+      break;
+    default:   // FN_RELU_SQ
+#pragma unroll
+      for (int r = 0; r < N; ++r) { const float t = linear_relu(z[r]); f[r] = t * t; df[r] = 2.0f * t; }
   }
 }
 
