@@ -26,8 +26,9 @@ __device__ __forceinline__ void expert_rows(const int* offsets, int experts, int
     n = e == 0 ? rows : 0;
     return;
   }
-  row0 = min(max(offsets[min(e, experts)], 0), rows);
-  const int end = e < experts ? min(max(offsets[e + 1], row0), rows) : rows;
+  const int from = offsets[min(e, experts)], to = offsets[min(e + 1, experts)];   // one trip to memory
+  row0 = min(max(from, 0), rows);
+  const int end = e < experts ? min(max(to, row0), rows) : rows;
   n = e <= experts ? end - row0 : 0;
 }
 
@@ -103,8 +104,9 @@ __device__ __forceinline__ bool find_row_piece_of(const int* offsets, int expert
 template <int LEAST = 0, typename Want>
 __device__ __forceinline__ bool find_row_piece(const int* offsets, int experts, int rows, int step, Want want,
                                                RowPiece& out) {
-  if (experts < 64) return find_row_piece_of<1, LEAST>(offsets, experts, rows, step, want, out);
-  if (experts < 320) return find_row_piece_of<5, LEAST>(offsets, experts, rows, step, want, out);
+  constexpr int kTail = LEAST == 0 ? 1 : 0;   // the rows behind the last offset take a place
+  if (experts <= 64 - kTail) return find_row_piece_of<1, LEAST>(offsets, experts, rows, step, want, out);
+  if (experts <= 256 - kTail) return find_row_piece_of<4, LEAST>(offsets, experts, rows, step, want, out);
   return find_row_piece_of<17, LEAST>(offsets, experts, rows, step, want, out);
 }
 

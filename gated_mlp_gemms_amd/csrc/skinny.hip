@@ -412,6 +412,13 @@ void skinny_experts_kernel(const ExpertGemm a) {
   const int blocks = (p.N + 15) / 16;
   const int run = blockIdx.x / blocks, n = (blockIdx.x % blocks) * 16 + r;
   const bool row_ok = n < p.N;
+  // (what does not depend on the rows stands before the search for them: the arguments arrive while the offsets do)
+  const int64_t wrow0 = (int64_t)(row_ok ? n : 0) * p.ldb;
+  const char* wrow[NB];
+  wrow[0] = reinterpret_cast<const char*>(shift<T>(p.B0, wrow0));
+  if constexpr (GATED) wrow[1] = reinterpret_cast<const char*>(shift<T>(p.B1, wrow0));
+  const int nblk = (p.K + kKBlock - 1) / kKBlock;
+  const int b0 = wave * nblk / WAVES, nb = (wave + 1) * nblk / WAVES - b0;
   int e = run, row0, M;
   if (run <= a.experts) {
     expert_rows(a.offsets, a.experts, a.rows, e, row0, M);
@@ -439,13 +446,10 @@ void skinny_experts_kernel(const ExpertGemm a) {
     return;
   }
   M = min(M, 16);
-  const int64_t wrow0 = e * a.w_stride + (int64_t)(row_ok ? n : 0) * p.ldb;
-  const char* wrow[NB];
-  wrow[0] = reinterpret_cast<const char*>(shift<T>(p.B0, wrow0));
-  if constexpr (GATED) wrow[1] = reinterpret_cast<const char*>(shift<T>(p.B1, wrow0));
-  const int nblk = (p.K + kKBlock - 1) / kKBlock;
-  const int b0 = wave * nblk / WAVES, nb = (wave + 1) * nblk / WAVES - b0;
-
+  p.bias0 = shift<T>(p.bias0, e * a.bias_stride);
+  p.bias1 = shift<T>(p.bias1, e * a.bias_stride);
+#pragma unroll
+  for (int m = 0; m < NB; ++m) wrow[m] += e * a.w_stride * (int64_t)sizeof(T);
   const bool tok_ok = r < M;
   const char* xrow = reinterpret_cast<const char*>(elem_ptr<T>(p.A, row0 + (tok_ok ? r : 0), p.lda, 0));
   u32x4 xa[NBUF][4], wa[NBUF][NB][4];
@@ -501,8 +505,6 @@ void skinny_experts_kernel(const ExpertGemm a) {
     c.C0 = shift<T>(p.C0, at * p.ldc0);
     c.aux = shift<T>(p.aux, at * p.ld_aux);
     c.res = shift<T>(p.res, at * p.ld_res);
-    c.bias0 = shift<T>(p.bias0, e * a.bias_stride);
-    c.bias1 = shift<T>(p.bias1, e * a.bias_stride);
     linear_finish<T, EPI>(c, M, q, n, v, u);
   }
 }

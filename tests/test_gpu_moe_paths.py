@@ -219,10 +219,11 @@ def test_products(p):
     check_linear(p.M, p.K, p.N, p.act, R.DT[p.dtype], experts=len(counts or ()), offsets=offsets_of(counts) if counts else None)
 
 
-@pytest.mark.parametrize("E", [256, 319, 320, 321])
+@pytest.mark.parametrize("E", [255, 256, 257, 319, 320, 321])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_numbers_of_experts_around_the_searchs(E, dtype):
-    """The search for a workgroup's rows holds 1, 5 or 17 experts a lane: up to 63, up to 319, above."""
+    """The search for a workgroup's rows holds 1, 4 or 17 experts a lane: up to 64, up to 256, above (one less where the
+    rows behind the last offset count). In 16 bits few rows are streamed, many in tiles; in fp32 all in tiles."""
     g = torch.Generator().manual_seed(E)
     for most in (3, 20):
         counts = [int(c) for c in torch.randint(0, most, (E - 2,), generator=g)] + [0, 5]
