@@ -99,8 +99,10 @@ constexpr int64_t kStreamGradBytes = 100 << 20;
 hipError_t run_expert_join(DType io, const ExpertBwd& a, hipStream_t s);
 // The forward with a few rows an expert, 16-bit (g.N output columns, any rows; grid: runs of column blocks).
 // Taken up to kExpertFewRows rows an expert on average (an expert's weights are streamed again for every 16 of its rows).
-// Uneven rows, against the tiles that the plan takes above (us): 64 experts of 2048 x 1376 gate and up, 96 rows 76 and 88,
-// 256 129 and 145, 512 150 and 127, 768 173 and 126; 8 of 2048 x 5504 gate and up, 64 rows 75 and 80, 96 83 and 81.
+// Streamed and in tiles (us, even and uneven rows): at 8 rows an expert, 4 experts of 1024 x 1024 4.4 and 8.7, 32 of 512 x 264
+// 5-7 and 7, 8 of 2048 x 5504 gate and up 70-75 and 80, 16 of 4096 x 1408 gate and up 75 and 76, 64 of 1376 x 2048 79 and 73,
+// 64 of 2048 x 1376 gate and up 139-149 and 124, 128 of 1024 x 512 27-31 and 24-29; at 4 rows, in the same order, 4.3 and
+// 8.7, 5-9 and 7, 66 and 79, 72 and 77, 68 and 70, 125-129 and 137, 25 and 24. The small ones gain most, and a few large ones lose.
 constexpr int kExpertFewRows = 8;
 hipError_t run_skinny_experts(DType in, int epi, const ExpertGemm& a, hipStream_t s);
 
