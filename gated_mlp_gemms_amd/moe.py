@@ -2,8 +2,8 @@
 linear layer with its epilogue, experts' products, and their gradients.
 
 As in the rest of the package the functions carry the C entry points' names, write into buffers the
-caller passes, take a workspace (or allocate one with torch) and run on the current stream of their
-tensors' device unless ``stream`` is given. Sizes come from the tensors, so every tensor's dtype, shape
+caller passes, take a workspace (or allocate one with torch, on the stream that the call runs on) and run on
+the current stream of their tensors' device unless ``stream`` is given. Sizes come from the tensors, so every tensor's dtype, shape
 and layout (contiguous, on one GPU) is checked first (``ValueError``); what the library refuses raises
 ``MlpError``. One training step of a layer of E experts, k a token::
 
