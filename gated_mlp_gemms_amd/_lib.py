@@ -1,4 +1,4 @@
-"""ctypes view of ``include/mlp.h`` and the loaded ``libgated_mlp.so`` (marshalling only)."""
+"""ctypes view of ``include/mlp.h``, ``moe.h``, ``norm.h`` and the loaded ``libgated_mlp.so`` (marshalling only)."""
 from __future__ import annotations
 
 import ctypes as C
@@ -75,6 +75,9 @@ class LinearDesc(C.Structure):
 _MOE_SIGNATURES = {
     "moe_route": (C.c_int, [_P, _I32, _I64, _I64, _I64, _I32, _I32, _P, _P, _P]),
     "moe_route_bwd": (C.c_int, [_P, _P, _P, _I32, _I64, _I64, _I64, _I32, _I32, _P, _P]),
+    "moe_balance_workspace_bytes": (C.c_size_t, [_I64, _I64]),
+    "moe_balance": (C.c_int, [_P, _P, _P, _I32, _I64, _I64, _I64, _I32, _P, _P, _P, _P, C.c_size_t, _P]),
+    "moe_balance_bwd": (C.c_int, [_P] * 6 + [_I32, _I64, _I64, _I64, _I32, _I32, _P, _P]),
     "moe_sort_workspace_bytes": (C.c_size_t, [_I64, _I64]),
     "moe_sort": (C.c_int, [_P, _I64, _I64, _P, _P, _P, _P, C.c_size_t, _P]),
     "moe_gather": (C.c_int, [_P, _P, _P, _I32, _I64, _I64, _I64, _I64, _P, _P]),
@@ -85,6 +88,21 @@ _MOE_SIGNATURES = {
     "linear_fwd": (C.c_int, [C.POINTER(LinearDesc)] + [_P] * 10 + [C.c_size_t, _P]),
     "linear_bwd": (C.c_int, [C.POINTER(LinearDesc)] + [_P] * 11 + [_I32, _P, C.c_size_t, _P]),
     "moe_abi_version": (C.c_int, []),
+}
+
+# norm.h
+NORM_LAYER, NORM_RMS = 0, 1
+
+
+class NormDesc(C.Structure):
+    _fields_ = [("M", C.c_int64), ("d", C.c_int64), ("dtype", C.c_int32), ("wdtype", C.c_int32), ("kind", C.c_int32),
+                ("eps", C.c_float)]
+
+
+_NORM_SIGNATURES = {
+    "norm_fwd": (C.c_int, [C.POINTER(NormDesc)] + [_P] * 9),
+    "norm_workspace_bytes": (C.c_size_t, [_I64, _I64]),
+    "norm_bwd": (C.c_int, [C.POINTER(NormDesc)] + [_P] * 9 + [_I32, _P, C.c_size_t, _P]),
 }
 
 _lib = None
@@ -100,7 +118,7 @@ def lib() -> C.CDLL:
                 f"{LIB_PATH} is missing: build it with `python -m gated_mlp_gemms_amd.build` "
                 "(the MLP engine has no non-HIP fallback)")
         handle = C.CDLL(LIB_PATH)
-        for name, (res, args) in {**_SIGNATURES, **_MOE_SIGNATURES}.items():
+        for name, (res, args) in {**_SIGNATURES, **_MOE_SIGNATURES, **_NORM_SIGNATURES}.items():
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args
@@ -110,7 +128,8 @@ def lib() -> C.CDLL:
 
 # bind.cpp's functions call these, in this order
 _BOUND = ("moe_route", "moe_route_bwd", "moe_sort_workspace_bytes", "moe_sort", "moe_gather", "moe_gather_bwd",
-          "moe_combine", "moe_combine_bwd", "linear_workspace_bytes", "linear_fwd", "linear_bwd")
+          "moe_combine", "moe_combine_bwd", "linear_workspace_bytes", "linear_fwd", "linear_bwd",
+          "moe_balance_workspace_bytes", "moe_balance", "moe_balance_bwd", "norm_fwd", "norm_workspace_bytes", "norm_bwd")
 
 
 def raw_stream(device: int) -> int:
@@ -133,7 +152,7 @@ def workspace_on(n: int, device: int, stream: int):
 
 
 def bind():
-    """The extension that checks tensors and makes moe.h's calls (bind.cpp), tied to the loaded library."""
+    """The extension that checks tensors and makes moe.h's and norm.h's calls (bind.cpp), tied to the loaded library."""
     global _bind
     if _bind is None:
         import torch

@@ -1,5 +1,5 @@
-// The Python side of moe.h's entry points: checks a call's tensors, turns them into device pointers and
-// makes the call, as functions of positional arguments that moe.py wraps. A call of a few tokens takes the
+// The Python side of moe.h's and norm.h's entry points: checks a call's tensors, turns them into device pointers and
+// makes the call, as functions of positional arguments that moe.py and norm.py wrap. A call of a few tokens takes the
 // GPU 2-4 us; checking 3 to 8 tensors and passing 10 to 17 arguments from Python took 4 to 7 us a call, more than
 // the launch itself, here it takes well under one.
 //
@@ -14,10 +14,11 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "moe.h"
+#include "norm.h"
 
 namespace {
 
-// What moe.py hands over once (setup): the library's entry points, and its own objects.
+// What _lib.py hands over once (setup): the library's entry points, and its own objects.
 struct Entry {
   decltype(&::moe_route) route;
   decltype(&::moe_route_bwd) route_bwd;
@@ -30,6 +31,12 @@ struct Entry {
   decltype(&::linear_workspace_bytes) linear_bytes;
   decltype(&::linear_fwd) fwd;
   decltype(&::linear_bwd) bwd;
+  decltype(&::moe_balance_workspace_bytes) balance_bytes;
+  decltype(&::moe_balance) balance;
+  decltype(&::moe_balance_bwd) balance_bwd;
+  decltype(&::norm_fwd) norm_fwd;
+  decltype(&::norm_workspace_bytes) norm_bytes;
+  decltype(&::norm_bwd) norm_bwd;
 } lib;
 PyObject *py_error, *py_workspace, *py_raw_stream;   // owned for good
 
@@ -66,6 +73,7 @@ std::string type_name(ScalarType t) {   // as torch prints it
     case ScalarType::Int: return "torch.int32";
     case ScalarType::Long: return "torch.int64";
     case ScalarType::Byte: return "torch.uint8";
+    case ScalarType::Bool: return "torch.bool";
     default: return c10::toString(t);
   }
 }
@@ -259,6 +267,46 @@ void route_bwd(PyObject* const* a) {
   call(dev, "moe_route_bwd", [&] { return lib.route_bwd(logits, ids, dw, code_of(dt), T, E, k, score, renorm, dl, s); });
 }
 
+// logits, ids, mask, counts, shares, loss, score, workspace, stream
+void balance(PyObject* const* a) {
+  Args arg;
+  const ScalarType dt = float_type(a[0], "logits");
+  const Shape te = dims(a[0], "logits", 2);
+  const int64_t T = te[0], E = te[1], k = dims(a[1], "ids", 2)[1];
+  const void* logits = arg(a[0], "logits", dt, te);
+  auto* ids = arg.as<int32_t>(a[1], "ids", kI32, {T, k});
+  auto* mask = static_cast<uint8_t*>(arg.opt(a[2], "mask", ScalarType::Bool, {T}));
+  auto* counts = arg.as<int32_t>(a[3], "counts", kI32, {E + 1});
+  auto* shares = arg.as<float>(a[4], "shares", kF32, {E});
+  auto* loss = arg.as<float>(a[5], "loss", kF32, {1});
+  const int score = (int)integer(a[6]), dev = arg.device();
+  void* s = stream_of(a[8], dev);
+  const Workspace ws(a[7], dev, s, [&] { return needed(lib.balance_bytes(T, E), "moe_balance_workspace_bytes"); });
+  call(dev, "moe_balance", [&] {
+    return lib.balance(logits, ids, mask, code_of(dt), T, E, k, score, counts, shares, loss, ws.ptr, ws.bytes, s);
+  });
+}
+
+// logits, ids, mask, counts, dloss, dweights, dlogits, score, renorm, stream
+void balance_bwd(PyObject* const* a) {
+  Args arg;
+  const ScalarType dt = float_type(a[0], "logits");
+  const Shape te = dims(a[0], "logits", 2);
+  const int64_t T = te[0], E = te[1], k = dims(a[1], "ids", 2)[1];
+  const void* logits = arg(a[0], "logits", dt, te);
+  auto* ids = arg.as<int32_t>(a[1], "ids", kI32, {T, k});
+  auto* mask = static_cast<uint8_t*>(arg.opt(a[2], "mask", ScalarType::Bool, {T}));
+  auto* counts = arg.as<int32_t>(a[3], "counts", kI32, {E + 1});
+  auto* dloss = static_cast<float*>(arg.opt(a[4], "dloss", kF32, {1}));
+  auto* dw = static_cast<float*>(arg.opt(a[5], "dweights", kF32, {T, k}));
+  void* dl = arg(a[6], "dlogits", dt, te);
+  const int score = (int)integer(a[7]), renorm = (int)integer(a[8]), dev = arg.device();
+  void* s = stream_of(a[9], dev);
+  call(dev, "moe_balance_bwd", [&] {
+    return lib.balance_bwd(logits, ids, mask, counts, dloss, dw, code_of(dt), T, E, k, score, renorm, dl, s);
+  });
+}
+
 // ids (any shape, taken in order), experts, offsets, row_of, slot_of, workspace, stream
 void sort(PyObject* const* a) {
   Args arg;
@@ -427,6 +475,69 @@ void bwd(PyObject* const* a) {
   });
 }
 
+float real(PyObject* o) {
+  const double v = PyFloat_AsDouble(o);
+  if (v == -1.0 && PyErr_Occurred()) throw PyFailed{};
+  return (float)v;
+}
+
+// A norm_desc from the rows' tensor and the weight's; the first of `given` that is a tensor has the weights' type.
+norm_desc norm_of(PyObject* rows, const char* name, std::initializer_list<PyObject*> given, PyObject* kind, PyObject* eps) {
+  const ScalarType dt = float_type(rows, name);
+  const Shape md = dims(rows, name, 2);
+  ScalarType wt = dt;
+  for (PyObject* o : given)
+    if (o != Py_None) {
+      wt = float_type(o, "weight");
+      break;
+    }
+  return {md[0], md[1], code_of(dt), code_of(wt), (int32_t)integer(kind), eps == nullptr ? 0.0f : real(eps)};
+}
+
+// x, y, weight, bias, residual, h, mean, rstd, kind, eps, stream
+void norm_fwd(PyObject* const* a) {
+  Args arg;
+  const norm_desc q = norm_of(a[0], "x", {a[2], a[3]}, a[8], a[9]);
+  const ScalarType dt = type_of(q.dtype), wt = type_of(q.wdtype);
+  const void* x = arg(a[0], "x", dt, {q.M, q.d});
+  void* y = arg(a[1], "y", dt, {q.M, q.d});
+  const void* w = arg.opt(a[2], "weight", wt, {q.d});
+  const void* b = arg.opt(a[3], "bias", wt, {q.d});
+  const void* res = arg.opt(a[4], "residual", dt, {q.M, q.d});
+  void* h = arg.opt(a[5], "h", dt, {q.M, q.d});
+  auto* mean = static_cast<float*>(arg.opt(a[6], "mean", kF32, {q.M}));
+  auto* rstd = static_cast<float*>(arg.opt(a[7], "rstd", kF32, {q.M}));
+  const int dev = arg.device();
+  void* s = stream_of(a[10], dev);
+  call(dev, "norm_fwd", [&] { return lib.norm_fwd(&q, x, res, w, b, y, h, mean, rstd, s); });
+}
+
+// dy, h, mean, rstd, weight, dresidual, dx, dweight, dbias, kind, grad_accum, workspace, stream
+void norm_bwd(PyObject* const* a) {
+  Args arg;
+  const int accum = (int)integer(a[10]);
+  // (gradients that are added to are fp32 whatever the weights are)
+  const norm_desc q = accum ? norm_of(a[0], "dy", {a[4]}, a[9], nullptr) : norm_of(a[0], "dy", {a[4], a[7], a[8]}, a[9], nullptr);
+  const ScalarType dt = type_of(q.dtype), wt = type_of(q.wdtype), gt = accum ? kF32 : wt;
+  const void* dy = arg(a[0], "dy", dt, {q.M, q.d});
+  const void* h = arg(a[1], "h", dt, {q.M, q.d});
+  auto* mean = static_cast<float*>(arg.opt(a[2], "mean", kF32, {q.M}));
+  auto* rstd = arg.as<float>(a[3], "rstd", kF32, {q.M});
+  const void* w = arg.opt(a[4], "weight", wt, {q.d});
+  const void* dres = arg.opt(a[5], "dresidual", dt, {q.M, q.d});
+  void* dx = arg.opt(a[6], "dx", dt, {q.M, q.d});
+  void* dw = arg.opt(a[7], "dweight", gt, {q.d});
+  void* db = arg.opt(a[8], "dbias", gt, {q.d});
+  const int dev = arg.device();
+  void* s = stream_of(a[12], dev);
+  auto run = [&](void* ws, size_t bytes) {
+    call(dev, "norm_bwd", [&] { return lib.norm_bwd(&q, dy, h, mean, rstd, w, dres, dx, dw, db, accum, ws, bytes, s); });
+  };
+  if (dw == nullptr && db == nullptr) return run(nullptr, 0);   // no sums, no workspace
+  const Workspace ws(a[11], dev, s, [&] { return needed(lib.norm_bytes(q.M, q.d), "norm_workspace_bytes"); });
+  run(ws.ptr, ws.bytes);
+}
+
 // addresses of the library's entry points in Entry's order, MlpError, workspace(bytes, device, stream), raw_stream(device)
 PyObject* setup(PyObject*, PyObject* args) {
   PyObject *at, *error, *workspace, *raw_stream;
@@ -465,6 +576,10 @@ PyMethodDef methods[] = {
     BIND_ENTRY("moe_combine_bwd", 9, combine_bwd),
     BIND_ENTRY("linear_fwd", 12, fwd),
     BIND_ENTRY("linear_bwd", 15, bwd),
+    BIND_ENTRY("moe_balance", 9, balance),
+    BIND_ENTRY("moe_balance_bwd", 10, balance_bwd),
+    BIND_ENTRY("norm_fwd", 11, norm_fwd),
+    BIND_ENTRY("norm_bwd", 13, norm_bwd),
     {"setup", setup, METH_VARARGS, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

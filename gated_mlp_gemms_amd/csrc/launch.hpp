@@ -128,6 +128,13 @@ hipError_t run_moe_route(DType dt, const void* logits, int64_t T, int E, int k, 
                          float* weights, hipStream_t s);
 hipError_t run_moe_route_bwd(DType dt, const void* logits, const int* ids, const float* dweights, int64_t T, int E,
                              int k, int sigmoid, int renorm, void* dlogits, hipStream_t s);
+// ws: moe_balance_parts x (E fp32 + E + 1 int32)
+int moe_balance_parts(int64_t T, int E);
+hipError_t run_moe_balance(DType dt, const void* logits, const int* ids, const uint8_t* mask, int64_t T, int E, int k,
+                           int sigmoid, int* counts, float* shares, float* loss, void* ws, hipStream_t s);
+hipError_t run_moe_balance_bwd(DType dt, const void* logits, const int* ids, const uint8_t* mask, const int* counts,
+                               const float* dloss, const float* dweights, int64_t T, int E, int k, int sigmoid, int renorm,
+                               void* dlogits, hipStream_t s);
 size_t moe_sort_counts_bytes(int64_t n, int E);   // 0: one workgroup sorts them
 hipError_t run_moe_sort(const int* ids, int64_t n, int E, int* offsets, int* row_of, int* slot_of, int* counts,
                         hipStream_t s);
@@ -139,6 +146,18 @@ hipError_t run_moe_combine(DType dt, const void* ys, const float* weights, const
 hipError_t run_moe_combine_bwd(DType dt, const void* dout, const void* ys, const float* weights, const int* slot_of,
                                const int* offsets, int n, int E, int k, int pieces, void* dys, float* dweights,
                                hipStream_t s);
+
+// ---- norm ------------------------------------------------------------------------------------------
+
+// Rows of `pieces` 16-byte pieces, d elements; wide: weight and bias are fp32, else of the rows' type.
+hipError_t run_norm_fwd(DType dt, bool wide, const void* x, const void* res, const void* w, const void* b, int64_t rows,
+                        int pieces, int64_t d, int layer, float eps, void* y, void* h, float* mean, float* rstd,
+                        hipStream_t s);
+// part: fp32 [norm_parts][2][d], where dw or db is asked for.
+int norm_parts(int64_t rows, int pieces);
+hipError_t run_norm_bwd(DType dt, bool wide, const void* dy, const void* h, const float* mean, const float* rstd,
+                        const void* w, const void* dres, int64_t rows, int pieces, int64_t d, void* dx, void* dw,
+                        void* db, int accumulate, float* part, hipStream_t s);
 
 // out = alpha * sum_s partial[s] (fixed order), stored as `io` or added into fp32 (accumulate).
 // Rows >= c_split go to C1 (row - c_split).

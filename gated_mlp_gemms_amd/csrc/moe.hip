@@ -3,49 +3,13 @@
 #include "common.hpp"
 #include "launch.hpp"
 #include "moe.h"
+#include "rows.hpp"
 
 #include <algorithm>
 
 namespace gmlp {
 
 namespace {
-
-template <typename T> __device__ __forceinline__ float load1(const void* p, int64_t i) {
-  if constexpr (sizeof(T) == 4) return reinterpret_cast<const float*>(p)[i];
-  else return Bits16<T>::to_f32(reinterpret_cast<const uint16_t*>(p)[i]);
-}
-template <typename T> __device__ __forceinline__ void store1(void* p, int64_t i, float v) {
-  if constexpr (sizeof(T) == 4) reinterpret_cast<float*>(p)[i] = v;
-  else reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)Bits16<T>::from_f32(v);
-}
-
-// ---- reductions over the L lanes of a token (a power of two, 16 .. 64), result in every lane --
-// Inside 16 lanes the partner is reached by a DPP operand (quad permutes, then the mirrors of 8 and
-// 16 lanes, which after the quad steps pair the same halves as xor 4 and xor 8 would).
-
-template <int CTRL> __device__ __forceinline__ uint32_t dpp(uint32_t v) {
-  return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xf, 0xf, false);
-}
-template <int L, typename Op> __device__ __forceinline__ uint32_t group_reduce(uint32_t v, Op op) {
-  v = op(v, dpp<0xB1>(v));    // lanes 1 0 3 2
-  v = op(v, dpp<0x4E>(v));    // lanes 2 3 0 1
-  v = op(v, dpp<0x141>(v));   // mirror of 8
-  v = op(v, dpp<0x140>(v));   // mirror of 16
-#pragma unroll
-  for (int o = 16; o < L; o <<= 1) v = op(v, (uint32_t)__shfl_xor((int)v, o));
-  return v;
-}
-template <int L> __device__ __forceinline__ uint32_t group_max(uint32_t v) {
-  return group_reduce<L>(v, [](uint32_t a, uint32_t b) { return max(a, b); });
-}
-template <int L> __device__ __forceinline__ uint32_t group_min(uint32_t v) {
-  return group_reduce<L>(v, [](uint32_t a, uint32_t b) { return min(a, b); });
-}
-template <int L> __device__ __forceinline__ float group_sum(float v) {
-  return __uint_as_float(group_reduce<L>(__float_as_uint(v), [](uint32_t a, uint32_t b) {
-    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
-  }));
-}
 
 // ---- router ------------------------------------------------------------------------------------
 
@@ -222,12 +186,12 @@ __device__ __forceinline__ void each_choice(int k, int id, float coef, F f) {
 //   softmax, renormalised: a softmax of the chosen alone, dx_i = w_i (g_i - m) at the chosen ones;
 //   softmax:               dx_e = [e chosen] w g - p_e m, p over every expert;
 //   sigmoid, renormalised: dx_i = w_i (1 - q_i) (g_i - m);   sigmoid: q_i (1 - q_i) g_i.
+// d: the gradient of the lane's C scores, which is added to.
 template <typename T, int L, int C>
-__device__ __forceinline__ void route_token_bwd(const void* __restrict__ logits, const int* __restrict__ ids,
-                                                const float* __restrict__ dweights, int64_t t, int64_t tokens, int E,
-                                                int k, int sigmoid, int renorm, void* __restrict__ dlogits) {
+__device__ __forceinline__ void route_grad(const void* __restrict__ logits, const int* __restrict__ ids,
+                                           const float* __restrict__ dweights, int64_t t, bool live, int E, int k,
+                                           int sigmoid, int renorm, float (&d)[C]) {
   const int lane = threadIdx.x & (L - 1);
-  const bool live = t < tokens;
   int id = -1;
   float g = 0.0f, s = -INFINITY;
   if (live && lane < k) {
@@ -239,9 +203,6 @@ __device__ __forceinline__ void route_token_bwd(const void* __restrict__ logits,
     }
   }
   const bool chosen = id >= 0;
-  float d[C];   // what every expert gets, chosen or not
-#pragma unroll
-  for (int j = 0; j < C; ++j) d[j] = 0.0f;
   float coef = 0.0f;
   if (sigmoid) {
     const Sigmoid p = sigmoid_of(s);
@@ -279,14 +240,18 @@ __device__ __forceinline__ void route_token_bwd(const void* __restrict__ logits,
       const float mean = group_sum<L>(g * w);
       coef = w * g;
 #pragma unroll
-      for (int j = 0; j < C; ++j) d[j] = -(x[j] / total) * mean;
+      for (int j = 0; j < C; ++j) d[j] += -(x[j] / total) * mean;   // what every expert gets, chosen or not
     }
   }
   each_choice<L, 0>(k, id, coef, [&](int at, float c) {
 #pragma unroll
     for (int j = 0; j < C; ++j) d[j] += at == lane * C + j ? c : 0.0f;
   });
-  if (!live) return;
+}
+
+// The lane's C values of row t of an [tokens, E] tensor (load_scores' other way).
+template <typename T, int C>
+__device__ __forceinline__ void store_scores(void* __restrict__ dlogits, int64_t t, int E, int lane, const float (&d)[C]) {
   if (C > 1 && E % C == 0) {   // a lane's gradients are one aligned piece
     using Part = typename ScorePart<T, C>::type;
     Part part;
@@ -312,8 +277,12 @@ __global__ __launch_bounds__(kRouteThreads) void route_bwd_kernel(const void* __
                                                                   int E, int k, int sigmoid, int renorm,
                                                                   void* __restrict__ dlogits) {
   constexpr int R = kRouteThreads / L;
-  for (int64_t t0 = (int64_t)blockIdx.x * R; t0 < tokens; t0 += (int64_t)gridDim.x * R)
-    route_token_bwd<T, L, C>(logits, ids, dweights, t0 + threadIdx.x / L, tokens, E, k, sigmoid, renorm, dlogits);
+  for (int64_t t0 = (int64_t)blockIdx.x * R; t0 < tokens; t0 += (int64_t)gridDim.x * R) {
+    const int64_t t = t0 + threadIdx.x / L;
+    float d[C] = {};
+    route_grad<T, L, C>(logits, ids, dweights, t, t < tokens, E, k, sigmoid, renorm, d);
+    if (t < tokens) store_scores<T, C>(dlogits, t, E, threadIdx.x & (L - 1), d);
+  }
 }
 
 // f(L, C) for the lanes a token and scores a lane that E takes.
@@ -326,6 +295,162 @@ template <typename F> hipError_t route_shape(int64_t E, F f) {
   if (E <= 256) return f(integral_constant<int, 32>{}, integral_constant<int, 8>{});
   if (E <= 512) return f(integral_constant<int, 64>{}, integral_constant<int, 8>{});
   return f(integral_constant<int, 64>{}, integral_constant<int, 16>{});
+}
+
+// ---- balance loss ------------------------------------------------------------------------------
+
+// A token's probabilities, in place of its C scores a lane: softmax, or each expert's sigmoid divided by their sum (as
+// sigmoid_share). A token without any, and a lane past the row, has zeros.
+template <int L, int C> __device__ __forceinline__ void balance_probs(int E, int lane, int sigmoid, float (&x)[C]) {
+  uint32_t m = 0u;
+#pragma unroll
+  for (int j = 0; j < C; ++j) m = max(m, lane * C + j < E ? score_key(x[j]) : 0u);
+  const float top = key_score(group_max<L>(m));
+  const bool none = sigmoid ? top < -104.0f : top == -INFINITY;
+  const float shift = sigmoid ? fminf(top, 0.0f) : top;
+  float part = 0.0f;
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+    const bool in = lane * C + j < E;
+    if (sigmoid) x[j] = in ? (x[j] < 0.0f ? expf(x[j] - shift) / (1.0f + expf(x[j])) : sigmoid_of(x[j]).q) : 0.0f;
+    else x[j] = in ? expf(x[j] - shift) : 0.0f;
+    part += x[j];
+  }
+  const float r = 1.0f / group_sum<L>(part);
+#pragma unroll
+  for (int j = 0; j < C; ++j) x[j] = none ? 0.0f : x[j] * r;
+}
+
+// The workgroup's share of the tokens, `chunk` of them: its sums of the probabilities into part_p [E], its tokens an
+// expert and its tokens that count into part_c [E + 1]. A lane has the same experts in every token, so their
+// sums stay in registers; the groups of a wave, then the waves, are joined in order.
+// 16384 x 128: bound by the exponentials and by a workgroup's handful of trips to memory one after another.
+template <typename T, int L, int C>
+__global__ __launch_bounds__(kRouteThreads) void balance_kernel(const void* __restrict__ logits, const int* __restrict__ ids,
+                                                                const uint8_t* __restrict__ mask, int64_t tokens, int E,
+                                                                int k, int sigmoid, int64_t chunk, float* __restrict__ part_p,
+                                                                int* __restrict__ part_c) {
+  constexpr int R = kRouteThreads / L, W = kRouteThreads / 64;
+  __shared__ int cnt[MOE_MAX_EXPERTS + 1];
+  __shared__ float sums[W][L * C];
+  const int tid = threadIdx.x, lane = tid & (L - 1);
+  for (int e = tid; e <= E; e += kRouteThreads) cnt[e] = 0;
+  __syncthreads();
+  const int64_t beg = blockIdx.x * chunk, end = min(tokens, beg + chunk);
+  float acc[C] = {};
+  int seen = 0;
+  for (int64_t t0 = beg; t0 < end; t0 += R) {
+    const int64_t t = t0 + tid / L;
+    const bool live = t < end && (mask == nullptr || mask[t] != 0);
+    float x[C];
+    load_scores<T, C>(logits, t, E, lane, live, 0.0f, x);
+    balance_probs<L, C>(E, lane, sigmoid, x);
+#pragma unroll
+    for (int j = 0; j < C; ++j) acc[j] += live ? x[j] : 0.0f;
+    seen += live ? 1 : 0;
+  }
+  for (int64_t i = beg * k + tid; i < end * k; i += kRouteThreads) {
+    const int id = ids[i];
+    if ((uint32_t)id < (uint32_t)E && (mask == nullptr || mask[i / k] != 0)) atomicAdd(&cnt[id], 1);
+  }
+  if (lane == 0) atomicAdd(&cnt[E], seen);
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+#pragma unroll
+    for (int o = L; o < 64; o <<= 1) acc[j] += __shfl_xor(acc[j], o);
+    if ((tid & 63) < L) sums[tid >> 6][lane * C + j] = acc[j];
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += kRouteThreads) {
+    float s = sums[0][e];
+#pragma unroll
+    for (int w = 1; w < W; ++w) s += sums[w][e];
+    part_p[(int64_t)blockIdx.x * E + e] = s;
+  }
+  for (int e = tid; e <= E; e += kRouteThreads) part_c[(int64_t)blockIdx.x * (E + 1) + e] = cnt[e];
+}
+
+// The workgroups' shares added up, by one workgroup: 2^sh >= E threads an expert's run of parts beside one another, joined in order.
+__global__ __launch_bounds__(1024) void balance_join_kernel(const float* __restrict__ part_p, const int* __restrict__ part_c,
+                                                            int parts, int E, int k, int sh, int* __restrict__ counts,
+                                                            float* __restrict__ shares, float* __restrict__ loss) {
+  __shared__ float ps[1024];
+  __shared__ int cs[1024];
+  __shared__ int live;
+  __shared__ float waves[16];
+  const int tid = threadIdx.x, e = tid & ((1 << sh) - 1), slice = tid >> sh, slices = 1024 >> sh;
+  if (tid == 0) live = 0;
+  __syncthreads();
+  float p = 0.0f;
+  int c = 0, n = 0;
+  if (e < E) {
+#pragma unroll 8
+    for (int g = slice; g < parts; g += slices) {
+      p += part_p[(int64_t)g * E + e];
+      c += part_c[(int64_t)g * (E + 1) + e];
+    }
+  }
+  for (int g = tid; g < parts; g += 1024) n += part_c[(int64_t)g * (E + 1) + E];
+  if (n != 0) atomicAdd(&live, n);
+  ps[tid] = p;
+  cs[tid] = c;
+  __syncthreads();
+  n = live;
+  float v = 0.0f;
+  if (slice == 0 && e < E) {
+    for (int s = 1; s < slices; ++s) {
+      p += ps[tid + (s << sh)];
+      c += cs[tid + (s << sh)];
+    }
+    p = n > 0 ? p / (float)n : 0.0f;
+    counts[e] = c;
+    shares[e] = p;
+    v = n > 0 ? p * ((float)c / ((float)n * (float)k)) : 0.0f;
+  }
+  v = group_sum<64>(v);
+  if ((tid & 63) == 0) waves[tid >> 6] = v;
+  __syncthreads();
+  if (tid != 0) return;
+  v = 0.0f;
+  for (int w = 0; w < 16; ++w) v += waves[w];
+  counts[E] = n;
+  loss[0] = (float)E * v;
+}
+
+// The gradient: with a_e = dloss E counts_e / (n^2 k) and m = sum_e p_e a_e, p_e (a_e - m), of sigmoid scores times
+// 1 - q_e; on top of the chosen weights' (dweights NULL: none), both rounded once.
+template <typename T, int L, int C>
+__global__ __launch_bounds__(kRouteThreads) void balance_bwd_kernel(const void* __restrict__ logits, const int* __restrict__ ids,
+                                                                    const uint8_t* __restrict__ mask,
+                                                                    const int* __restrict__ counts,
+                                                                    const float* __restrict__ dloss,
+                                                                    const float* __restrict__ dweights, int64_t tokens,
+                                                                    int E, int k, int sigmoid, int renorm,
+                                                                    void* __restrict__ dlogits) {
+  constexpr int R = kRouteThreads / L;
+  const int lane = threadIdx.x & (L - 1);
+  const float n = (float)counts[E];
+  const float each = n > 0.0f ? (dloss != nullptr ? dloss[0] : 1.0f) * ((float)E / (n * (float)k)) / n : 0.0f;
+  float a[C];
+#pragma unroll
+  for (int j = 0; j < C; ++j) a[j] = lane * C + j < E ? each * (float)counts[lane * C + j] : 0.0f;
+  for (int64_t t0 = (int64_t)blockIdx.x * R; t0 < tokens; t0 += (int64_t)gridDim.x * R) {
+    const int64_t t = t0 + threadIdx.x / L;
+    const bool in = t < tokens, live = in && (mask == nullptr || mask[t] != 0);
+    float x[C], d[C], rest[C];
+    load_scores<T, C>(logits, t, E, lane, live, 0.0f, x);
+#pragma unroll
+    for (int j = 0; j < C; ++j) rest[j] = sigmoid ? sigmoid_of(x[j]).rest : 1.0f;
+    balance_probs<L, C>(E, lane, sigmoid, x);
+    float part = 0.0f;
+#pragma unroll
+    for (int j = 0; j < C; ++j) part = __builtin_fmaf(x[j], a[j], part);
+    const float m = group_sum<L>(part);
+#pragma unroll
+    for (int j = 0; j < C; ++j) d[j] = live ? x[j] * rest[j] * (a[j] - m) : 0.0f;
+    if (dweights != nullptr) route_grad<T, L, C>(logits, ids, dweights, t, in, E, k, sigmoid, renorm, d);
+    if (in) store_scores<T, C>(dlogits, t, E, lane, d);
+  }
 }
 
 // ---- tokens by expert ----------------------------------------------------------------------------
@@ -450,32 +575,7 @@ inline int row_shift(int64_t pieces) {
   while (sh < 8 && (int64_t)(1 << sh) < pieces) ++sh;
   return sh;
 }
-// Workgroups for `items` items, `per` a workgroup: at most 2^20, which then take several (2^32 threads are more
-// than a launch can have).
-inline unsigned item_grid(int64_t items, int64_t per) { return (unsigned)std::min<int64_t>((items + per - 1) / per, 1 << 20); }
 inline unsigned row_grid(int64_t rows, int sh) { return item_grid(rows, kRowThreads >> sh); }
-
-template <typename T> struct Piece {   // 16 bytes of a row
-  static constexpr int N = 16 / (int)sizeof(T);
-  static __device__ __forceinline__ void unpack(const u32x4 x, float (&v)[N]) {
-    if constexpr (N == 4) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) v[r] = __uint_as_float(x[r]);
-    } else {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        v[2 * r] = Bits16<T>::to_f32(x[r] & 0xffffu);
-        v[2 * r + 1] = Bits16<T>::to_f32(x[r] >> 16);
-      }
-    }
-  }
-  static __device__ __forceinline__ u32x4 pack(const float (&v)[N]) {
-    if constexpr (N == 4)
-      return u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
-    else
-      return u32x4{pack16x2<T>(v[0], v[1]), pack16x2<T>(v[2], v[3]), pack16x2<T>(v[4], v[5]), pack16x2<T>(v[6], v[7])};
-  }
-};
 
 // Rows that no cache will hold until they are read again are streamed (NT: non-temporal loads of the
 // rows read once, non-temporal stores): from 32 MiB of sorted rows on. Bound by HBM. Gather, combine and both gradients
@@ -486,15 +586,6 @@ template <typename T> struct Piece {   // 16 bytes of a row
 // 208, 104 MB 388 and 395, 150 MB 554 and 552; 2048 x 256, 6 a token, 20 MB 53 and 55, 62 MB 118 and 105, 150 MB 250 and 230.
 constexpr int64_t kStreamBytes = 32 << 20;
 inline bool stream_rows(int64_t rows, int pieces) { return rows * pieces * 16 >= kStreamBytes; }
-
-template <bool NT> __device__ __forceinline__ u32x4 load_piece(const u32x4* p) {
-  if constexpr (NT) return __builtin_nontemporal_load(p);
-  else return *p;
-}
-template <bool NT> __device__ __forceinline__ void store_piece(u32x4* p, u32x4 v) {
-  if constexpr (NT) __builtin_nontemporal_store(v, p);
-  else *p = v;
-}
 
 // xs[r] = x[slot_of[r] / k]: a row is moved as it is, in 16-byte pieces.
 template <bool NT>
@@ -604,16 +695,6 @@ __global__ __launch_bounds__(kRowThreads) void combine_bwd_kernel(const u32x4* _
   }
 }
 
-// f() with the element type of `dt` as its argument.
-template <typename F> hipError_t by_type(DType dt, F f) {
-  switch (dt) {
-    case DT_F32: return f(float{});
-    case DT_BF16: return f(bf16{});
-    case DT_F16: return f(f16{});
-    default: return hipErrorInvalidValue;
-  }
-}
-
 template <typename F> hipError_t by_stream(int64_t rows, int pieces, F f) {
   return stream_rows(rows, pieces) ? f(std::true_type{}) : f(std::false_type{});
 }
@@ -639,6 +720,56 @@ hipError_t run_moe_route_bwd(DType dt, const void* logits, const int* ids, const
       constexpr int L = decltype(l)::value, C = decltype(c)::value, R = kRouteThreads / L;
       hipLaunchKernelGGL((route_bwd_kernel<decltype(v), L, C>), dim3(item_grid(T, R)), dim3(kRouteThreads), 0,
                          s, logits, ids, dweights, T, E, k, sigmoid, renorm, dlogits);
+      return hipGetLastError();
+    });
+  });
+}
+
+// Tokens of a workgroup of balance_kernel: two turns at least, at most kBalanceParts workgroups.
+constexpr int64_t kBalanceParts = 128;
+static int64_t balance_chunk(int64_t T, int E) {
+  int64_t r = 1;
+  (void)route_shape(E, [&](auto l, auto) {
+    r = kRouteThreads / decltype(l)::value;
+    return hipSuccess;
+  });
+  return std::max<int64_t>(2 * r, ((T + kBalanceParts - 1) / kBalanceParts + r - 1) / r * r);
+}
+int moe_balance_parts(int64_t T, int E) {
+  const int64_t c = balance_chunk(T, E);
+  return (int)((T + c - 1) / c);
+}
+
+hipError_t run_moe_balance(DType dt, const void* logits, const int* ids, const uint8_t* mask, int64_t T, int E, int k,
+                           int sigmoid, int* counts, float* shares, float* loss, void* ws, hipStream_t s) {
+  const int parts = moe_balance_parts(T, E);
+  float* part_p = static_cast<float*>(ws);
+  int* part_c = reinterpret_cast<int*>(part_p + (int64_t)parts * E);
+  if (parts > 0) {
+    const hipError_t e = by_type(dt, [&](auto v) {
+      return route_shape(E, [&](auto l, auto c) {
+        hipLaunchKernelGGL((balance_kernel<decltype(v), decltype(l)::value, decltype(c)::value>), dim3(parts),
+                           dim3(kRouteThreads), 0, s, logits, ids, mask, T, E, k, sigmoid, balance_chunk(T, E), part_p,
+                           part_c);
+        return hipGetLastError();
+      });
+    });
+    if (e != hipSuccess) return e;
+  }
+  int sh = 6;
+  while ((1 << sh) < E) ++sh;
+  hipLaunchKernelGGL(balance_join_kernel, dim3(1), dim3(1024), 0, s, part_p, part_c, parts, E, k, sh, counts, shares, loss);
+  return hipGetLastError();
+}
+
+hipError_t run_moe_balance_bwd(DType dt, const void* logits, const int* ids, const uint8_t* mask, const int* counts,
+                               const float* dloss, const float* dweights, int64_t T, int E, int k, int sigmoid, int renorm,
+                               void* dlogits, hipStream_t s) {
+  return by_type(dt, [&](auto v) {
+    return route_shape(E, [&](auto l, auto c) {
+      constexpr int L = decltype(l)::value, C = decltype(c)::value, R = kRouteThreads / L;
+      hipLaunchKernelGGL((balance_bwd_kernel<decltype(v), L, C>), dim3(item_grid(T, R)), dim3(kRouteThreads), 0, s, logits,
+                         ids, mask, counts, dloss, dweights, T, E, k, sigmoid, renorm, dlogits);
       return hipGetLastError();
     });
   });

@@ -398,6 +398,43 @@ mlp_status moe_route_bwd(const void* logits, const int32_t* ids, const float* dw
                                       renorm, dlogits, stream_of(stream)), "moe_route_bwd");
 }
 
+size_t moe_balance_workspace_bytes(int64_t T, int64_t E) {
+  if (check_choices(T, E, 1) != MLP_OK) return 0;
+  return std::max(kAlign, round_up((size_t)moe_balance_parts(T, (int)E) * (2 * E + 1) * sizeof(float)));
+}
+
+mlp_status moe_balance(const void* logits, const int32_t* ids, const uint8_t* mask, int dtype, int64_t T, int64_t E,
+                       int64_t k, int score, int32_t* counts, float* shares, float* loss, void* ws, size_t ws_bytes,
+                       void* stream) {
+  MLP_TRY(check_router(dtype, T, E, k, score, 0));
+  MLP_TRY(need_buf(logits, T, "logits"));
+  MLP_TRY(need_buf(ids, T, "ids", false));
+  MLP_TRY(need_ptr(counts, "counts", false));
+  MLP_TRY(need_ptr(shares, "shares", false));
+  MLP_TRY(need_ptr(loss, "loss", false));
+  const size_t need = moe_balance_workspace_bytes(T, E);
+  if (ws_bytes < need)
+    return fail(MLP_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu needed", ws_bytes, need);
+  MLP_TRY(need_ptr(ws, "workspace"));
+  return hip_status(run_moe_balance(dtype_of(dtype), logits, ids, mask, T, (int)E, (int)k, score == MOE_SIGMOID, counts,
+                                    shares, loss, ws, stream_of(stream)), "moe_balance");
+}
+
+mlp_status moe_balance_bwd(const void* logits, const int32_t* ids, const uint8_t* mask, const int32_t* counts,
+                           const float* dloss, const float* dweights, int dtype, int64_t T, int64_t E, int64_t k,
+                           int score, int renorm, void* dlogits, void* stream) {
+  MLP_TRY(check_router(dtype, T, E, k, score, renorm));
+  MLP_TRY(need_buf(logits, T, "logits"));
+  if (dweights) MLP_TRY(need_buf(ids, T, "ids", false));
+  MLP_TRY(need_ptr(counts, "counts", false));
+  if (dloss) MLP_TRY(need_ptr(dloss, "dloss", false));
+  if (dweights) MLP_TRY(need_ptr(dweights, "dweights", false));
+  MLP_TRY(need_buf(dlogits, T, "dlogits"));
+  if (T == 0) return MLP_OK;
+  return hip_status(run_moe_balance_bwd(dtype_of(dtype), logits, ids, mask, counts, dloss, dweights, T, (int)E, (int)k,
+                                        score == MOE_SIGMOID, renorm, dlogits, stream_of(stream)), "moe_balance_bwd");
+}
+
 static mlp_status check_sort(int64_t n, int64_t E) {
   MLP_TRY(check_experts(E));
   if (n < 0) return fail(MLP_ERR_INVALID_ARG, "n = %lld slots", (long long)n);

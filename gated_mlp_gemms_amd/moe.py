@@ -1,4 +1,4 @@
-"""The mixture-of-experts operators of ``include/moe.h``: router, tokens sorted by expert and back,
+"""The mixture-of-experts operators of ``include/moe.h``: router, balance loss, tokens sorted by expert and back,
 linear layer with its epilogue, experts' products, and their gradients.
 
 As in the rest of the package the functions carry the C entry points' names, write into buffers the
@@ -53,6 +53,31 @@ def moe_route_bwd(logits, ids, dweights, dlogits, score="softmax", renorm=True, 
     """``dlogits`` [T, E] (logits' dtype): the gradient of :func:`moe_route`'s weights against
     ``dweights`` [T, k] (fp32), ``ids`` being what it chose."""
     bind().moe_route_bwd(logits, ids, dweights, dlogits, _score(score), 1 if renorm else 0, stream)
+    return dlogits
+
+
+# ---- balance loss ------------------------------------------------------------------------------------
+
+def moe_balance_workspace_bytes(T, experts) -> int:
+    b = lib().moe_balance_workspace_bytes(int(T), int(experts))
+    if b == 0:
+        raise MlpError(1, "moe_balance_workspace_bytes")
+    return int(b)
+
+
+def moe_balance(logits, ids, counts, shares, loss, mask=None, score="softmax", workspace=None, stream=None):
+    """The load of each expert under the choices ``ids`` [T, k]: ``counts`` [E + 1] (int32, the last the number n
+    of tokens that count), ``shares`` [E] (fp32) the mean probabilities (sigmoids divided by their sum), and
+    ``loss`` [1] (fp32) = E sum_e counts[e] / (n k) shares[e]. ``mask`` [T] (bool): the tokens that count."""
+    bind().moe_balance(logits, ids, mask, counts, shares, loss, _score(score), workspace, stream)
+    return loss
+
+
+def moe_balance_bwd(logits, ids, counts, dlogits, mask=None, dloss=None, dweights=None, score="softmax", renorm=True,
+                    stream=None):
+    """``dlogits`` [T, E]: ``dloss`` [1] (fp32, None: 1) times the gradient of :func:`moe_balance`'s loss, and with
+    ``dweights`` [T, k] that of :func:`moe_route`'s weights added: the router's whole gradient, rounded once."""
+    bind().moe_balance_bwd(logits, ids, mask, counts, dloss, dweights, dlogits, _score(score), 1 if renorm else 0, stream)
     return dlogits
 
 

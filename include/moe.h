@@ -9,6 +9,7 @@
  * t k + j is token t's j-th choice):
  *
  *   moe_route        scores [T, E] -> ids [T, k], weights [T, k]
+ *   moe_balance      scores, ids -> tokens an expert, the loss that balances them
  *   moe_sort         ids -> offsets [E + 1], row_of [n], slot_of [n]   (slots in expert order)
  *   moe_gather       x [T, d] -> xs [n, d], row r = the token of slot slot_of[r]
  *   linear_fwd       experts > 0: rows of expert e times its weight, with bias and activation
@@ -58,6 +59,30 @@ mlp_status moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_
  */
 mlp_status moe_route_bwd(const void* logits, const int32_t* ids, const float* dweights, int dtype, int64_t T,
                          int64_t E, int64_t k, int score, int renorm, void* dlogits, void* stream);
+
+/*
+ * The load of each expert and the loss that balances it. Over the n tokens that count (mask [T], bytes: those
+ * that are not 0; NULL: all), with the choices ids [T, k] held fixed,
+ *   counts[e] = choices of expert e (an id outside [0, E) is none), counts[E] = n,
+ *   shares[e] = mean of p[t][e],  p = softmax(logits[t]), or sigmoids divided by their sum over all E,
+ *   loss[0] = E sum_e counts[e] / (n k) shares[e]        (1 when the load is even; 0 when n = 0).
+ * counts [E + 1] int32; shares [E], loss [1] fp32, summed in fp32 in an order that depends on the sizes only. A token
+ * whose scores are all -inf (sigmoid: below -104) has p = 0. What a token that does not count holds does not matter.
+ * mask has any alignment.
+ */
+size_t moe_balance_workspace_bytes(int64_t T, int64_t E);   /* 0 for sizes moe_balance refuses, else >= 256 */
+mlp_status moe_balance(const void* logits, const int32_t* ids, const uint8_t* mask, int dtype, int64_t T, int64_t E,
+                       int64_t k, int score, int32_t* counts, float* shares, float* loss, void* workspace,
+                       size_t workspace_bytes, void* stream);
+/*
+ * dlogits [T, E] (in dtype) = dloss[0] (fp32; NULL: 1) times the loss' gradient, through shares (counts do not depend
+ * on the scores), 0 for a token that does not count; plus, with dweights [T, k] (fp32, NULL: none), what
+ * moe_route_bwd gives for every token: the router's whole gradient in one pass, rounded once. counts is what
+ * moe_balance wrote; ids is read with dweights only; renorm concerns dweights.
+ */
+mlp_status moe_balance_bwd(const void* logits, const int32_t* ids, const uint8_t* mask, const int32_t* counts,
+                           const float* dloss, const float* dweights, int dtype, int64_t T, int64_t E, int64_t k,
+                           int score, int renorm, void* dlogits, void* stream);
 
 /*
  * Slots in expert order, a stable counting sort of the n ids: offsets[e] = number of slots of
