@@ -6,8 +6,8 @@ become device pointers, the current HIP stream is passed along, and a non-OK sta
 ``MlpError``. Every step of the MLP runs in the library's HIP kernels; there is no other path.
 
 The mixture-of-experts operators (``include/moe.h``: router, tokens by expert and back, linear layer,
-experts' products) are in ``moe.py``, the norm in front of a layer (``include/norm.h``) in ``norm.py``, and
-reached from here by the same names.
+experts' products) are in ``moe.py``, the norm in front of a layer (``include/norm.h``) in ``norm.py``,
+microscaled 4-bit products (``include/mx4.h``) in ``mx4.py``; all are reached from here by the same names.
 """
 from __future__ import annotations
 
@@ -181,5 +181,8 @@ def mlp_fp8_next_scale(amax: float, prev_scale: float, gain: float, floor: float
 from .moe import (  # noqa: E402,F401
     linear_bwd, linear_fwd, linear_workspace_bytes, make_linear_desc, moe_balance, moe_balance_bwd,
     moe_balance_workspace_bytes, moe_combine, moe_combine_bwd, moe_gather, moe_gather_bwd, moe_route, moe_route_bwd, moe_sort, moe_sort_workspace_bytes,
+)
+from .mx4 import (  # noqa: E402,F401
+    mx4_dequantize, mx4_linear_fwd, mx4_linear_workspace_bytes, mx4_quantize, mx4_shapes,
 )
 from .norm import norm_bwd, norm_fwd, norm_workspace_bytes  # noqa: E402,F401

@@ -1,4 +1,4 @@
-"""ctypes view of ``include/mlp.h``, ``moe.h``, ``norm.h`` and the loaded ``libgated_mlp.so`` (marshalling only)."""
+"""ctypes view of ``include/mlp.h``, ``moe.h``, ``norm.h``, ``mx4.h`` and the loaded ``libgated_mlp.so`` (marshalling only)."""
 from __future__ import annotations
 
 import ctypes as C
@@ -105,6 +105,16 @@ _NORM_SIGNATURES = {
     "norm_bwd": (C.c_int, [C.POINTER(NormDesc)] + [_P] * 9 + [_I32, _P, C.c_size_t, _P]),
 }
 
+# mx4.h
+_MX4_SIGNATURES = {
+    "mx4_planes": (_I64, [_I64]),
+    "mx4_scale_rows": (_I64, [_I64]),
+    "mx4_quantize": (C.c_int, [_P, _I32, _I64, _I64, _I64, _P, _P, _P, _P, _P]),
+    "mx4_dequantize": (C.c_int, [_P, _P, _I32, _I64, _I64, _I64, _P, _P]),
+    "mx4_linear_workspace_bytes": (C.c_size_t, [C.POINTER(LinearDesc)]),
+    "mx4_linear_fwd": (C.c_int, [C.POINTER(LinearDesc)] + [_P] * 13 + [C.c_size_t, _P]),
+}
+
 _lib = None
 _bind = None
 
@@ -118,7 +128,7 @@ def lib() -> C.CDLL:
                 f"{LIB_PATH} is missing: build it with `python -m gated_mlp_gemms_amd.build` "
                 "(the MLP engine has no non-HIP fallback)")
         handle = C.CDLL(LIB_PATH)
-        for name, (res, args) in {**_SIGNATURES, **_MOE_SIGNATURES, **_NORM_SIGNATURES}.items():
+        for name, (res, args) in {**_SIGNATURES, **_MOE_SIGNATURES, **_NORM_SIGNATURES, **_MX4_SIGNATURES}.items():
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args
@@ -129,7 +139,8 @@ def lib() -> C.CDLL:
 # bind.cpp's functions call these, in this order
 _BOUND = ("moe_route", "moe_route_bwd", "moe_sort_workspace_bytes", "moe_sort", "moe_gather", "moe_gather_bwd",
           "moe_combine", "moe_combine_bwd", "linear_workspace_bytes", "linear_fwd", "linear_bwd",
-          "moe_balance_workspace_bytes", "moe_balance", "moe_balance_bwd", "norm_fwd", "norm_workspace_bytes", "norm_bwd")
+          "moe_balance_workspace_bytes", "moe_balance", "moe_balance_bwd", "norm_fwd", "norm_workspace_bytes", "norm_bwd",
+          "mx4_planes", "mx4_scale_rows", "mx4_quantize", "mx4_dequantize", "mx4_linear_workspace_bytes", "mx4_linear_fwd")
 
 
 def raw_stream(device: int) -> int:
@@ -152,7 +163,7 @@ def workspace_on(n: int, device: int, stream: int):
 
 
 def bind():
-    """The extension that checks tensors and makes moe.h's and norm.h's calls (bind.cpp), tied to the loaded library."""
+    """The extension that checks tensors and makes moe.h's, norm.h's and mx4.h's calls (bind.cpp), tied to the loaded library."""
     global _bind
     if _bind is None:
         import torch

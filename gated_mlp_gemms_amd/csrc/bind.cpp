@@ -1,5 +1,5 @@
-// The Python side of moe.h's and norm.h's entry points: checks a call's tensors, turns them into device pointers and
-// makes the call, as functions of positional arguments that moe.py and norm.py wrap. A call of a few tokens takes the
+// The Python side of moe.h's, norm.h's and mx4.h's entry points: checks a call's tensors, turns them into device pointers and
+// makes the call, as functions of positional arguments that moe.py, norm.py and mx4.py wrap. A call of a few tokens takes the
 // GPU 2-4 us; checking 3 to 8 tensors and passing 10 to 17 arguments from Python took 4 to 7 us a call, more than
 // the launch itself, here it takes well under one.
 //
@@ -14,6 +14,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include "moe.h"
+#include "mx4.h"
 #include "norm.h"
 
 namespace {
@@ -37,6 +38,12 @@ struct Entry {
   decltype(&::norm_fwd) norm_fwd;
   decltype(&::norm_workspace_bytes) norm_bytes;
   decltype(&::norm_bwd) norm_bwd;
+  decltype(&::mx4_planes) mx4_planes;
+  decltype(&::mx4_scale_rows) mx4_scale_rows;
+  decltype(&::mx4_quantize) mx4_quantize;
+  decltype(&::mx4_dequantize) mx4_dequantize;
+  decltype(&::mx4_linear_workspace_bytes) mx4_bytes;
+  decltype(&::mx4_linear_fwd) mx4_fwd;
 } lib;
 PyObject *py_error, *py_workspace, *py_raw_stream;   // owned for good
 
@@ -538,6 +545,90 @@ void norm_bwd(PyObject* const* a) {
   run(ws.ptr, ws.bytes);
 }
 
+constexpr ScalarType kU8 = ScalarType::Byte;
+
+// The codes and scales of [batch][rows][K] (n dimensions with the batch, or two without), and their device pointers.
+struct Blocks {
+  Blocks(int64_t n, int64_t batch, int64_t rows, int64_t K)
+      : codes_{batch, rows, K / 2}, scales_{batch, lib.mx4_planes(K), lib.mx4_scale_rows(rows), 8}, skip_(n == 3 ? 0 : 1) {}
+  Shape codes() const { return Shape(codes_ + skip_, 3 - skip_); }
+  Shape scales() const { return Shape(scales_ + skip_, 4 - skip_); }
+
+ private:
+  int64_t codes_[3], scales_[4];
+  int skip_;
+};
+
+// A matrix, or a batch of them.
+struct Matrix {
+  int64_t n, batch, rows, cols;
+  Matrix(PyObject* o, const char* name) {
+    n = THPVariable_Check(o) && THPVariable_Unpack(o).dim() == 3 ? 3 : 2;
+    const Shape s = dims(o, name, n);
+    batch = n == 3 ? s[0] : 1;
+    rows = s[n - 2];
+    cols = s[n - 1];
+  }
+};
+
+// x, codes, scales, codes_t, scales_t, stream
+void mx4_quantize(PyObject* const* a) {
+  Args arg;
+  const ScalarType dt = float_type(a[0], "x");
+  const Matrix m(a[0], "x");
+  const Blocks b(m.n, m.batch, m.rows, m.cols), t(m.n, m.batch, m.cols, (m.rows + 31) / 32 * 32);
+  const void* x = arg(a[0], "x", dt, THPVariable_Unpack(a[0]).sizes());
+  void* codes = arg.opt(a[1], "codes", kU8, b.codes());
+  void* scales = arg.opt(a[2], "scales", kU8, b.scales());
+  void* codes_t = arg.opt(a[3], "codes_t", kU8, t.codes());
+  void* scales_t = arg.opt(a[4], "scales_t", kU8, t.scales());
+  const int dev = arg.device();
+  void* s = stream_of(a[5], dev);
+  call(dev, "mx4_quantize", [&] {
+    return lib.mx4_quantize(x, code_of(dt), m.batch, m.rows, m.cols, codes, scales, codes_t, scales_t, s);
+  });
+}
+
+// codes, scales, out, stream
+void mx4_dequantize(PyObject* const* a) {
+  Args arg;
+  const ScalarType dt = float_type(a[2], "out");
+  const Matrix m(a[2], "out");
+  const Blocks b(m.n, m.batch, m.rows, m.cols);
+  const void* codes = arg(a[0], "codes", kU8, b.codes());
+  const void* scales = arg(a[1], "scales", kU8, b.scales());
+  void* out = arg(a[2], "out", dt, THPVariable_Unpack(a[2]).sizes());
+  const int dev = arg.device();
+  void* s = stream_of(a[3], dev);
+  call(dev, "mx4_dequantize", [&] { return lib.mx4_dequantize(codes, scales, code_of(dt), m.batch, m.rows, m.cols, out, s); });
+}
+
+// desc, x, x_scales, w, w_scales, y, w_up, w_up_scales, bias, bias_up, residual, offsets, preact, workspace, stream
+void mx4_fwd(PyObject* const* a) {
+  Args arg;
+  const Desc q(a[0]);
+  const int64_t M = q.d.M, K = q.d.K, N = q.d.N, E = q.d.experts;
+  const Blocks bx(2, 1, M, K), bw(E ? 3 : 2, E ? E : 1, N, K);
+  const void* x = arg(a[1], "x", kU8, bx.codes());
+  const void* xs = arg(a[2], "x_scales", kU8, bx.scales());
+  const void* w = arg(a[3], "w", kU8, bw.codes());
+  const void* wsc = arg(a[4], "w_scales", kU8, bw.scales());
+  void* y = arg(a[5], "y", q.dt, {M, N});
+  const void* w_up = arg.opt(a[6], "w_up", kU8, bw.codes());
+  const void* w_ups = arg.opt(a[7], "w_up_scales", kU8, bw.scales());
+  const void* bias = arg.opt(a[8], "bias", q.dt, q.bias());
+  const void* bias_up = arg.opt(a[9], "bias_up", q.dt, q.bias());
+  const void* res = arg.opt(a[10], "residual", q.dt, {M, N});
+  auto* offsets = static_cast<int32_t*>(arg.opt(a[11], "offsets", kI32, {E + 1}));
+  void* preact = arg.opt(a[12], "preact", q.dt, {M, q.P});
+  const int dev = arg.device();
+  void* s = stream_of(a[14], dev);
+  const Workspace ws(a[13], dev, s, [&] { return needed(lib.mx4_bytes(&q.d), "mx4_linear_workspace_bytes"); });
+  call(dev, "mx4_linear_fwd", [&] {
+    return lib.mx4_fwd(&q.d, x, xs, w, wsc, w_up, w_ups, bias, bias_up, res, offsets, y, preact, ws.ptr, ws.bytes, s);
+  });
+}
+
 // addresses of the library's entry points in Entry's order, MlpError, workspace(bytes, device, stream), raw_stream(device)
 PyObject* setup(PyObject*, PyObject* args) {
   PyObject *at, *error, *workspace, *raw_stream;
@@ -580,6 +671,9 @@ PyMethodDef methods[] = {
     BIND_ENTRY("moe_balance_bwd", 10, balance_bwd),
     BIND_ENTRY("norm_fwd", 11, norm_fwd),
     BIND_ENTRY("norm_bwd", 13, norm_bwd),
+    BIND_ENTRY("mx4_quantize", 6, mx4_quantize),
+    BIND_ENTRY("mx4_dequantize", 4, mx4_dequantize),
+    BIND_ENTRY("mx4_linear_fwd", 15, mx4_fwd),
     {"setup", setup, METH_VARARGS, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

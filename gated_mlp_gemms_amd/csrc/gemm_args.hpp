@@ -97,6 +97,19 @@ struct ExpertBwd {
   int strip_parts;
 };
 
+// A product of microscaled 4-bit operands (gemm_mx4.hpp), one weight (offsets NULL, experts 1) or one an expert. In g, A, B0 and B1
+// are codes and K, lda, ldb, k_per_split bytes of them (two values each); the scales are sa, sb0, sb1, planes of 256 values of every
+// row sa_plane and sb_plane bytes apart. w_stride, ws_stride: bytes from an expert's codes and scales to the next's.
+struct Mx4Gemm {
+  GemmArgs g;
+  const char* sa; const char* sb0; const char* sb1;
+  int64_t sa_plane, sb_plane;
+  const int* offsets;
+  int experts, rows;
+  int64_t w_stride, ws_stride, bias_stride;
+  int grid, splits;   // workgroups, an upper bound of the tiles; parts of K
+};
+
 // Up to kGroupMax independent GEMMs run by one launch (gemm_dma_group_kernel): member j covers
 // workgroups [begin[j], begin[j+1]) (multiples of 8 apart), has items[j] tiles (one per
 // workgroup, no split) and takes tile body kind[j] (0 or 1) of the kernel's two.

@@ -2,6 +2,7 @@
 // planner and planned launches. Defined in mlp_api.hip unless inline here.
 #pragma once
 
+#include <algorithm>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -80,6 +81,26 @@ RowsPlan plan_rows(DType in, int64_t M, int64_t N, int64_t K);
 size_t partial_bytes(const RowsPlan& r, int64_t M, int64_t N);
 
 double list_makespan(const int64_t* tiles, const int64_t* steps, int count, double overhead);
+
+// Seconds of a K-step of a tile with few workgroups on the chip, with one on each of the 256 CUs, with two on some of
+// them, and with every slot taken (all of a CU's slots together), and of what a tile does besides: its first loads
+// and its epilogue.
+struct StepTime { double few, one, two, full, rest; };
+
+// Seconds of `tiles` tiles of `steps` K-steps each.
+inline double tiles_time(const StepTime& st, int64_t slots, int64_t tiles, int64_t steps) {
+  const int64_t round = 256 * slots, last = tiles % round;
+  double t = (double)(tiles / round) * (st.full * (double)steps + st.rest);
+  if (last > 0) {
+    const double step = last <= 256 ? st.few + (st.one - st.few) * (double)last / 256.0
+                                    : st.two + (st.full - st.two) * (double)(last - 256) / (double)(round - 256);
+    t += step * (double)steps + st.rest;
+  }
+  return t;
+}
+
+// Row tiles of bm rows that M rows of E experts (and the rows behind them) take at most.
+inline int64_t row_tiles(int64_t M, int64_t E, int64_t bm) { return M / bm + std::min(M, E) + 1; }
 
 // ---- planned launches --------------------------------------------------------------------------
 

@@ -147,6 +147,21 @@ hipError_t run_moe_combine_bwd(DType dt, const void* dout, const void* ys, const
                                const int* offsets, int n, int E, int k, int pieces, void* dys, float* dweights,
                                hipStream_t s);
 
+// ---- microscaled 4-bit floating point ------------------------------------------------------------------
+
+hipError_t run_mx4_rows(DType dt, const void* x, int64_t batch, int64_t rows, int64_t cols, void* codes, void* scales,
+                        hipStream_t s);
+hipError_t run_mx4_columns(DType dt, const void* x, int64_t batch, int64_t rows, int64_t cols, void* codes, void* scales,
+                           hipStream_t s);
+hipError_t run_mx4_values(DType dt, const void* codes, const void* scales, int64_t batch, int64_t rows, int64_t K, void* out,
+                          hipStream_t s);
+// EPI_LIN or EPI_LIN_GATED, unsplit; tiles TILE_256x256, TILE_128x128 and TILE_64x64 (gated: 64 x 128)
+hipError_t run_mx4_linear_bf16(int epi, TileShape tile, const Mx4Gemm& a, hipStream_t s);
+hipError_t run_mx4_linear_f16(int epi, TileShape tile, const Mx4Gemm& a, hipStream_t s);
+hipError_t run_mx4_linear_f32(int epi, TileShape tile, const Mx4Gemm& a, hipStream_t s);
+// fp32 sums of a.splits parts of K, a.g.partial [splits][M][N]; B1: more rows of B from a.g.b_split on
+hipError_t run_mx4_partial(TileShape tile, const Mx4Gemm& a, hipStream_t s);
+
 // ---- norm ------------------------------------------------------------------------------------------
 
 // Rows of `pieces` 16-byte pieces, d elements; wide: weight and bias are fp32, else of the rows' type.

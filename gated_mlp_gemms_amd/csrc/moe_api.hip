@@ -112,13 +112,10 @@ int linear_tiles(DType in, bool gated, TileInfo (&t)[4]) {
   return n;
 }
 
-// Seconds of a K-step (64 deep, fp32 32) of a tile with few workgroups on the chip, with one on each of the 256
-// CUs, with two on some of them, and with every slot taken (all of a CU's slots together), and of what a tile does
-// besides: its first loads and its epilogue. Measured with forced tiles (us): 2000^3 128 x 128 (one a CU) 26.3, 256 x 128
+// StepTime of a tile, a K-step 64 deep (fp32 32). Measured with forced tiles (us): 2000^3 128 x 128 (one a CU) 26.3, 256 x 128
 // (128 tiles) 33.6, 64 x 64 (two rounds) 38.8; 2000 x 512 x 4096 gated 24.1 / 30.9 / 30.1 / 37.2 (256 x 256, 256 x 128, 128 x 128,
 // 64 x 128); 1000 x 4096 x 512 73 / 47 / 38 / 22; a weight gradient of 2440 x 1560 over 14050 rows in 260 tiles of 128 x 128,
 // two on 4 CUs, 211 (256 x 256 in three parts of K 125), one of 2048 x 2048 over 8192 in 256 of them 74.
-struct StepTime { double few, one, two, full, rest; };
 StepTime step_time(TileShape t, DType in, bool gated) {
   if (in == DT_F32) {
     if (t != TILE_64x64) return {2.2e-6, 2.3e-6, 4.2e-6, 4.5e-6, 5e-6};
@@ -130,18 +127,6 @@ StepTime step_time(TileShape t, DType in, bool gated) {
     case TILE_128x128: return {0.50e-6, 0.65e-6, 0.95e-6, 1.20e-6, 2.5e-6};
     default: return gated ? StepTime{0.33e-6, 0.55e-6, 0.60e-6, 0.77e-6, 1.5e-6} : StepTime{0.25e-6, 0.40e-6, 0.42e-6, 0.52e-6, 1.5e-6};
   }
-}
-
-// Seconds of `tiles` tiles of `steps` K-steps each.
-double tiles_time(const StepTime& st, int64_t slots, int64_t tiles, int64_t steps) {
-  const int64_t round = 256 * slots, last = tiles % round;
-  double t = (double)(tiles / round) * (st.full * (double)steps + st.rest);
-  if (last > 0) {
-    const double step = last <= 256 ? st.few + (st.one - st.few) * (double)last / 256.0
-                                    : st.two + (st.full - st.two) * (double)(last - 256) / (double)(round - 256);
-    t += step * (double)steps + st.rest;
-  }
-  return t;
 }
 
 Plan plan_linear_gemm(DType in, int64_t M, int64_t N, int64_t K, bool allow_split, bool gated) {
@@ -204,9 +189,6 @@ struct ExpertPlan {
   bool dw_first;
   int strip_parts;       // backward, few rows an expert: shares of a strip's weight gradient (ExpertBwd); else 0
 };
-
-// Row tiles of bm rows that M rows of E experts (and the rows behind them) take at most.
-int64_t row_tiles(int64_t M, int64_t E, int64_t bm) { return M / bm + std::min(M, E) + 1; }
 
 // K-steps that are not worth another launch to join them (about 0.3 us each of a product with CUs to spare, against 5 us).
 constexpr double kJoinSteps = 20.0;
