@@ -25,6 +25,91 @@ __device__ __forceinline__ void mx_mma(const u32x4& a, const u32x4& b, uint32_t 
   acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, acc, 4, 4, S, (int)sa, S, (int)sb);   // 4: e2m1
 }
 
+// The epilogue of a tile: the accumulators go to LDS (two block rows of 32 at a time, a wave its own), and come back as 8 consecutive
+// columns of a row a lane, U rows at a time: the loop is rolled and its activation's switch taken once for all U, as a wave
+// that is alone on its SIMD waits out every branch and a cold line of code (4096 x 4096 x 1024 with a row at a time
+// 26.6 us, unrolled over every row 33).
+constexpr int mx_staged_blocks(int MI) { return MI > 2 ? 2 : MI; }
+template <int BM, int BN> constexpr int mx_epilogue_bytes() { return 4 * mx_staged_blocks(BM / 64) * 32 * (BN / 2 * 4 + 16); }
+template <int EPI, typename IoT, int BM, int BN, int MI, int NI>
+__device__ __forceinline__ void mx_epilogue(const GemmArgs& p, f32x16 (&acc)[MI][NI], int n0, int wm, int wn, int lane, int wave, char* lds) {
+  constexpr bool GATED = epi_gated(EPI);
+  constexpr int WM = BM / 2, WN = BN / 2, IB = mx_staged_blocks(MI);   // block rows staged at once
+  constexpr int STRIDE = WN * 4 + 16, UNITS = GATED ? WN / 2 : WN, LPR = UNITS / 8, RPI = 64 / LPR;
+  constexpr int U = IB * 32 / RPI < 4 ? IB * 32 / RPI : 4;
+  const int frow = lane & 31, fhalf = lane >> 5;
+  char* wbuf = lds + wave * IB * 32 * STRIDE;
+  const int nbase = GATED ? n0 + wn * (WN / 2) : n0 + wn * WN;
+  const int rl = lane / LPR, cl = (lane % LPR) * 8, n = nbase + cl;
+  const bool col = n < p.N;
+  const int nin = col ? n : 0;
+  const bool full = p.M >= BM && n0 + (GATED ? BN / 2 : BN) <= p.N;   // (uniform)
+  float bias0[8] = {}, bias1[8] = {};
+  if constexpr (epi_linear(EPI)) {
+    if (p.bias0) Vec8<IoT>::load(elem_ptr<IoT>(p.bias0, 0, 0, nin), bias0);
+    if constexpr (GATED) if (p.bias1) Vec8<IoT>::load(elem_ptr<IoT>(p.bias1, 0, 0, nin), bias1);
+  }
+#pragma unroll
+  for (int i0 = 0; i0 < MI; i0 += IB) {
+#pragma unroll
+    for (int i = 0; i < IB; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<f32x4*>(wbuf + (i * 32 + frow) * STRIDE + (j * 32 + 8 * g + 4 * fhalf) * 4) =
+              f32x4{acc[i0 + i][j][4 * g], acc[i0 + i][j][4 * g + 1], acc[i0 + i][j][4 * g + 2], acc[i0 + i][j][4 * g + 3]};
+    wait_lgkmcnt0();   // this wave's rows are written
+    __builtin_amdgcn_wave_barrier();
+    const int m1 = wm * WM + i0 * 32 + rl;
+#pragma unroll 1
+    for (int r0 = 0; r0 < IB * 32; r0 += U * RPI) {
+      float v[8 * U], u[GATED ? 8 * U : 1], y[8 * U], o[8 * U];
+      auto each = [&](auto f) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) f(k, m1 + r0 + k * RPI, reinterpret_cast<float(&)[8]>(v[8 * k]));
+      };
+      auto store = [&](auto where, float* z) {   // 8 columns of row m to where(m)
+        each([&](int k, int m, float(&)[8]) {
+          if (full || (col && m < p.M)) Vec8<typename std::conditional<EPI == EPI_PARTIAL, float, IoT>::type>::store(where(m), z + 8 * k);
+        });
+      };
+      if (EPI != EPI_PARTIAL && p.res) {
+        each([&](int k, int m, float(&)[8]) { Vec8<IoT>::load(elem_ptr<IoT>(p.res, min(m, p.M - 1), p.ld_res, nin), o + 8 * k); });
+      } else {
+#pragma unroll
+        for (int q = 0; q < 8 * U; ++q) o[q] = 0.0f;
+      }
+      each([&](int k, int, float(&z)[8]) {
+        const char* src = wbuf + (rl + r0 + k * RPI) * STRIDE + cl * 4;
+        const f32x4 a0 = *reinterpret_cast<const f32x4*>(src), a1 = *reinterpret_cast<const f32x4*>(src + 16);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) { z[q] = a0[q] + bias0[q]; z[4 + q] = a1[q] + bias0[4 + q]; }
+        if constexpr (GATED) {
+          const f32x4 b0 = *reinterpret_cast<const f32x4*>(src + UNITS * 4), b1 = *reinterpret_cast<const f32x4*>(src + UNITS * 4 + 16);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) { u[8 * k + q] = b0[q] + bias1[q]; u[8 * k + 4 + q] = b1[q] + bias1[4 + q]; }
+        }
+      });
+      if constexpr (EPI == EPI_PARTIAL) {
+        store([&](int m) { return elem_ptr<float>(p.partial, m, p.N, n); }, v);
+      } else {
+        if (p.flags & 1) {
+          store([&](int m) { return elem_ptr<IoT>(p.aux, m, p.ld_aux, n); }, v);
+          if constexpr (GATED) store([&](int m) { return elem_ptr<IoT>(p.aux, m, p.ld_aux, p.half + n); }, u);
+        }
+        if constexpr (GATED) linear_act<8 * U, true>(p.act, v, u, y);
+        else linear_act<8 * U, false>(p.act, v, v, y);
+#pragma unroll
+        for (int q = 0; q < 8 * U; ++q) y[q] += o[q];
+        store([&](int m) { return elem_ptr<IoT>(p.C0, m, p.ldc0, n); }, y);
+      }
+    }
+    wait_lgkmcnt0();   // read before the next rows are written
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
 // Workgroup b's tile.
 template <typename IoT, int BM, int BN, int EPI>
 __device__ __forceinline__ void mx_tile(const Mx4Gemm& a, int b, char* smem) {
@@ -133,12 +218,28 @@ __device__ __forceinline__ void mx_tile(const Mx4Gemm& a, int b, char* smem) {
   constexpr int N_DMA = DA::kInst + DB::kInst + 1;
   static_assert((NS - 1) * N_DMA < 64, "vmcnt range");
   const int planes = (p.K + BK - 1) / BK - kbeg / BK;
-  // K-step kt into ring stage st; steps past the end load zeros, and scales that are not used
+  auto issue_scales = [&](int kt, char* stage) {
+    if (SCH == 64 || lane < SCH) dma16(sc + (int64_t)min(kt, planes - 1) * sc_plane, stage + S_AT + wave * SCH * 16);
+  };
+  // DMA d of K-step kt into ring stage st; steps past the end load zeros, and scales that are not used. fast: the step
+  // is wholly in range and no row of the tile is clamped. (Without a branch: products sink below one.)
+  auto issue_one = [&](int kt, int st, int d, auto fast) {
+    char* stage = smem + st * STAGE;
+    if (d < DA::kInst) {
+      if constexpr (decltype(fast)::value) ka.issue_fast_i(stage, wave, d, kt * BK);
+      else ka.issue_i(stage, wave, lane, d, kt * BK, kend - kbeg, locA);
+    } else if (d < DA::kInst + DB::kInst) {
+      if constexpr (decltype(fast)::value) kb.issue_fast_i(stage + A_BYTES, wave, d - DA::kInst, kt * BK);
+      else kb.issue_i(stage + A_BYTES, wave, lane, d - DA::kInst, kt * BK, kend - kbeg, locB);
+    } else {
+      issue_scales(kt, stage);
+    }
+  };
   auto issue = [&](int kt, int st) {
     char* stage = smem + st * STAGE;
     ka.issue(stage, wave, lane, kt * BK, kend - kbeg, locA);
     kb.issue(stage + A_BYTES, wave, lane, kt * BK, kend - kbeg, locB);
-    if (SCH == 64 || lane < SCH) dma16(sc + (int64_t)min(kt, planes - 1) * sc_plane, stage + S_AT + wave * SCH * 16);
+    issue_scales(kt, stage);
   };
 
   const int frow = lane & 31, fhalf = lane >> 5;
@@ -202,7 +303,7 @@ __device__ __forceinline__ void mx_tile(const Mx4Gemm& a, int b, char* smem) {
   take_scales();
   wait_lgkmcnt0();
   int cur = 0;
-  for (int kt = 0; kt < nk; ++kt) {
+  auto k_step = [&](int kt, auto fast) {
     const int nxt = cur + 1 == NS ? 0 : cur + 1;
     read_frags(cur, 1, 1);
     mma_all(std::integral_constant<int, 0>{});
@@ -219,21 +320,25 @@ __device__ __forceinline__ void mx_tile(const Mx4Gemm& a, int b, char* smem) {
     wait_vmcnt<(NS - 2) * N_DMA>();
     wait_lgkmcnt0();
     __builtin_amdgcn_s_barrier();
-    issue(kt + NS, cur);
+#pragma unroll
+    for (int d = 0; d < N_DMA; ++d) issue_one(kt + NS, cur, d, fast);
     read_frags(nxt, 0, 0);
     read_scales(nxt);
     mma_all(std::integral_constant<int, 3>{});
-    interleave<N_MMA, 2 * N_RD, 0>();
+    interleave<N_MMA, 2 * N_RD, N_DMA>();
     take_scales();
     cur = nxt;
-  }
+  };
+  const int nk_main = ka.interior && kb.interior ? max(0, min(nk, (kend - kbeg) / BK - NS)) : 0;
+  int kt = 0;
+  for (; kt < nk_main; ++kt) k_step(kt, std::true_type{});
+  for (; kt < nk; ++kt) k_step(kt, std::false_type{});
   // the trailing DMAs have landed and no wave reads the ring any more: its LDS becomes the epilogue's staging area
   wait_vmcnt<0>();
   wait_lgkmcnt0();
   __builtin_amdgcn_s_barrier();
-  static_assert(epilogue_lds_bytes<BN, WAVES>() <= NS * STAGE, "epilogue staging must fit the ring");
-  if constexpr (ElemTraits<IoT>::bytes == 4 && EPI != EPI_PARTIAL) epilogue<EPI, IoT, BM, BN, MI, NI>(p, acc, 0, n0, 0, wm, wn, lane);
-  else epilogue_rows<EPI, IoT, BM, BN, MI, NI, WAVES, 2>(p, acc, 0, n0, 0, wm, wn, lane, wave, smem);
+  static_assert(mx_epilogue_bytes<BM, BN>() <= NS * STAGE, "epilogue staging must fit the ring");
+  mx_epilogue<EPI, IoT, BM, BN, MI, NI>(p, acc, n0, wm, wn, lane, wave, smem);
 }
 
 template <typename IoT, int BM, int BN, int EPI>
