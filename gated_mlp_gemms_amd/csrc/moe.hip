@@ -300,7 +300,8 @@ template <typename F> hipError_t route_shape(int64_t E, F f) {
 // ---- balance loss ------------------------------------------------------------------------------
 
 // A token's probabilities, in place of its C scores a lane: softmax, or each expert's sigmoid divided by their sum (as
-// sigmoid_share). A token without any, and a lane past the row, has zeros.
+// sigmoid_share). A token without any, and a lane past the row, has zeros. The exponentials are the hardware's, off by the
+// rounding of their argument, |x| half steps (expf is a dozen instructions; 16384 x 128: 8.5 -> 7.1 us, the gradient 12.0 -> 11.2).
 template <int L, int C> __device__ __forceinline__ void balance_probs(int E, int lane, int sigmoid, float (&x)[C]) {
   uint32_t m = 0u;
 #pragma unroll
@@ -312,8 +313,8 @@ template <int L, int C> __device__ __forceinline__ void balance_probs(int E, int
 #pragma unroll
   for (int j = 0; j < C; ++j) {
     const bool in = lane * C + j < E;
-    if (sigmoid) x[j] = in ? (x[j] < 0.0f ? expf(x[j] - shift) / (1.0f + expf(x[j])) : sigmoid_of(x[j]).q) : 0.0f;
-    else x[j] = in ? expf(x[j] - shift) : 0.0f;
+    if (sigmoid) x[j] = in ? (x[j] < 0.0f ? __expf(x[j] - shift) / (1.0f + __expf(x[j])) : 1.0f / (1.0f + __expf(-x[j]))) : 0.0f;
+    else x[j] = in ? __expf(x[j] - shift) : 0.0f;
     part += x[j];
   }
   const float r = 1.0f / group_sum<L>(part);
@@ -321,59 +322,11 @@ template <int L, int C> __device__ __forceinline__ void balance_probs(int E, int
   for (int j = 0; j < C; ++j) x[j] = none ? 0.0f : x[j] * r;
 }
 
-// The workgroup's share of the tokens, `chunk` of them: its sums of the probabilities into part_p [E], its tokens an
-// expert and its tokens that count into part_c [E + 1]. A lane has the same experts in every token, so their
-// sums stay in registers; the groups of a wave, then the waves, are joined in order.
-// 16384 x 128: bound by the exponentials and by a workgroup's handful of trips to memory one after another.
-template <typename T, int L, int C>
-__global__ __launch_bounds__(kRouteThreads) void balance_kernel(const void* __restrict__ logits, const int* __restrict__ ids,
-                                                                const uint8_t* __restrict__ mask, int64_t tokens, int E,
-                                                                int k, int sigmoid, int64_t chunk, float* __restrict__ part_p,
-                                                                int* __restrict__ part_c) {
-  constexpr int R = kRouteThreads / L, W = kRouteThreads / 64;
-  __shared__ int cnt[MOE_MAX_EXPERTS + 1];
-  __shared__ float sums[W][L * C];
-  const int tid = threadIdx.x, lane = tid & (L - 1);
-  for (int e = tid; e <= E; e += kRouteThreads) cnt[e] = 0;
-  __syncthreads();
-  const int64_t beg = blockIdx.x * chunk, end = min(tokens, beg + chunk);
-  float acc[C] = {};
-  int seen = 0;
-  for (int64_t t0 = beg; t0 < end; t0 += R) {
-    const int64_t t = t0 + tid / L;
-    const bool live = t < end && (mask == nullptr || mask[t] != 0);
-    float x[C];
-    load_scores<T, C>(logits, t, E, lane, live, 0.0f, x);
-    balance_probs<L, C>(E, lane, sigmoid, x);
-#pragma unroll
-    for (int j = 0; j < C; ++j) acc[j] += live ? x[j] : 0.0f;
-    seen += live ? 1 : 0;
-  }
-  for (int64_t i = beg * k + tid; i < end * k; i += kRouteThreads) {
-    const int id = ids[i];
-    if ((uint32_t)id < (uint32_t)E && (mask == nullptr || mask[i / k] != 0)) atomicAdd(&cnt[id], 1);
-  }
-  if (lane == 0) atomicAdd(&cnt[E], seen);
-#pragma unroll
-  for (int j = 0; j < C; ++j) {
-#pragma unroll
-    for (int o = L; o < 64; o <<= 1) acc[j] += __shfl_xor(acc[j], o);
-    if ((tid & 63) < L) sums[tid >> 6][lane * C + j] = acc[j];
-  }
-  __syncthreads();
-  for (int e = tid; e < E; e += kRouteThreads) {
-    float s = sums[0][e];
-#pragma unroll
-    for (int w = 1; w < W; ++w) s += sums[w][e];
-    part_p[(int64_t)blockIdx.x * E + e] = s;
-  }
-  for (int e = tid; e <= E; e += kRouteThreads) part_c[(int64_t)blockIdx.x * (E + 1) + e] = cnt[e];
-}
-
-// The workgroups' shares added up, by one workgroup: 2^sh >= E threads an expert's run of parts beside one another, joined in order.
-__global__ __launch_bounds__(1024) void balance_join_kernel(const float* __restrict__ part_p, const int* __restrict__ part_c,
-                                                            int parts, int E, int k, int sh, int* __restrict__ counts,
-                                                            float* __restrict__ shares, float* __restrict__ loss) {
+// The parts' sums added up, by one workgroup of 1024 threads: 2^sh >= E threads an expert's run of parts beside one another,
+// joined in order.
+__device__ __forceinline__ void balance_finish(const float* part_p, const int* part_c, int parts, int E, int k, int sh,
+                                               int* __restrict__ counts, float* __restrict__ shares,
+                                               float* __restrict__ loss) {
   __shared__ float ps[1024];
   __shared__ int cs[1024];
   __shared__ int live;
@@ -416,6 +369,74 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(const float* __restr
   counts[E] = n;
   loss[0] = (float)E * v;
 }
+__global__ __launch_bounds__(1024) void balance_join_kernel(const float* __restrict__ part_p, const int* __restrict__ part_c,
+                                                            int parts, int E, int k, int sh, int* __restrict__ counts,
+                                                            float* __restrict__ shares, float* __restrict__ loss) {
+  balance_finish(part_p, part_c, parts, E, k, sh, counts, shares, loss);
+}
+
+// The workgroup's share of the tokens, `chunk` of them: its sums of the probabilities into part_p [E], its tokens an
+// expert and its tokens that count into part_c [E + 1]. A lane has the same experts in every token, so their
+// sums stay in registers; the groups of a wave, then the waves, are joined in order. A workgroup that has every token
+// finishes by itself. 16384 x 128: bound by its trips to memory, so kBalanceAtOnce tokens of a group are under way at once, and
+// the mask, read beside them, only chooses what is added (256 threads, a token at a time 15.6 us).
+constexpr int kBalanceThreads = 1024, kBalanceAtOnce = 2;
+template <typename T, int L, int C>
+__global__ __launch_bounds__(kBalanceThreads) void balance_kernel(const void* __restrict__ logits, const int* __restrict__ ids,
+                                                                  const uint8_t* __restrict__ mask, int64_t tokens, int E,
+                                                                  int k, int sigmoid, int64_t chunk, float* part_p,
+                                                                  int* part_c, int sh, int* __restrict__ counts,
+                                                                  float* __restrict__ shares, float* __restrict__ loss) {
+  constexpr int R = kBalanceThreads / L, W = kBalanceThreads / 64, U = kBalanceAtOnce;
+  __shared__ int cnt[MOE_MAX_EXPERTS + 1];
+  __shared__ float sums[W][L * C];
+  const int tid = threadIdx.x, lane = tid & (L - 1);
+  for (int e = tid; e <= E; e += kBalanceThreads) cnt[e] = 0;
+  __syncthreads();
+  const int64_t beg = blockIdx.x * chunk, end = min(tokens, beg + chunk);
+  float acc[C] = {};
+  int seen = 0;
+  for (int64_t t0 = beg; t0 < end; t0 += R * U) {
+    float x[U][C];
+    bool live[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t t = t0 + u * R + tid / L;
+      load_scores<T, C>(logits, t, E, lane, t < end, 0.0f, x[u]);
+      live[u] = t < end && (mask == nullptr || mask[t] != 0);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      balance_probs<L, C>(E, lane, sigmoid, x[u]);
+#pragma unroll
+      for (int j = 0; j < C; ++j) acc[j] += live[u] ? x[u][j] : 0.0f;
+      seen += live[u] ? 1 : 0;
+    }
+  }
+  for (int64_t i = beg * k + tid; i < end * k; i += kBalanceThreads) {
+    const int id = ids[i];
+    const bool live = mask == nullptr || mask[i / k] != 0;
+    if ((uint32_t)id < (uint32_t)E && live) atomicAdd(&cnt[id], 1);
+  }
+  if (lane == 0) atomicAdd(&cnt[E], seen);
+#pragma unroll
+  for (int j = 0; j < C; ++j) {
+#pragma unroll
+    for (int o = L; o < 64; o <<= 1) acc[j] += __shfl_xor(acc[j], o);
+    if ((tid & 63) < L) sums[tid >> 6][lane * C + j] = acc[j];
+  }
+  __syncthreads();
+  for (int e = tid; e < E; e += kBalanceThreads) {
+    float s = sums[0][e];
+#pragma unroll
+    for (int w = 1; w < W; ++w) s += sums[w][e];
+    part_p[(int64_t)blockIdx.x * E + e] = s;
+  }
+  for (int e = tid; e <= E; e += kBalanceThreads) part_c[(int64_t)blockIdx.x * (E + 1) + e] = cnt[e];
+  if (gridDim.x > 1) return;
+  __syncthreads();
+  balance_finish(part_p, part_c, 1, E, k, sh, counts, shares, loss);
+}
 
 // The gradient: with a_e = dloss E counts_e / (n^2 k) and m = sum_e p_e a_e, p_e (a_e - m), of sigmoid scores times
 // 1 - q_e; on top of the chosen weights' (dweights NULL: none), both rounded once.
@@ -429,16 +450,19 @@ __global__ __launch_bounds__(kRouteThreads) void balance_bwd_kernel(const void* 
                                                                     void* __restrict__ dlogits) {
   constexpr int R = kRouteThreads / L;
   const int lane = threadIdx.x & (L - 1);
+  int c[C];   // loaded at once, whatever is past the experts
+#pragma unroll
+  for (int j = 0; j < C; ++j) c[j] = counts[min(lane * C + j, E)];
   const float n = (float)counts[E];
   const float each = n > 0.0f ? (dloss != nullptr ? dloss[0] : 1.0f) * ((float)E / (n * (float)k)) / n : 0.0f;
   float a[C];
 #pragma unroll
-  for (int j = 0; j < C; ++j) a[j] = lane * C + j < E ? each * (float)counts[lane * C + j] : 0.0f;
+  for (int j = 0; j < C; ++j) a[j] = lane * C + j < E ? each * (float)c[j] : 0.0f;
   for (int64_t t0 = (int64_t)blockIdx.x * R; t0 < tokens; t0 += (int64_t)gridDim.x * R) {
     const int64_t t = t0 + threadIdx.x / L;
     const bool in = t < tokens, live = in && (mask == nullptr || mask[t] != 0);
     float x[C], d[C], rest[C];
-    load_scores<T, C>(logits, t, E, lane, live, 0.0f, x);
+    load_scores<T, C>(logits, t, E, lane, in, 0.0f, x);   // (not `live`: the mask would be one more trip to memory first)
 #pragma unroll
     for (int j = 0; j < C; ++j) rest[j] = sigmoid ? sigmoid_of(x[j]).rest : 1.0f;
     balance_probs<L, C>(E, lane, sigmoid, x);
@@ -725,15 +749,16 @@ hipError_t run_moe_route_bwd(DType dt, const void* logits, const int* ids, const
   });
 }
 
-// Tokens of a workgroup of balance_kernel: two turns at least, at most kBalanceParts workgroups.
-constexpr int64_t kBalanceParts = 128;
+// Tokens of a workgroup of balance_kernel: whole turns of its groups, at most kBalanceParts workgroups; few tokens one workgroup.
+constexpr int64_t kBalanceParts = 128, kBalanceSingle = 4;   // (turns)
 static int64_t balance_chunk(int64_t T, int E) {
   int64_t r = 1;
   (void)route_shape(E, [&](auto l, auto) {
-    r = kRouteThreads / decltype(l)::value;
+    r = kBalanceThreads / decltype(l)::value;
     return hipSuccess;
   });
-  return std::max<int64_t>(2 * r, ((T + kBalanceParts - 1) / kBalanceParts + r - 1) / r * r);
+  if (T <= kBalanceSingle * r) return kBalanceSingle * r;
+  return std::max<int64_t>(kBalanceAtOnce * r, ((T + kBalanceParts - 1) / kBalanceParts + r - 1) / r * r);
 }
 int moe_balance_parts(int64_t T, int E) {
   const int64_t c = balance_chunk(T, E);
@@ -745,19 +770,19 @@ hipError_t run_moe_balance(DType dt, const void* logits, const int* ids, const u
   const int parts = moe_balance_parts(T, E);
   float* part_p = static_cast<float*>(ws);
   int* part_c = reinterpret_cast<int*>(part_p + (int64_t)parts * E);
+  int sh = 6;
+  while ((1 << sh) < E) ++sh;
   if (parts > 0) {
     const hipError_t e = by_type(dt, [&](auto v) {
       return route_shape(E, [&](auto l, auto c) {
         hipLaunchKernelGGL((balance_kernel<decltype(v), decltype(l)::value, decltype(c)::value>), dim3(parts),
-                           dim3(kRouteThreads), 0, s, logits, ids, mask, T, E, k, sigmoid, balance_chunk(T, E), part_p,
-                           part_c);
+                           dim3(kBalanceThreads), 0, s, logits, ids, mask, T, E, k, sigmoid, balance_chunk(T, E), part_p,
+                           part_c, sh, counts, shares, loss);
         return hipGetLastError();
       });
     });
-    if (e != hipSuccess) return e;
+    if (e != hipSuccess || parts == 1) return e;
   }
-  int sh = 6;
-  while ((1 << sh) < E) ++sh;
   hipLaunchKernelGGL(balance_join_kernel, dim3(1), dim3(1024), 0, s, part_p, part_c, parts, E, k, sh, counts, shares, loss);
   return hipGetLastError();
 }

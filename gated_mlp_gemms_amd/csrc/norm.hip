@@ -12,15 +12,15 @@ namespace {
 // wave is one run of memory. L < 256: 256 / L rows a workgroup; else a workgroup a row.
 template <int L> constexpr int norm_threads() { return L < 256 ? 256 : L; }
 
-// The sum over a row's L threads, in every one of them. Wider rows than a wave: each wave leaves its part in `slot`; a
-// caller alternates between two slots, so that one barrier a sum is enough.
+// The sum over a row's L threads, in every one of them. Wider rows than a wave: each wave leaves its part in `slot`, the row's
+// own; a caller alternates between two slots, so that one barrier a sum is enough.
 template <int L> __device__ __forceinline__ float row_sum(float v, float* slot) {
   if constexpr (L <= 64) {
     return group_sum<L>(v);
   } else {
     constexpr int W = L / 64;
     v = group_sum<64>(v);
-    if ((threadIdx.x & 63) == 0) slot[threadIdx.x >> 6] = v;
+    if ((threadIdx.x & 63) == 0) slot[threadIdx.x % L / 64] = v;
     __syncthreads();
     float s = 0.0f;
 #pragma unroll
@@ -35,11 +35,12 @@ template <int L> __device__ __forceinline__ void row_sum2(float& a, float& b, fl
     b = group_sum<L>(b);
   } else {
     constexpr int W = L / 64;
+    const int wave = threadIdx.x % L / 64;
     a = group_sum<64>(a);
     b = group_sum<64>(b);
     if ((threadIdx.x & 63) == 0) {
-      slot[threadIdx.x >> 6] = a;
-      slot[W + (threadIdx.x >> 6)] = b;
+      slot[wave] = a;
+      slot[W + wave] = b;
     }
     __syncthreads();
     a = b = 0.0f;
@@ -106,8 +107,8 @@ __device__ __forceinline__ u32x4 norm_piece(const NormFwd& a, int c, u32x4 h, fl
 template <typename T, typename W, int L, int P>
 __global__ __launch_bounds__(norm_threads<L>()) void norm_fwd_kernel(const NormFwd a) {
   constexpr int N = Piece<T>::N, R = norm_threads<L>() / L;
-  __shared__ float slots[2][L > 64 ? L / 64 : 1];
-  const int lane = threadIdx.x % L;
+  __shared__ float slots[2][L > 64 ? norm_threads<L>() / 64 : 1];
+  const int lane = threadIdx.x % L, own = L > 64 ? threadIdx.x / L * (L / 64) : 0;
   for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.rows; r0 += (int64_t)gridDim.x * R) {
     const int64_t row = r0 + threadIdx.x / L;
     const bool live = row < a.rows;
@@ -141,7 +142,7 @@ __global__ __launch_bounds__(norm_threads<L>()) void norm_fwd_kernel(const NormF
 #pragma unroll
         for (int r = 0; r < N; ++r) sum += f[r];
       }
-      m = row_sum<L>(sum, slots[0]) * a.inv_d;
+      m = row_sum<L>(sum, slots[0] + own) * a.inv_d;
     }
     float sq = 0.0f;
 #pragma unroll
@@ -153,7 +154,7 @@ __global__ __launch_bounds__(norm_threads<L>()) void norm_fwd_kernel(const NormF
       sq += in[i] ? part : 0.0f;   // (what is past the row is 0, not m)
     }
     if (!a.layer && L > 64) __syncthreads();   // the other sum's barrier: every wave has read the last row's slot
-    const float s = 1.0f / __builtin_sqrtf(row_sum<L>(sq, slots[1]) * a.inv_d + a.eps);
+    const float s = 1.0f / __builtin_sqrtf(row_sum<L>(sq, slots[1] + own) * a.inv_d + a.eps);
     if (live && lane == 0) {
       if (a.mean != nullptr) a.mean[row] = m;
       if (a.rstd != nullptr) a.rstd[row] = s;
@@ -259,40 +260,54 @@ __device__ __forceinline__ u32x4 dx_piece(const float (&g)[N], const float (&n)[
 }
 
 // A workgroup takes every gridDim-th run of R rows. A thread has the same columns in every one of them, so their sums
-// over the rows stay in its registers; the R threads of a column are joined through LDS at the end, in order.
+// over the rows stay in its registers; the R threads of a column are joined through LDS at the end, in order. The next
+// rows are loaded before these are worked on.
 template <typename T, typename W, int L, int P>
-__global__ __launch_bounds__(256) void norm_bwd_kernel(const NormBwd a) {
-  constexpr int N = Piece<T>::N, R = 256 / L;
-  __shared__ float slots[2][L > 64 ? 2 * L / 64 : 1];
+__global__ __launch_bounds__(norm_threads<L>()) void norm_bwd_kernel(const NormBwd a) {
+  constexpr int N = Piece<T>::N, TH = norm_threads<L>(), R = TH / L;
+  __shared__ float slots[2][L > 64 ? 2 * TH / 64 : 1];
   __shared__ float joined[R > 1 ? 2 * L * P * N : 1];
   const int lane = threadIdx.x % L;
+  float* slot0 = slots[0] + (L > 64 ? threadIdx.x / L * (2 * L / 64) : 0);
+  float* slot1 = slots[1] + (L > 64 ? threadIdx.x / L * (2 * L / 64) : 0);
   float aw[P][N], ab[P][N];
 #pragma unroll
   for (int i = 0; i < P; ++i)
 #pragma unroll
     for (int r = 0; r < N; ++r) aw[i][r] = ab[i][r] = 0.0f;
+  struct Rows {
+    u32x4 dy[P], h[P], q[P];
+    float m, s;
+  };
+  auto load = [&](int64_t r0, Rows& x) {
+    const int64_t row = r0 + threadIdx.x / L;
+    const bool live = row < a.rows;
+    const int64_t base = row * a.pieces + lane;
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      const bool in = live && lane + i * L < a.pieces;
+      x.dy[i] = in ? a.dy[base + i * L] : zero;
+      x.h[i] = in ? a.h[base + i * L] : zero;
+      x.q[i] = in && a.dres != nullptr ? a.dres[base + i * L] : zero;
+    }
+    x.m = live && a.mean != nullptr ? a.mean[row] : 0.0f;
+    x.s = live ? a.rstd[row] : 0.0f;
+  };
+  Rows next;
+  load((int64_t)blockIdx.x * R, next);
   int turn = 0;
   for (int64_t r0 = (int64_t)blockIdx.x * R; r0 < a.rows; r0 += (int64_t)gridDim.x * R, turn ^= 1) {
     const int64_t row = r0 + threadIdx.x / L;
     const bool live = row < a.rows;
-    const int64_t base = row * a.pieces;
-    const u32x4 zero = {0u, 0u, 0u, 0u};
-    u32x4 dy[P], h[P], q[P];
-    bool in[P];
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      in[i] = live && lane + i * L < a.pieces;
-      dy[i] = in[i] ? a.dy[base + lane + i * L] : zero;
-      h[i] = in[i] ? a.h[base + lane + i * L] : zero;
-      q[i] = in[i] && a.dres != nullptr ? a.dres[base + lane + i * L] : zero;
-    }
-    const float m = live && a.mean != nullptr ? a.mean[row] : 0.0f, s = live ? a.rstd[row] : 0.0f;
+    const Rows x = next;
+    if (r0 + (int64_t)gridDim.x * R < a.rows) load(r0 + (int64_t)gridDim.x * R, next);
     float c1 = 0.0f, c2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      if (!in[i]) continue;
+      if (!live || lane + i * L >= a.pieces) continue;
       float y[N], n[N], g[N];
-      grad_piece<T, W>(a, lane + i * L, dy[i], h[i], m, s, y, n, g);
+      grad_piece<T, W>(a, lane + i * L, x.dy[i], x.h[i], x.m, x.s, y, n, g);
 #pragma unroll
       for (int r = 0; r < N; ++r) {
         c1 += g[r];
@@ -302,15 +317,15 @@ __global__ __launch_bounds__(256) void norm_bwd_kernel(const NormBwd a) {
       }
     }
     if (a.dx == nullptr) continue;   // (uniform)
-    row_sum2<L>(c1, c2, slots[turn]);
+    row_sum2<L>(c1, c2, turn ? slot1 : slot0);
     c1 = a.mean != nullptr ? c1 * a.inv_d : 0.0f;
     c2 *= a.inv_d;
 #pragma unroll
     for (int i = 0; i < P; ++i) {
-      if (!in[i]) continue;
+      if (!live || lane + i * L >= a.pieces) continue;
       float y[N], n[N], g[N];
-      grad_piece<T, W>(a, lane + i * L, dy[i], h[i], m, s, y, n, g);
-      a.dx[base + lane + i * L] = dx_piece<T>(g, n, s, c1, c2, a.dres != nullptr, q[i]);
+      grad_piece<T, W>(a, lane + i * L, x.dy[i], x.h[i], x.m, x.s, y, n, g);
+      a.dx[row * a.pieces + lane + i * L] = dx_piece<T>(g, n, x.s, c1, c2, a.dres != nullptr, x.q[i]);
     }
   }
   if (a.part == nullptr) return;
@@ -408,34 +423,40 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(const NormBwd a) {
   }
 }
 
-// The workgroups' column sums added up: 4 columns a thread, 32 threads a run of columns and 8 runs of the parts beside
-// one another, joined in order. blockIdx.y 0: dweight, 1: dbias.
-constexpr int kJoinCols = 128;
+// The workgroups' column sums added up: 16 columns (of dweight, then of dbias) a workgroup, 4 a thread, and 64 runs of the
+// parts beside one another, joined in order: of a wave's 16 by lanes, then the four waves.
+// 512 parts of 4096 columns: bound by a handful of trips to memory (with 8 runs 4.7 us, with 64 a third of that).
+constexpr int kJoinCols = 16;
 template <typename W>
 __global__ __launch_bounds__(256) void norm_join_kernel(const float* __restrict__ part, int parts, int64_t d, void* dw,
                                                         void* db, int accumulate) {
-  __shared__ f32x4 sums[8][32];
-  void* out = blockIdx.y == 0 ? dw : db;
-  if (out == nullptr) return;
-  const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
-  const int64_t c = (int64_t)blockIdx.x * kJoinCols + tx * 4;
+  __shared__ f32x4 sums[4][4];
+  const int tx = threadIdx.x & 3, run = threadIdx.x >> 2, wave = threadIdx.x >> 6;
+  const int64_t c = (int64_t)blockIdx.x * kJoinCols + tx * 4;   // d is a multiple of 4: a thread's columns are of one gradient
   f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
-  if (c < d) {
-    const float* p = part + (int64_t)blockIdx.y * d + c;
+  if (c < 2 * d) {
 #pragma unroll 8
-    for (int g = ty; g < parts; g += 8) s += *reinterpret_cast<const f32x4*>(p + (int64_t)g * 2 * d);
+    for (int g = run; g < parts; g += 64) s += *reinterpret_cast<const f32x4*>(part + (int64_t)g * 2 * d + c);
   }
-  sums[ty][tx] = s;
-  __syncthreads();
-  if (ty != 0 || c >= d) return;
 #pragma unroll
-  for (int g = 1; g < 8; ++g) s += sums[g][tx];
+  for (int o = 4; o < 64; o <<= 1) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) s[r] += __shfl_xor(s[r], o);
+  }
+  if ((threadIdx.x & 63) < 4) sums[wave][tx] = s;
+  __syncthreads();
+  if (run != 0 || c >= 2 * d) return;
+#pragma unroll
+  for (int w = 1; w < 4; ++w) s += sums[w][tx];
+  void* out = c < d ? dw : db;
+  if (out == nullptr) return;
+  const int64_t at = c < d ? c : c - d;
   if (accumulate) {
-    f32x4* o = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(out) + c);
+    f32x4* o = reinterpret_cast<f32x4*>(reinterpret_cast<float*>(out) + at);
     *o = *o + s;
   } else {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) store1<W>(out, c + r, s[r]);
+    for (int r = 0; r < 4; ++r) store1<W>(out, at + r, s[r]);
   }
 }
 
@@ -447,42 +468,41 @@ template <typename F> hipError_t norm_types(DType dt, bool wide, F f) {
   });
 }
 
-template <int L, int P> struct NormShape { static constexpr int lanes = L, per = P; };
+template <int L, int P> struct NormShape { static constexpr int lanes = L, per = P, rows = L < 256 ? 256 / L : 1; };
 
 constexpr int kNormPieces = 8192, kNormBwdPieces = 2048;   // the widest rows that registers hold
-constexpr int kNormParts = 512;                            // workgroups of a backward at most
 
-// Few rows: a workgroup a row instead of a wave.
-inline bool norm_few(int64_t rows) { return rows <= 1024; }
-
-// f(NormShape) for rows of `pieces` pieces that the register kernels take.
-template <typename F> hipError_t norm_shape(int64_t rows, int pieces, F f) {
+// f(NormShape) for rows of `pieces` pieces: few of them a thread, so that the backward's column sums (two fp32 an element)
+// leave room for several waves, and as few lanes idle as three pieces a thread allow. 8192 rows of 4096 bf16, residual, lanes x pieces
+// (us): forward 64 x 8 56.8, 128 x 4 50.0, 512 x 1 48.7; backward 64 x 8 101, 128 x 4 64, 256 x 2 62, 512 x 1 58.
+template <typename F> hipError_t norm_shape(int pieces, F f) {
   if (pieces <= 16) return f(NormShape<16, 1>{});
+  if (pieces <= 32) return f(NormShape<32, 1>{});
   if (pieces <= 64) return f(NormShape<64, 1>{});
-  if (!norm_few(rows)) {
-    if (pieces <= 128) return f(NormShape<64, 2>{});
-    if (pieces <= 256) return f(NormShape<64, 4>{});
-    if (pieces <= 512) return f(NormShape<64, 8>{});
-  }
-  if (pieces <= 512) return f(NormShape<256, 2>{});
-  if (pieces <= 1024) return f(NormShape<256, 4>{});
-  return f(NormShape<256, 8>{});
-}
-int norm_rows_at_once(int64_t rows, int pieces) {
-  int r = 1;
-  (void)norm_shape(rows, pieces, [&](auto s) {
-    r = s.lanes < 256 ? 256 / s.lanes : 1;
-    return hipSuccess;
-  });
-  return r;
+  if (pieces <= 128) return f(NormShape<128, 1>{});
+  if (pieces <= 192) return f(NormShape<64, 3>{});
+  if (pieces <= 256) return f(NormShape<256, 1>{});
+  if (pieces <= 384) return f(NormShape<128, 3>{});
+  if (pieces <= 512) return f(NormShape<512, 1>{});
+  if (pieces <= 768) return f(NormShape<256, 3>{});
+  if (pieces <= 1024) return f(NormShape<512, 2>{});
+  if (pieces <= 1536) return f(NormShape<512, 3>{});
+  return f(NormShape<1024, 2>{});
 }
 
 }  // namespace
 
+// Workgroups of a backward: a multiple of the CUs whose column sums are at most some 20 MB. Backward and join with 256, 512 and 1024
+// (us): 8192 rows of 4096 bf16 64 + 3, 57 + 3, 61 + 11; 4096 of 8192 63 + 4, 69 + 12, 76 + 21; 5003 of 1024 fp32 -, 20 + 3, 17 + 3.
 int norm_parts(int64_t rows, int pieces) {
   if (pieces > kNormBwdPieces) return (int)std::min<int64_t>(rows, 64);
-  const int r = norm_rows_at_once(rows, pieces);
-  return (int)std::min<int64_t>((rows + r - 1) / r, kNormParts);
+  int r = 1;
+  (void)norm_shape(pieces, [&](auto s) {
+    r = decltype(s)::rows;
+    return hipSuccess;
+  });
+  const int64_t most = std::min<int64_t>(1024, ((1 << 18) / pieces + 255) / 256 * 256);
+  return (int)std::min<int64_t>((rows + r - 1) / r, most);
 }
 
 hipError_t run_norm_fwd(DType dt, bool wide, const void* x, const void* res, const void* w, const void* b, int64_t rows,
@@ -502,7 +522,7 @@ hipError_t run_norm_fwd(DType dt, bool wide, const void* x, const void* res, con
       hipLaunchKernelGGL((norm_fwd_kernel<T, W, L, P>), dim3(item_grid(rows, TH / L)), dim3(TH), 0, s, a);
       return hipGetLastError();
     };
-    return pieces > kNormBwdPieces ? launch(NormShape<1024, 8>{}) : norm_shape(rows, pieces, launch);
+    return pieces > kNormBwdPieces ? launch(NormShape<1024, 8>{}) : norm_shape(pieces, launch);
   });
 }
 
@@ -529,14 +549,14 @@ hipError_t run_norm_bwd(DType dt, bool wide, const void* dy, const void* h, cons
         e = hipGetLastError();
       }
     } else {
-      e = norm_shape(rows, pieces, [&](auto shape) {
+      e = norm_shape(pieces, [&](auto shape) {
         constexpr int L = decltype(shape)::lanes, P = decltype(shape)::per;
-        hipLaunchKernelGGL((norm_bwd_kernel<T, W, L, P>), dim3(parts), dim3(256), 0, s, a);
+        hipLaunchKernelGGL((norm_bwd_kernel<T, W, L, P>), dim3(parts), dim3(norm_threads<L>()), 0, s, a);
         return hipGetLastError();
       });
     }
     if (e != hipSuccess || !sums) return e;
-    hipLaunchKernelGGL((norm_join_kernel<W>), dim3((unsigned)((d + kJoinCols - 1) / kJoinCols), 2), dim3(256), 0, s, part,
+    hipLaunchKernelGGL((norm_join_kernel<W>), dim3((unsigned)((2 * d + kJoinCols - 1) / kJoinCols)), dim3(256), 0, s, part,
                        parts, d, dw, db, accumulate);
     return hipGetLastError();
   });
