@@ -159,6 +159,12 @@ hipError_t run_mx4_values(DType dt, const void* codes, const void* scales, int64
 hipError_t run_mx4_linear_bf16(int epi, TileShape tile, const Mx4Gemm& a, hipStream_t s);
 hipError_t run_mx4_linear_f16(int epi, TileShape tile, const Mx4Gemm& a, hipStream_t s);
 hipError_t run_mx4_linear_f32(int epi, TileShape tile, const Mx4Gemm& a, hipStream_t s);
+// Few rows: 16 rows of one weight by 16 columns a workgroup. Taken up to kMxSkinnyRows rows of one weight, and up to
+// kMxExpertRows an expert on average. Streamed and in tiles (us): 16 rows of 4096 x 11008 8.9 and 9.3, 32 14.8 and 9.3, 32 of
+// 1024 x 1024 4.2 and 5.5, 16 of 2048 x 5504 gate and up 6.0 and 8.1; 64 experts of 2048 x 1376 gate and up, 2 rows each 42 and 48, 4 41
+// and 45, 8 43 and 45, 16 48 and 45; 16 experts of 4096 x 1024, 16 rows each 11.3 and 9.5.
+constexpr int kMxSkinnyRows = 16, kMxExpertRows = 8;
+hipError_t run_mx4_skinny(DType io, int gated, const Mx4Gemm& a, hipStream_t s);
 // fp32 sums of a.splits parts of K, a.g.partial [splits][M][N]; B1: more rows of B from a.g.b_split on
 hipError_t run_mx4_partial(TileShape tile, const Mx4Gemm& a, hipStream_t s);
 

@@ -70,17 +70,23 @@ const MxTile kMxTiles[] = {
 };
 
 struct MxPlan {
+  bool skinny;       // few rows: run_mx4_skinny
   TileShape tile;
   int bm, bn;        // rows and output columns of a tile
   int splits, kps;   // parts of K, bytes of codes of one
   double est;
 };
 
-// stacked: a gated product as one of 2N columns, whose partial sums are joined afterwards.
 MxPlan plan_product(const linear_desc* d) {
   const bool gated = is_gated(d->act);
   const int64_t M = d->M, E = d->experts, steps = mx_planes(d->K);
   MxPlan best{};
+  if (M <= (E ? kMxExpertRows * E : kMxSkinnyRows)) {
+    best.skinny = true;
+    best.bm = best.bn = 16;
+    best.splits = 1;
+    return best;
+  }
   best.est = 1e300;
   for (const MxTile& t : kMxTiles) {
     const int wide = t.t == TILE_64x64 && gated ? 2 * t.bn : t.bn;   // (its gate and up rows)
@@ -94,7 +100,7 @@ MxPlan plan_product(const linear_desc* d) {
       double est = tiles_time(t.st, t.slots, tiles * s, kps);
       if (s > 1) est += (2.0 * s + 1.0) * (double)M * (double)N * 4.0 / 6.0e12 + 4e-6;   // partial sums there and back, a launch
       if (est >= best.est * 0.98) continue;
-      best = {t.t, t.bm, bn, s, (int)(kps * (kMxPlane / 2)), est};
+      best = {false, t.t, t.bm, bn, s, (int)(kps * (kMxPlane / 2)), est};
     }
   }
   return best;
@@ -233,6 +239,7 @@ mlp_status mx4_linear_fwd(const linear_desc* d, const void* x, const void* x_sca
     MLP_TRY(hip_status(run_mx4_partial(p.tile, a, s), "4-bit product (partial sums)"));
     return hip_status(run_linear_reduce(io, gated, g.partial, p.splits, join, s), "4-bit product (join)");
   }
+  if (p.skinny) return hip_status(run_mx4_skinny(io, gated, a, s), "4-bit product (few rows)");
   const int epi = gated ? EPI_LIN_GATED : EPI_LIN;
   switch (io) {
     case DT_BF16: return hip_status(run_mx4_linear_bf16(epi, p.tile, a, s), "4-bit product");
