@@ -97,7 +97,7 @@ def test_workspaces():
         gm.norm_workspace_bytes(1 << 31, 8)
     for M in (0, 1, 17, 1024, 1025, 1 << 20):
         for d in (4, 64, 4096, 16384, 16392, 1 << 17):
-            assert 256 <= gm.norm_workspace_bytes(M, d) <= max(256, 512 * 2 * d * 4 + 256)
+            assert 256 <= gm.norm_workspace_bytes(M, d) <= max(256, 1024 * 2 * d * 4 + 256)
 
 
 def test_balance_checks():
