@@ -107,7 +107,7 @@ struct Mx4Gemm {
   const int* offsets;
   int experts, rows;
   int64_t w_stride, ws_stride, bias_stride;
-  int grid, splits;   // workgroups, an upper bound of the tiles; parts of K
+  int tiles, splits;   // an upper bound of the tiles, those of every part of K; parts of K
 };
 
 // Up to kGroupMax independent GEMMs run by one launch (gemm_dma_group_kernel): member j covers

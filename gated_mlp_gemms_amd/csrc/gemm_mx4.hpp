@@ -5,6 +5,11 @@
 // K-step are 8 bytes a row, one run of memory for a tile's rows (mx4.h's planes): one more DMA a wave. In
 // substep s of four the lane half h takes block 4 h + s, so a lane's four scales of a step are the four bytes of one word, which
 // the instruction picks from by number.
+//
+// Four waves, 2 x 2, one a SIMD. Large products are bound by power: with random operands the 4-bit MFMA alone runs at 6 PFLOP/s
+// of its 8.4 with constant ones, with its LDS reads at 4.9, and with the DMAs a 256 x 256 tile's step takes 2.1 us
+// (4.1 PFLOP/s; 1.5 us with constant operands). Half steps of 64 bytes in a ring of four were no faster (a DMA of half lines
+// takes 1.28 us a step by itself, of whole ones 1.05).
 #pragma once
 
 #include "gemm_dma.hpp"
@@ -24,6 +29,245 @@ __device__ __forceinline__ void mx_mma(const u32x4& a, const u32x4& b, uint32_t 
   const i32x8 bv = {(int)b[0], (int)b[1], (int)b[2], (int)b[3], 0, 0, 0, 0};
   acc = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(av, bv, acc, 4, 4, S, (int)sa, S, (int)sb);   // 4: e2m1
 }
+
+// A tile: rows row0 .. row0 + rows - 1 of expert e (e = the number of experts: rows of none) by the columns from n0 on.
+struct MxPlace {
+  int e, rows, n0, split;
+  int64_t row0;
+};
+
+// Tile b of the product; false: there are no more.
+template <int BM, int BNC>
+__device__ __forceinline__ bool mx_place(const Mx4Gemm& a, int b, MxPlace& at) {
+  const int tiles_n = a.g.tiles_n;
+  int tile = 0, split = 0;
+  RowPiece t;
+  const bool found = find_row_piece(a.offsets, a.experts, a.rows, BM, [&](int total) {
+    const int tiles = (int)min((int64_t)total * tiles_n, (int64_t)(a.tiles / a.splits));
+    if (b >= tiles * a.splits) return -1;
+    tile = xcd_remap(b, tiles * a.splits);
+    split = tile / tiles;
+    tile -= split * tiles;
+    return tile / tiles_n;
+  }, t);
+  if (!found) return false;
+  int tm, tn;
+  grouped_tile(tile - t.first * tiles_n, (t.rows + BM - 1) / BM, tiles_n, a.g.group_m, tm, tn);
+  at = {t.e, min(t.rows - tm * BM, BM), tn * BNC, split, t.row0 + (int64_t)tm * BM};
+  return true;
+}
+
+// A tile of rows of no expert: zeros (plus the residual).
+template <typename IoT, int BNC, bool GATED>
+__device__ __forceinline__ void mx_zero_rows(const GemmArgs& p, const MxPlace& t) {
+  constexpr int V = 16 / ElemTraits<IoT>::bytes, W = BNC / V;
+  const u32x4 zero = {0u, 0u, 0u, 0u};
+  for (int i = threadIdx.x; i < t.rows * W; i += blockDim.x) {
+    const int64_t m = t.row0 + i / W;
+    const int n = t.n0 + i % W * V;
+    if (n >= p.N) continue;
+    if (p.flags & 1) {
+      *reinterpret_cast<u32x4*>(elem_ptr<IoT>(p.aux, m, p.ld_aux, n)) = zero;
+      if (GATED) *reinterpret_cast<u32x4*>(elem_ptr<IoT>(p.aux, m, p.ld_aux, p.half + n)) = zero;
+    }
+    *reinterpret_cast<u32x4*>(elem_ptr<IoT>(p.C0, m, p.ldc0, n)) =
+        p.res ? *reinterpret_cast<const u32x4*>(elem_ptr<IoT>(p.res, m, p.ld_res, n)) : zero;
+  }
+}
+
+// The K loop of a BM x BN tile of four waves, and its ring. GATED: half of the columns are rows of B0, half of B1.
+template <int BM, int BN, bool GATED> struct MxPipe {
+  static constexpr int WAVES = 4, WM = BM / 2, WN = BN / 2, MI = WM / 32, NI = WN / 32, BNC = GATED ? BN / 2 : BN;
+  static constexpr int BK = 128;   // bytes of a row in a step
+  static constexpr int A_BYTES = BM * BK, S_AT = (BM + BN) * BK, STAGE = mx_stage_bytes<BM, BN>();
+  static constexpr int NS = ring_stages(STAGE, BM * BN), SCH = (BM + BN) / 2 / WAVES;   // SCH: lanes of a wave's scale DMA
+  using DA = KTileDma<e4m3, BM, WAVES>;   // (a byte is its element)
+  using DB = KTileDma<e4m3, BN, WAVES>;
+  static constexpr int N_DMA = DA::kInst + DB::kInst + 1, N_MMA = MI * NI, N_RD = MI + NI;
+  static_assert(NS >= 2 && (NS - 1) * N_DMA < 64, "ring and vmcnt range");
+
+  char* smem;
+  int lane, wave, wm, wn, frow, fhalf;
+  // the tile that is loaded
+  DA ka;
+  DB kb;
+  const char* sc;        // per lane: its 16 bytes (two rows') of the first step's scales
+  int64_t sc_plane;
+  int rows, n0, N, b_split, k_left, planes;
+  bool stacked;
+  // the tile that is multiplied
+  int a_base[MI], b_base[NI];   // first tile row of each block
+  u32x4 fa[2][MI], fb[2][NI];
+  uint32_t sa[MI], sb[NI], na[MI], nb[NI];
+  f32x16 acc[MI][NI];
+
+  __device__ __forceinline__ void init(char* lds) {
+    smem = lds;
+    lane = threadIdx.x & 63;
+    wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    wm = wave / 2;
+    wn = wave % 2;
+    frow = lane & 31;
+    fhalf = lane >> 5;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) a_base[i] = wm * WM + i * 32;
+#pragma unroll
+    for (int j = 0; j < NI; ++j) {
+      constexpr int NH = NI / 2;
+      b_base[j] = !GATED ? wn * WN + j * 32 : j < NH ? wn * (WN / 2) + j * 32 : BN / 2 + wn * (WN / 2) + (j - NH) * 32;
+    }
+  }
+
+  // Tile t's operands: bytes [kbeg, kend) of the rows. Rows past the matrix are given an existing row, and pairs of scales past the
+  // padded rows the last one (their products are never stored).
+  __device__ __forceinline__ void place(const Mx4Gemm& a, const MxPlace& t, int kbeg, int kend) {
+    const GemmArgs& p = a.g;
+    constexpr int b_half = BN / 2;
+    rows = t.rows;
+    n0 = t.n0;
+    N = p.N;
+    b_split = p.b_split;
+    stacked = p.B1 != nullptr;
+    k_left = kend - kbeg;
+    planes = (p.K + BK - 1) / BK - kbeg / BK;
+    const char* a0 = static_cast<const char*>(p.A) + t.row0 * p.lda;
+    ka.init(lane, kbeg, a0, a0, p.lda, BM, rows == BM);
+    const char* w0 = static_cast<const char*>(p.B0) + t.e * a.w_stride;
+    const char* w1 = stacked ? static_cast<const char*>(p.B1) + t.e * a.w_stride : nullptr;
+    const char* b0 = w0 + (int64_t)n0 * p.ldb;
+    const bool inner = n0 + BNC <= N;
+    auto before = [&](int64_t rel) { return reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(w1) + rel * p.ldb); };
+    if constexpr (GATED) kb.init(lane, kbeg, b0, before(n0 - b_half), p.ldb, b_half, inner);
+    else if (stacked) kb.init(lane, kbeg, b0, before(n0 - b_split), p.ldb, b_split - n0, inner);
+    else kb.init(lane, kbeg, b0, b0, p.ldb, BN, inner);
+    const int q = 2 * (wave * SCH + lane);   // the first of the lane's two tile rows: A's, then B's
+    const char* base;
+    int64_t row;
+    if (q < BM) {
+      base = a.sa;
+      row = t.row0 + q;
+      sc_plane = a.sa_plane;
+    } else {
+      const int r = q - BM;
+      sc_plane = a.sb_plane;
+      const bool second = GATED ? r >= b_half : stacked && n0 + r >= b_split;
+      base = (second ? a.sb1 : a.sb0) + t.e * a.ws_stride;
+      row = GATED ? n0 + (r >= b_half ? r - b_half : r) : second ? n0 + r - b_split : n0 + r;
+    }
+    const int64_t last = sc_plane / 8 - 2;
+    sc = base + (row < last ? row : last) * 8 + (int64_t)(kbeg / BK) * sc_plane;
+  }
+  __device__ __forceinline__ int2 loc_a(int r) const { return make_int2(0, min(r, rows - 1)); }
+  __device__ __forceinline__ int2 loc_b(int r) const {
+    constexpr int b_half = BN / 2;
+    if constexpr (GATED) {
+      return r < b_half ? make_int2(0, min(n0 + r, N - 1) - n0) : make_int2(1, min(n0 + r - b_half, N - 1) - (n0 - b_half));
+    } else {
+      const int n = min(n0 + r, N - 1);
+      return make_int2(stacked && n >= b_split ? 1 : 0, n - n0);
+    }
+  }
+  // Steps below this are wholly in range, and no row is clamped: their DMAs need no work per lane.
+  __device__ __forceinline__ int fast_steps() const { return ka.interior && kb.interior ? k_left / BK : 0; }
+
+  // DMA d of step kt into ring stage st; steps past the end load zeros, and scales that are not used. (Without a branch:
+  // products sink below one.)
+  template <bool FAST> __device__ __forceinline__ void issue_one(int kt, int st, int d) const {
+    char* stage = smem + st * STAGE;
+    if (d < DA::kInst) {
+      if constexpr (FAST) ka.issue_fast_i(stage, wave, d, kt * BK);
+      else ka.issue_i(stage, wave, lane, d, kt * BK, k_left, [&](int r) { return loc_a(r); });
+    } else if (d < DA::kInst + DB::kInst) {
+      if constexpr (FAST) kb.issue_fast_i(stage + A_BYTES, wave, d - DA::kInst, kt * BK);
+      else kb.issue_i(stage + A_BYTES, wave, lane, d - DA::kInst, kt * BK, k_left, [&](int r) { return loc_b(r); });
+    } else if (SCH == 64 || lane < SCH) {
+      dma16(sc + (int64_t)min(kt, planes - 1) * sc_plane, stage + S_AT + wave * SCH * 16);
+    }
+  }
+  __device__ __forceinline__ void issue(int kt, int st) const {
+    if (kt < fast_steps()) {
+#pragma unroll
+      for (int d = 0; d < N_DMA; ++d) issue_one<true>(kt, st, d);
+    } else {
+#pragma unroll
+      for (int d = 0; d < N_DMA; ++d) issue_one<false>(kt, st, d);
+    }
+  }
+
+  __device__ __forceinline__ void read_frags(int st, int s, int slot) {
+    const char* stage = smem + st * STAGE;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) fa[slot][i] = DA::read_block(stage, a_base[i], frow, 4 * fhalf + s);
+#pragma unroll
+    for (int j = 0; j < NI; ++j) fb[slot][j] = DB::read_block(stage + A_BYTES, b_base[j], frow, 4 * fhalf + s);
+  }
+  __device__ __forceinline__ void read_scales(int st) {   // of the lane's row: the half's four bytes
+    const char* stage = smem + st * STAGE + S_AT;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) na[i] = *reinterpret_cast<const uint32_t*>(stage + (a_base[i] + frow) * 8 + 4 * fhalf);
+#pragma unroll
+    for (int j = 0; j < NI; ++j) nb[j] = *reinterpret_cast<const uint32_t*>(stage + (BM + b_base[j] + frow) * 8 + 4 * fhalf);
+  }
+  __device__ __forceinline__ void take_scales() {
+#pragma unroll
+    for (int i = 0; i < MI; ++i) sa[i] = na[i];
+#pragma unroll
+    for (int j = 0; j < NI; ++j) sb[j] = nb[j];
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  }
+  template <int S> __device__ __forceinline__ void mma() {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) mx_mma<S>(fb[S & 1][j], fa[S & 1][i], sb[j], sa[i], acc[i][j]);
+  }
+  // The first fragments of ring stage 0, whose step must have landed for every wave.
+  __device__ __forceinline__ void begin() {
+    wait_lgkmcnt0();
+    __builtin_amdgcn_s_barrier();
+    read_frags(0, 0, 0);
+    read_scales(0);
+    take_scales();
+    wait_lgkmcnt0();
+  }
+  // The step in stage cur, whose first fragments are there; then the DMAs of step kt of the tile that is loaded (ISSUE 1: a
+  // fast one, 2: any, 0: none) into that stage, and the next stage's first fragments. YOUNGER: memory operations that may
+  // be in flight besides NS - 2 steps' DMAs, made after the next step's.
+  template <int ISSUE, int YOUNGER> __device__ __forceinline__ void step(int kt, int& cur) {
+    const int nxt = cur + 1 == NS ? 0 : cur + 1;
+    read_frags(cur, 1, 1);
+    mma<0>();
+    interleave<N_MMA, N_RD, 0>();
+    read_frags(cur, 2, 0);
+    mma<1>();
+    interleave<N_MMA, N_RD, 0>();
+    read_frags(cur, 3, 1);
+    mma<2>();
+    interleave<N_MMA, N_RD, 0>();
+    // the next step must have landed; after the barrier every wave is done reading this stage
+    __builtin_amdgcn_sched_barrier(0);
+    wait_vmcnt<(NS - 2) * N_DMA + YOUNGER>();
+    wait_lgkmcnt0();
+    __builtin_amdgcn_s_barrier();
+    if constexpr (ISSUE != 0) {
+#pragma unroll
+      for (int d = 0; d < N_DMA; ++d) issue_one<ISSUE == 1>(kt, cur, d);
+    }
+    read_frags(nxt, 0, 0);
+    read_scales(nxt);
+    mma<3>();
+    interleave<N_MMA, 2 * N_RD, ISSUE != 0 ? N_DMA : 0>();
+    take_scales();
+    cur = nxt;
+  }
+};
 
 // The epilogue of a tile: the accumulators go to LDS (two block rows of 32 at a time, a wave its own), and come back as 8 consecutive
 // columns of a row a lane, U rows at a time: the loop is rolled and its activation's switch taken once for all U, as a wave
@@ -110,245 +354,136 @@ __device__ __forceinline__ void mx_epilogue(const GemmArgs& p, f32x16 (&acc)[MI]
   }
 }
 
-// Workgroup b's tile.
-template <typename IoT, int BM, int BN, int EPI>
-__device__ __forceinline__ void mx_tile(const Mx4Gemm& a, int b, char* smem) {
-  constexpr int WAVES = 4, WM = BM / 2, WN = BN / 2, MI = WM / 32, NI = WN / 32;
-  constexpr bool GATED = epi_gated(EPI);
-  constexpr int BNC = GATED ? BN / 2 : BN;
-  constexpr int BK = 128, NSUB = 4;
-  constexpr int A_BYTES = BM * BK, S_AT = (BM + BN) * BK, STAGE = mx_stage_bytes<BM, BN>();
-  constexpr int NS = ring_stages(STAGE, BM * BN);
-  static_assert(NS >= 2, "the ring needs two stages");
-  const int tiles_n = a.g.tiles_n;
-
-  int tile = 0, split = 0;
-  RowPiece t;
-  const bool found = find_row_piece(a.offsets, a.experts, a.rows, BM, [&](int total) {
-    const int tiles = (int)min((int64_t)total * tiles_n, (int64_t)(a.grid / a.splits));
-    if (b >= tiles * a.splits) return -1;
-    tile = xcd_remap(b, tiles * a.splits);
-    split = tile / tiles;
-    tile -= split * tiles;
-    return tile / tiles_n;
-  }, t);
-  if (!found) return;
-  GemmArgs p = a.g;
-  if (t.e == a.experts) {   // rows of no expert: zeros (plus the residual)
-    const int m0 = t.row0 + t.index * BM, m1 = min(m0 + BM, a.rows);
-    const int n0 = (tile % tiles_n) * BNC, n1 = min(n0 + BNC, p.N);
-    constexpr int V = 16 / ElemTraits<IoT>::bytes, W = BNC / V;
-    for (int i = threadIdx.x; i < BM * W; i += 64 * WAVES) {
-      const int m = m0 + i / W, n = n0 + i % W * V;
-      if (m >= m1 || n >= n1) continue;
-      const u32x4 zero = {0u, 0u, 0u, 0u};
-      if (p.flags & 1) {
-        *reinterpret_cast<u32x4*>(elem_ptr<IoT>(p.aux, m, p.ld_aux, n)) = zero;
-        if (GATED) *reinterpret_cast<u32x4*>(elem_ptr<IoT>(p.aux, m, p.ld_aux, p.half + n)) = zero;
+// The activation on a wave's accumulators and its rows to memory straight from registers, for 16-bit outputs without residual and
+// pre-activation. Lane l has row l % 32 of a block and, in register 4 g + r, column 8 g + 4 (l / 32) + r; swapping halves
+// between two g's registers leaves 8 consecutive columns a lane. Rows and columns past the tile are stored at an offset past
+// the buffer's end, which stores nothing and needs no branch. Against the way through LDS (us): 4096 x 4096 x 11008 132 and 119,
+// 32768 rows of 32 experts of 2048 x 1376 gate and up 163 and 148.
+template <typename IoT, int FN, bool GATED, int MI, int NI>
+__device__ __forceinline__ void mx_store_tile(const f32x16 (&acc)[MI][NI], __amdgpu_buffer_rsrc_t out, int ldc_bytes, int rows,
+                                              int cols, int m0, int c0, int frow, int fhalf) {
+  constexpr int NO = GATED ? NI / 2 : NI;
+  constexpr uint32_t kNowhere = 0x80000000u;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int m = m0 + i * 32 + frow;
+    const uint32_t row = m < rows ? (uint32_t)m * (uint32_t)ldc_bytes : kNowhere;
+#pragma unroll
+    for (int j = 0; j < NO; ++j) {
+      float v[16], u[16], y[16];
+#pragma unroll
+      for (int r = 0; r < 16; ++r) {
+        v[r] = acc[i][j][r];
+        u[r] = acc[i][GATED ? NO + j : j][r];
       }
-      *reinterpret_cast<u32x4*>(elem_ptr<IoT>(p.C0, m, p.ldc0, n)) =
-          p.res ? *reinterpret_cast<const u32x4*>(elem_ptr<IoT>(p.res, m, p.ld_res, n)) : zero;
+      linear_act<16, GATED>(FN, v, u, y);
+#pragma unroll
+      for (int g = 0; g < 4; g += 2) {
+        u32x4 w;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const auto s = __builtin_amdgcn_permlane32_swap(pack16x2<IoT>(y[4 * g + 2 * h], y[4 * g + 2 * h + 1]),
+                                                          pack16x2<IoT>(y[4 * g + 4 + 2 * h], y[4 * g + 5 + 2 * h]), false, false);
+          w[h] = s[0];
+          w[2 + h] = s[1];
+        }
+        const int c = c0 + j * 32 + 8 * g + 8 * fhalf;
+        __builtin_amdgcn_raw_buffer_store_b128(w, out, (int)(c < cols ? row + 2u * (uint32_t)c : kNowhere), 0, 0);
+      }
+      __builtin_amdgcn_sched_barrier(0);   // (else every block's accumulators are fetched at once)
     }
+  }
+}
+
+// Workgroup b's tile, any epilogue.
+template <typename IoT, int BM, int BN, int EPI, bool DIRECT>
+__device__ __forceinline__ void mx_tile(const Mx4Gemm& a, int b, char* smem) {
+  using Pipe = MxPipe<BM, BN, epi_gated(EPI)>;
+  constexpr int NS = Pipe::NS;
+  MxPlace t;
+  if (!mx_place<BM, Pipe::BNC>(a, b, t)) return;
+  if (t.e == a.experts) {
+    mx_zero_rows<IoT, Pipe::BNC, epi_gated(EPI)>(a.g, t);
     return;
   }
-  int tm, tn;
-  grouped_tile(tile - t.first * tiles_n, (t.rows + BM - 1) / BM, tiles_n, p.group_m, tm, tn);
-  const int64_t row0 = t.row0 + tm * BM;
-  const int rows = min(t.rows - tm * BM, BM), n0 = tn * BNC;
-  p.M = rows;
-  p.C0 = shift<IoT>(p.C0, row0 * p.ldc0);
-  p.aux = shift<IoT>(p.aux, row0 * p.ld_aux);
-  p.res = shift<IoT>(p.res, row0 * p.ld_res);
+  GemmArgs p = a.g;
+  p.M = t.rows;
+  p.C0 = shift<IoT>(p.C0, t.row0 * p.ldc0);
+  p.aux = shift<IoT>(p.aux, t.row0 * p.ld_aux);
+  p.res = shift<IoT>(p.res, t.row0 * p.ld_res);
   p.bias0 = shift<IoT>(p.bias0, t.e * a.bias_stride);
   p.bias1 = shift<IoT>(p.bias1, t.e * a.bias_stride);
-  if (EPI == EPI_PARTIAL) p.partial += ((int64_t)split * a.rows + row0) * p.N;
-  const int kbeg = split * p.k_per_split, kend = min(p.K, kbeg + p.k_per_split), nk = (kend - kbeg + BK - 1) / BK;
-
-  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = wave / 2, wn = wave % 2;
-
-  // ---- codes: rows past the matrix are given an existing row (their products are never stored)
-  using DA = KTileDma<e4m3, BM, WAVES>;   // a byte is its element
-  using DB = KTileDma<e4m3, BN, WAVES>;
-  DA ka;
-  DB kb;
-  constexpr int b_half = BN / 2;
-  auto locA = [&](int r) { return make_int2(0, min(r, rows - 1)); };
-  auto locB = [&](int r) {
-    if constexpr (GATED) {
-      return r < b_half ? make_int2(0, min(n0 + r, p.N - 1) - n0) : make_int2(1, min(n0 + r - b_half, p.N - 1) - (n0 - b_half));
-    } else {
-      const int n = min(n0 + r, p.N - 1);
-      return make_int2(p.B1 != nullptr && n >= p.b_split ? 1 : 0, n - n0);
-    }
-  };
-  const char* a0 = static_cast<const char*>(p.A) + row0 * p.lda;
-  ka.init(lane, kbeg, a0, a0, p.lda, BM, rows == BM);
-  const char* w0 = static_cast<const char*>(p.B0) + t.e * a.w_stride;
-  const char* w1 = p.B1 != nullptr ? static_cast<const char*>(p.B1) + t.e * a.w_stride : nullptr;
-  const char* b0 = w0 + (int64_t)n0 * p.ldb;
-  const bool inner = n0 + BNC <= p.N;
-  auto before = [&](int64_t rel) { return reinterpret_cast<const char*>(reinterpret_cast<uintptr_t>(w1) + rel * p.ldb); };
-  if constexpr (GATED) kb.init(lane, kbeg, b0, before(n0 - b_half), p.ldb, b_half, inner);
-  else if (w1 != nullptr) kb.init(lane, kbeg, b0, before(n0 - p.b_split), p.ldb, p.b_split - n0, inner);
-  else kb.init(lane, kbeg, b0, b0, p.ldb, BN, inner);
-
-  // ---- scales: 16 bytes (two rows) a lane; a pair past the padded rows takes the last one (its rows are never stored)
-  constexpr int SCH = (BM + BN) / 2 / WAVES;   // lanes of a wave
-  const char* sc;
-  int64_t sc_plane;
-  {
-    const int q = 2 * (wave * SCH + lane);   // the first of the two tile rows: A's, then B's
-    const char* base;
-    int64_t row;
-    if (q < BM) {
-      base = a.sa;
-      row = row0 + q;
-      sc_plane = a.sa_plane;
-    } else {
-      const int r = q - BM;
-      sc_plane = a.sb_plane;
-      const bool second = GATED ? r >= b_half : p.B1 != nullptr && n0 + r >= p.b_split;
-      base = (second ? a.sb1 : a.sb0) + t.e * a.ws_stride;
-      row = GATED ? n0 + (r >= b_half ? r - b_half : r) : second ? n0 + r - p.b_split : n0 + r;
-    }
-    const int64_t last = sc_plane / 8 - 2;
-    sc = base + (row < last ? row : last) * 8 + (int64_t)(kbeg / BK) * sc_plane;
-  }
-  constexpr int N_DMA = DA::kInst + DB::kInst + 1;
-  static_assert((NS - 1) * N_DMA < 64, "vmcnt range");
-  const int planes = (p.K + BK - 1) / BK - kbeg / BK;
-  auto issue_scales = [&](int kt, char* stage) {
-    if (SCH == 64 || lane < SCH) dma16(sc + (int64_t)min(kt, planes - 1) * sc_plane, stage + S_AT + wave * SCH * 16);
-  };
-  // DMA d of K-step kt into ring stage st; steps past the end load zeros, and scales that are not used. fast: the step
-  // is wholly in range and no row of the tile is clamped. (Without a branch: products sink below one.)
-  auto issue_one = [&](int kt, int st, int d, auto fast) {
-    char* stage = smem + st * STAGE;
-    if (d < DA::kInst) {
-      if constexpr (decltype(fast)::value) ka.issue_fast_i(stage, wave, d, kt * BK);
-      else ka.issue_i(stage, wave, lane, d, kt * BK, kend - kbeg, locA);
-    } else if (d < DA::kInst + DB::kInst) {
-      if constexpr (decltype(fast)::value) kb.issue_fast_i(stage + A_BYTES, wave, d - DA::kInst, kt * BK);
-      else kb.issue_i(stage + A_BYTES, wave, lane, d - DA::kInst, kt * BK, kend - kbeg, locB);
-    } else {
-      issue_scales(kt, stage);
-    }
-  };
-  auto issue = [&](int kt, int st) {
-    char* stage = smem + st * STAGE;
-    ka.issue(stage, wave, lane, kt * BK, kend - kbeg, locA);
-    kb.issue(stage + A_BYTES, wave, lane, kt * BK, kend - kbeg, locB);
-    issue_scales(kt, stage);
-  };
-
-  const int frow = lane & 31, fhalf = lane >> 5;
-  int a_base[MI], b_base[NI];
+  if (EPI == EPI_PARTIAL) p.partial += ((int64_t)t.split * a.rows + t.row0) * p.N;
+  const int kbeg = t.split * p.k_per_split, kend = min(p.K, kbeg + p.k_per_split);
+  const int nk = (kend - kbeg + Pipe::BK - 1) / Pipe::BK;
+  Pipe k;
+  k.init(smem);
+  k.place(a, t, kbeg, kend);
 #pragma unroll
-  for (int i = 0; i < MI; ++i) a_base[i] = wm * WM + i * 32;
-#pragma unroll
-  for (int j = 0; j < NI; ++j) {
-    if constexpr (GATED) {
-      constexpr int NH = NI / 2;
-      b_base[j] = j < NH ? wn * (WN / 2) + j * 32 : BN / 2 + wn * (WN / 2) + (j - NH) * 32;
-    } else {
-      b_base[j] = wn * WN + j * 32;
-    }
-  }
-  u32x4 fa[2][MI], fb[2][NI];
-  uint32_t sa[MI], sb[NI], na[MI], nb[NI];
-  auto read_frags = [&](int st, int s, int slot) {
-    const char* stage = smem + st * STAGE;
-#pragma unroll
-    for (int i = 0; i < MI; ++i) fa[slot][i] = DA::read_block(stage, a_base[i], frow, 4 * fhalf + s);
-#pragma unroll
-    for (int j = 0; j < NI; ++j) fb[slot][j] = DB::read_block(stage + A_BYTES, b_base[j], frow, 4 * fhalf + s);
-  };
-  auto read_scales = [&](int st) {   // of the lane's row: the half's four bytes
-    const char* stage = smem + st * STAGE + S_AT;
-#pragma unroll
-    for (int i = 0; i < MI; ++i) na[i] = *reinterpret_cast<const uint32_t*>(stage + (a_base[i] + frow) * 8 + 4 * fhalf);
-#pragma unroll
-    for (int j = 0; j < NI; ++j) nb[j] = *reinterpret_cast<const uint32_t*>(stage + (BM + b_base[j] + frow) * 8 + 4 * fhalf);
-  };
-  auto take_scales = [&] {
-#pragma unroll
-    for (int i = 0; i < MI; ++i) sa[i] = na[i];
-#pragma unroll
-    for (int j = 0; j < NI; ++j) sb[j] = nb[j];
-  };
-  f32x16 acc[MI][NI];
-#pragma unroll
-  for (int i = 0; i < MI; ++i)
+  for (int s = 0; s < NS; ++s) k.issue(s, s);
+  wait_vmcnt<(NS - 1) * Pipe::N_DMA>();   // step 0 landed
+  k.begin();
+  if (DIRECT && p.bias0 != nullptr) {   // the sums start from the bias: a lane's columns of block j are 8 g + 4 (l / 32) + r
+    constexpr int NI = Pipe::NI, NO = epi_gated(EPI) ? NI / 2 : NI;
 #pragma unroll
     for (int j = 0; j < NI; ++j)
 #pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
-  auto mma_all = [&](auto sub) {
-    constexpr int S = decltype(sub)::value;
+      for (int g = 0; g < 4; ++g) {
+        const int n = t.n0 + k.wn * (Pipe::BNC / 2) + (j % NO) * 32 + 8 * g + 4 * k.fhalf;
+        float f[4];
+        Vec4<IoT>::load(elem_ptr<IoT>(j < NO ? p.bias0 : p.bias1, 0, 0, n < p.N ? n : 0), f);
 #pragma unroll
-    for (int i = 0; i < MI; ++i)
+        for (int r = 0; r < 4; ++r)
 #pragma unroll
-      for (int j = 0; j < NI; ++j) mx_mma<S>(fb[S & 1][j], fa[S & 1][i], sb[j], sa[i], acc[i][j]);
-  };
-  constexpr int N_MMA = MI * NI, N_RD = MI + NI;
-
-#pragma unroll
-  for (int s = 0; s < NS; ++s) issue(s, s);
-  wait_vmcnt<(NS - 1) * N_DMA>();   // step 0 landed
-  wait_lgkmcnt0();
-  __builtin_amdgcn_s_barrier();
-  read_frags(0, 0, 0);
-  read_scales(0);
-  take_scales();
-  wait_lgkmcnt0();
-  int cur = 0;
-  auto k_step = [&](int kt, auto fast) {
-    const int nxt = cur + 1 == NS ? 0 : cur + 1;
-    read_frags(cur, 1, 1);
-    mma_all(std::integral_constant<int, 0>{});
-    interleave<N_MMA, N_RD, 0>();
-    read_frags(cur, 2, 0);
-    mma_all(std::integral_constant<int, 1>{});
-    interleave<N_MMA, N_RD, 0>();
-    read_frags(cur, 3, 1);
-    mma_all(std::integral_constant<int, 2>{});
-    interleave<N_MMA, N_RD, 0>();
-    // step kt+1 must have landed (NS-2 younger steps may be in flight); after the barrier every wave is done reading
-    // this stage, which takes step kt+NS
-    __builtin_amdgcn_sched_barrier(0);
-    wait_vmcnt<(NS - 2) * N_DMA>();
-    wait_lgkmcnt0();
-    __builtin_amdgcn_s_barrier();
-#pragma unroll
-    for (int d = 0; d < N_DMA; ++d) issue_one(kt + NS, cur, d, fast);
-    read_frags(nxt, 0, 0);
-    read_scales(nxt);
-    mma_all(std::integral_constant<int, 3>{});
-    interleave<N_MMA, 2 * N_RD, N_DMA>();
-    take_scales();
-    cur = nxt;
-  };
-  const int nk_main = ka.interior && kb.interior ? max(0, min(nk, (kend - kbeg) / BK - NS)) : 0;
-  int kt = 0;
-  for (; kt < nk_main; ++kt) k_step(kt, std::true_type{});
-  for (; kt < nk; ++kt) k_step(kt, std::false_type{});
+          for (int i = 0; i < Pipe::MI; ++i) k.acc[i][j][4 * g + r] = f[r];
+      }
+  } else {
+    k.clear();
+  }
+  const int fast = k.fast_steps() - NS;
+  int cur = 0, kt = 0;
+  for (; kt < min(nk, fast); ++kt) k.template step<1, 0>(kt + NS, cur);
+  for (; kt < nk; ++kt) k.template step<2, 0>(kt + NS, cur);
+  if constexpr (DIRECT) {
+    const auto out = __builtin_amdgcn_make_buffer_rsrc(elem_ptr<IoT>(p.C0, 0, 0, t.n0), 0, 0x7fffffff, 0x00020000);
+    auto store = [&](auto fn) {
+      mx_store_tile<IoT, decltype(fn)::value, epi_gated(EPI)>(k.acc, out, (int)p.ldc0 * 2, t.rows, p.N - t.n0, k.wm * Pipe::WM,
+                                                              k.wn * (Pipe::BNC / 2), k.frow, k.fhalf);
+    };
+    switch (p.act) {   // (once a tile: a switch inside would be one a block)
+      case FN_SILU: store(std::integral_constant<int, FN_SILU>{}); break;
+      case FN_GELU_TANH: store(std::integral_constant<int, FN_GELU_TANH>{}); break;
+      case FN_RELU: store(std::integral_constant<int, FN_RELU>{}); break;
+      case FN_SIGMOID: store(std::integral_constant<int, FN_SIGMOID>{}); break;
+      case FN_RELU_SQ: store(std::integral_constant<int, FN_RELU_SQ>{}); break;
+      default: store(std::integral_constant<int, FN_NONE>{});
+    }
+    wait_vmcnt<0>();
+    return;
+  }
   // the trailing DMAs have landed and no wave reads the ring any more: its LDS becomes the epilogue's staging area
   wait_vmcnt<0>();
   wait_lgkmcnt0();
   __builtin_amdgcn_s_barrier();
-  static_assert(mx_epilogue_bytes<BM, BN>() <= NS * STAGE, "epilogue staging must fit the ring");
-  mx_epilogue<EPI, IoT, BM, BN, MI, NI>(p, acc, n0, wm, wn, lane, wave, smem);
+  static_assert(mx_epilogue_bytes<BM, BN>() <= NS * Pipe::STAGE, "epilogue staging must fit the ring");
+  mx_epilogue<EPI, IoT, BM, BN, Pipe::MI, Pipe::NI>(p, k.acc, t.n0, k.wm, k.wn, k.lane, k.wave, smem);
 }
 
-template <typename IoT, int BM, int BN, int EPI>
+template <typename IoT, int BM, int BN, int EPI, bool DIRECT>
 __global__ __launch_bounds__(256, 1) void mx_kernel(const Mx4Gemm a) {
   __shared__ __attribute__((aligned(1024))) char smem[mx_ring_bytes<BM, BN>()];
-  mx_tile<IoT, BM, BN, EPI>(a, blockIdx.x, smem);
+  mx_tile<IoT, BM, BN, EPI, DIRECT>(a, blockIdx.x, smem);
 }
 
 template <typename IoT, int BM, int BN, int EPI> hipError_t launch_mx(const Mx4Gemm& a, hipStream_t s) {
-  hipLaunchKernelGGL((mx_kernel<IoT, BM, BN, EPI>), dim3(a.grid), dim3(256), 0, s, a);
+  if constexpr (ElemTraits<IoT>::bytes == 2 && EPI != EPI_PARTIAL && BM == 256) {
+    // (offsets inside a tile's rows are 31 bits)
+    if (a.g.res == nullptr && !(a.g.flags & 1) && a.g.ldc0 <= (1 << 21)) {
+      hipLaunchKernelGGL((mx_kernel<IoT, BM, BN, EPI, true>), dim3(a.tiles), dim3(256), 0, s, a);
+      return hipGetLastError();
+    }
+  }
+  hipLaunchKernelGGL((mx_kernel<IoT, BM, BN, EPI, false>), dim3(a.tiles), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

@@ -230,7 +230,7 @@ mlp_status mx4_linear_fwd(const linear_desc* d, const void* x, const void* x_sca
   a.ws_stride = mx_scale_bytes(N, K);
   a.bias_stride = N;
   a.splits = p.splits;
-  a.grid = (int)((d->experts ? row_tiles(M, d->experts, p.bm) : (M + p.bm - 1) / p.bm) * g.tiles_n * p.splits);
+  a.tiles = (int)((d->experts ? row_tiles(M, d->experts, p.bm) : (M + p.bm - 1) / p.bm) * g.tiles_n * p.splits);
   if (p.splits > 1) {
     const GemmArgs join = g;
     g.N = (int)P;

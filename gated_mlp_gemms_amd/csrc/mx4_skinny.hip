@@ -145,8 +145,8 @@ __global__ __launch_bounds__(64 * kWaves) void mx_skinny_kernel(const Mx4Gemm a)
 }
 
 template <typename IoT, bool GATED> hipError_t launch(const Mx4Gemm& a, hipStream_t s) {
-  if (a.offsets == nullptr) hipLaunchKernelGGL((mx_skinny_kernel<IoT, GATED, 1>), dim3(a.grid), dim3(64 * kWaves), 0, s, a);
-  else hipLaunchKernelGGL((mx_skinny_kernel<IoT, GATED, 4>), dim3(a.grid), dim3(64 * kWaves), 0, s, a);
+  if (a.offsets == nullptr) hipLaunchKernelGGL((mx_skinny_kernel<IoT, GATED, 1>), dim3(a.tiles), dim3(64 * kWaves), 0, s, a);
+  else hipLaunchKernelGGL((mx_skinny_kernel<IoT, GATED, 4>), dim3(a.tiles), dim3(64 * kWaves), 0, s, a);
   return hipGetLastError();
 }
 
