@@ -36,7 +36,7 @@ struct MxPlace {
   int64_t row0;
 };
 
-// Tile b of the product; false: there are no more.
+// Tile b of the product; false: there is none.
 template <int BM, int BNC>
 __device__ __forceinline__ bool mx_place(const Mx4Gemm& a, int b, MxPlace& at) {
   const int tiles_n = a.g.tiles_n;
@@ -88,14 +88,12 @@ template <int BM, int BN, bool GATED> struct MxPipe {
 
   char* smem;
   int lane, wave, wm, wn, frow, fhalf;
-  // the tile that is loaded
   DA ka;
   DB kb;
   const char* sc;        // per lane: its 16 bytes (two rows') of the first step's scales
   int64_t sc_plane;
   int rows, n0, N, b_split, k_left, planes;
   bool stacked;
-  // the tile that is multiplied
   int a_base[MI], b_base[NI];   // first tile row of each block
   u32x4 fa[2][MI], fb[2][NI];
   uint32_t sa[MI], sb[NI], na[MI], nb[NI];
@@ -237,10 +235,9 @@ template <int BM, int BN, bool GATED> struct MxPipe {
     take_scales();
     wait_lgkmcnt0();
   }
-  // The step in stage cur, whose first fragments are there; then the DMAs of step kt of the tile that is loaded (ISSUE 1: a
-  // fast one, 2: any, 0: none) into that stage, and the next stage's first fragments. YOUNGER: memory operations that may
-  // be in flight besides NS - 2 steps' DMAs, made after the next step's.
-  template <int ISSUE, int YOUNGER> __device__ __forceinline__ void step(int kt, int& cur) {
+  // The step in stage cur, whose first fragments are there; then the DMAs of step kt into that stage, and the next stage's
+  // first fragments.
+  template <bool FAST> __device__ __forceinline__ void step(int kt, int& cur) {
     const int nxt = cur + 1 == NS ? 0 : cur + 1;
     read_frags(cur, 1, 1);
     mma<0>();
@@ -253,17 +250,15 @@ template <int BM, int BN, bool GATED> struct MxPipe {
     interleave<N_MMA, N_RD, 0>();
     // the next step must have landed; after the barrier every wave is done reading this stage
     __builtin_amdgcn_sched_barrier(0);
-    wait_vmcnt<(NS - 2) * N_DMA + YOUNGER>();
+    wait_vmcnt<(NS - 2) * N_DMA>();
     wait_lgkmcnt0();
     __builtin_amdgcn_s_barrier();
-    if constexpr (ISSUE != 0) {
 #pragma unroll
-      for (int d = 0; d < N_DMA; ++d) issue_one<ISSUE == 1>(kt, cur, d);
-    }
+    for (int d = 0; d < N_DMA; ++d) issue_one<FAST>(kt, cur, d);
     read_frags(nxt, 0, 0);
     read_scales(nxt);
     mma<3>();
-    interleave<N_MMA, 2 * N_RD, ISSUE != 0 ? N_DMA : 0>();
+    interleave<N_MMA, 2 * N_RD, N_DMA>();
     take_scales();
     cur = nxt;
   }
@@ -442,8 +437,8 @@ __device__ __forceinline__ void mx_tile(const Mx4Gemm& a, int b, char* smem) {
   }
   const int fast = k.fast_steps() - NS;
   int cur = 0, kt = 0;
-  for (; kt < min(nk, fast); ++kt) k.template step<1, 0>(kt + NS, cur);
-  for (; kt < nk; ++kt) k.template step<2, 0>(kt + NS, cur);
+  for (; kt < min(nk, fast); ++kt) k.template step<true>(kt + NS, cur);
+  for (; kt < nk; ++kt) k.template step<false>(kt + NS, cur);
   if constexpr (DIRECT) {
     const auto out = __builtin_amdgcn_make_buffer_rsrc(elem_ptr<IoT>(p.C0, 0, 0, t.n0), 0, 0x7fffffff, 0x00020000);
     auto store = [&](auto fn) {

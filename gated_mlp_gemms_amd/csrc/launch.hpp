@@ -151,8 +151,9 @@ hipError_t run_moe_combine_bwd(DType dt, const void* dout, const void* ys, const
 
 hipError_t run_mx4_rows(DType dt, const void* x, int64_t batch, int64_t rows, int64_t cols, void* codes, void* scales,
                         hipStream_t s);
+// row_codes: also what run_mx4_rows gives (16-bit types), x read once.
 hipError_t run_mx4_columns(DType dt, const void* x, int64_t batch, int64_t rows, int64_t cols, void* codes, void* scales,
-                           hipStream_t s);
+                           void* row_codes, void* row_scales, hipStream_t s);
 hipError_t run_mx4_values(DType dt, const void* codes, const void* scales, int64_t batch, int64_t rows, int64_t K, void* out,
                           hipStream_t s);
 // EPI_LIN or EPI_LIN_GATED, unsplit; tiles TILE_256x256, TILE_128x128 and TILE_64x64 (gated: 64 x 128)

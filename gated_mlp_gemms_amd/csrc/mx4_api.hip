@@ -61,13 +61,17 @@ mlp_status need_rows(const void* p, int64_t elems, const char* name) {
 
 // ---- plans --------------------------------------------------------------------------------------
 
-// A K-step is 256 values deep. A gated tile has half as many units as columns.
+// A K-step is 256 values deep. A gated tile has half as many units as columns. Measured with forced tiles (us; 256^2, 128^2, 64^2):
+// 4096 x 4096 x 11008 129, 149, 225; 4096^3 44, 47, 76; 4864 x 8192 x 2048 61, 62, 81; 2048^3 21, 12.2, 16;
+// 1024 x 4096 x 4096 32, 17.8, 21.5; 512 x 4096 x 11008 34, 21, 30; 128 x 4096 x 11008 30, 15.5, 11.6; 64 x 4096 x 4096 29, 14.9,
+// 8.2. 32 experts of 2048 x 1376 gate and up: 32768 rows 150, 175, 218; 8192 48, 49, 60; 4096 43, 34, 36; 1024 39, 28, 22.
 struct MxTile { TileShape t; int bm, bn, slots; StepTime st; };
 const MxTile kMxTiles[] = {
-    {TILE_256x256, 256, 256, 1, {1.6e-6, 1.8e-6, 1.8e-6, 1.8e-6, 5e-6}},
-    {TILE_128x128, 128, 128, 2, {0.55e-6, 0.65e-6, 1.0e-6, 1.2e-6, 3e-6}},
-    {TILE_64x64, 64, 64, 2, {0.30e-6, 0.40e-6, 0.45e-6, 0.55e-6, 2e-6}},
+    {TILE_256x256, 256, 256, 1, {1.5e-6, 2.0e-6, 2.0e-6, 2.0e-6, 10e-6}},
+    {TILE_128x128, 128, 128, 2, {0.50e-6, 0.69e-6, 0.85e-6, 0.99e-6, 7e-6}},
+    {TILE_64x64, 64, 64, 2, {0.20e-6, 0.28e-6, 0.36e-6, 0.38e-6, 4.5e-6}},
 };
+const StepTime kMxWide = {0.25e-6, 0.40e-6, 0.50e-6, 0.60e-6, 5.2e-6};   // 64 x 128: 64 gated units
 
 struct MxPlan {
   bool skinny;       // few rows: run_mx4_skinny
@@ -89,16 +93,19 @@ MxPlan plan_product(const linear_desc* d) {
   }
   best.est = 1e300;
   for (const MxTile& t : kMxTiles) {
-    const int wide = t.t == TILE_64x64 && gated ? 2 * t.bn : t.bn;   // (its gate and up rows)
-    const int64_t rt = E ? std::max<int64_t>(1, M / t.bm + (std::min(M, E) + 1) / 2) : (M + t.bm - 1) / t.bm;
+    const bool wide = t.t == TILE_64x64 && gated;   // (twice the columns, for 64 gate and 64 up rows)
+    // of experts: a tile each, or all their rows and half a tile each over
+    const int64_t rt = E ? std::max(std::min(M, E), M / t.bm + (std::min(M, E) + 1) / 2) : (M + t.bm - 1) / t.bm;
     for (int s = 1; s <= (E ? 1 : 16); ++s) {
       const bool stacked = gated && s > 1;
-      const int bn = stacked ? t.bn : gated ? wide / 2 : t.bn;
+      const int bn = gated && !stacked && !wide ? t.bn / 2 : t.bn;
       const int64_t N = stacked ? 2 * d->N : d->N, tiles = rt * ((N + bn - 1) / bn);
       const int64_t kps = (steps + s - 1) / s;
       if ((steps + kps - 1) / kps != s) continue;
-      double est = tiles_time(t.st, t.slots, tiles * s, kps);
-      if (s > 1) est += (2.0 * s + 1.0) * (double)M * (double)N * 4.0 / 6.0e12 + 4e-6;   // partial sums there and back, a launch
+      double est = tiles_time(wide && !stacked ? kMxWide : t.st, t.slots, tiles * s, kps);
+      // partial sums there and back, a launch. In 1, 2, 4, 8, 16 parts (us): 64 x 16384 x 512 on 64^2 21.7, 15.2, 11.6, 9.9, 10.1;
+      // 256 x 16384 x 1024 20.6, 16.0, 13.8, 16.7, 21.9; 64 x 4096 x 4096 8.2, 9.3, 10.4, 14; 2048^3 on 128^2 12.2, 30.7, 40
+      if (s > 1) est += (2.0 * s + 1.0) * (double)M * (double)N * 4.0 / 4.5e12 + 3.5e-6;
       if (est >= best.est * 0.98) continue;
       best = {false, t.t, t.bm, bn, s, (int)(kps * (kMxPlane / 2)), est};
     }
@@ -134,8 +141,11 @@ mlp_status mx4_quantize(const void* x, int dtype, int64_t batch, int64_t rows, i
     if (p) MLP_TRY(need_ptr(p, name));
   if (n == 0) return MLP_OK;
   hipStream_t s = stream_of(stream);
-  if (codes) MLP_TRY(hip_status(run_mx4_rows(dtype_of(dtype), x, batch, rows, cols, codes, scales, s), "mx4_quantize"));
-  if (codes_t) MLP_TRY(hip_status(run_mx4_columns(dtype_of(dtype), x, batch, rows, cols, codes_t, scales_t, s), "mx4_quantize (transposed)"));
+  const bool both = codes && codes_t && dtype != MLP_F32;   // (8192 x 4096 of bf16: 23.5 us, in two launches 32.5)
+  if (codes && !both) MLP_TRY(hip_status(run_mx4_rows(dtype_of(dtype), x, batch, rows, cols, codes, scales, s), "mx4_quantize"));
+  if (codes_t)
+    MLP_TRY(hip_status(run_mx4_columns(dtype_of(dtype), x, batch, rows, cols, codes_t, scales_t, both ? codes : nullptr, scales, s),
+                       "mx4_quantize (transposed)"));
   return MLP_OK;
 }
 
