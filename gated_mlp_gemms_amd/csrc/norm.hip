@@ -425,7 +425,7 @@ __global__ __launch_bounds__(256) void norm_columns_kernel(const NormBwd a) {
 
 // The workgroups' column sums added up: 16 columns (of dweight, then of dbias) a workgroup, 4 a thread, and 64 runs of the
 // parts beside one another, joined in order: of a wave's 16 by lanes, then the four waves.
-// 512 parts of 4096 columns: bound by a handful of trips to memory (with 8 runs 4.7 us, with 64 a third of that).
+// 512 parts of 4096 columns: bound by a handful of trips to memory (with 8 runs 4.7 us, with 64 3; behind a backward that has just written them 6.9).
 constexpr int kJoinCols = 16;
 template <typename W>
 __global__ __launch_bounds__(256) void norm_join_kernel(const float* __restrict__ part, int parts, int64_t d, void* dw,
