@@ -240,7 +240,9 @@ mlp_status mx4_linear_fwd(const linear_desc* d, const void* x, const void* x_sca
   a.ws_stride = mx_scale_bytes(N, K);
   a.bias_stride = N;
   a.splits = p.splits;
-  a.tiles = (int)((d->experts ? row_tiles(M, d->experts, p.bm) : (M + p.bm - 1) / p.bm) * g.tiles_n * p.splits);
+  const int64_t tiles = (d->experts ? row_tiles(M, d->experts, p.bm) : (M + p.bm - 1) / p.bm) * g.tiles_n * p.splits;
+  if (tiles >= (int64_t)1 << 24) return fail(MLP_ERR_UNSUPPORTED, "more than 2^32 threads");   // (of 256 a tile: no launch has them)
+  a.tiles = (int)tiles;
   if (p.splits > 1) {
     const GemmArgs join = g;
     g.N = (int)P;

@@ -191,3 +191,9 @@ def test_reference_codes():
     # each value within half a step of itself: 1/4 of its power of two, or of the block's smallest step
     big = x.double().reshape(6, 3, 32).abs().amax(-1, keepdim=True).expand(6, 3, 32).reshape(6, 96)
     assert ((X.rounded(x) - x.double()).abs() <= torch.maximum(x.double().abs() / 4, big / 16)).all()
+
+
+def test_more_threads_than_a_launch_has():
+    """Few rows of many experts by a very wide weight: refused, not left to the launch."""
+    d = desc(M=8192, K=32, N=1 << 22, act="none", experts=1024)
+    assert fwd(d, up=None, ups=None, off=FAKE) == MLP_ERR_UNSUPPORTED and "threads" in err()
