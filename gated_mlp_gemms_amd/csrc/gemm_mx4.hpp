@@ -414,33 +414,47 @@ __device__ __forceinline__ void mx_tile(const Mx4Gemm& a, int b, char* smem) {
   Pipe k;
   k.init(smem);
   k.place(a, t, kbeg, kend);
-#pragma unroll
-  for (int s = 0; s < NS; ++s) k.issue(s, s);
-  wait_vmcnt<(NS - 1) * Pipe::N_DMA>();   // step 0 landed
-  k.begin();
-  if (DIRECT && p.bias0 != nullptr) {   // the sums start from the bias: a lane's columns of block j are 8 g + 4 (l / 32) + r
+  if constexpr (DIRECT) {   // the sums start from the bias: a lane's columns of block j are 8 g + 4 (l / 32) + r
     constexpr int NI = Pipe::NI, NO = epi_gated(EPI) ? NI / 2 : NI;
+    u32x2 b[NI][4];   // (beside the first stage: behind the others the sums would wait for those, too)
 #pragma unroll
     for (int j = 0; j < NI; ++j)
 #pragma unroll
       for (int g = 0; g < 4; ++g) {
         const int n = t.n0 + k.wn * (Pipe::BNC / 2) + (j % NO) * 32 + 8 * g + 4 * k.fhalf;
-        float f[4];
-        Vec4<IoT>::load(elem_ptr<IoT>(j < NO ? p.bias0 : p.bias1, 0, 0, n < p.N ? n : 0), f);
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-#pragma unroll
-          for (int i = 0; i < Pipe::MI; ++i) k.acc[i][j][4 * g + r] = f[r];
+        const void* bias = j < NO ? p.bias0 : p.bias1;
+        b[j][g] = bias != nullptr ? *reinterpret_cast<const u32x2*>(elem_ptr<IoT>(bias, 0, 0, n < p.N ? n : 0)) : u32x2{0u, 0u};
       }
+    __builtin_amdgcn_sched_barrier(0);
+    k.issue(0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int j = 0; j < NI; ++j)
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const float f = Bits16<IoT>::to_f32(r & 1 ? b[j][g][r / 2] >> 16 : b[j][g][r / 2] & 0xffffu);
+#pragma unroll
+          for (int i = 0; i < Pipe::MI; ++i) k.acc[i][j][4 * g + r] = f;
+        }
+    __builtin_amdgcn_sched_barrier(0);
   } else {
+    k.issue(0, 0);
     k.clear();
   }
+#pragma unroll
+  for (int s = 1; s < NS; ++s) k.issue(s, s);
+  wait_vmcnt<(NS - 1) * Pipe::N_DMA>();   // step 0 landed
+  k.begin();
   const int fast = k.fast_steps() - NS;
   int cur = 0, kt = 0;
   for (; kt < min(nk, fast); ++kt) k.template step<true>(kt + NS, cur);
   for (; kt < nk; ++kt) k.template step<false>(kt + NS, cur);
   if constexpr (DIRECT) {
     const auto out = __builtin_amdgcn_make_buffer_rsrc(elem_ptr<IoT>(p.C0, 0, 0, t.n0), 0, 0x7fffffff, 0x00020000);
+    // The trailing DMAs have landed: what is in flight when the workgroup ends are stores, which the next one need not wait for.
+    wait_vmcnt<0>();
     auto store = [&](auto fn) {
       mx_store_tile<IoT, decltype(fn)::value, epi_gated(EPI)>(k.acc, out, (int)p.ldc0 * 2, t.rows, p.N - t.n0, k.wm * Pipe::WM,
                                                               k.wn * (Pipe::BNC / 2), k.frow, k.fhalf);
@@ -453,7 +467,6 @@ __device__ __forceinline__ void mx_tile(const Mx4Gemm& a, int b, char* smem) {
       case FN_RELU_SQ: store(std::integral_constant<int, FN_RELU_SQ>{}); break;
       default: store(std::integral_constant<int, FN_NONE>{});
     }
-    wait_vmcnt<0>();
     return;
   }
   // the trailing DMAs have landed and no wave reads the ring any more: its LDS becomes the epilogue's staging area
