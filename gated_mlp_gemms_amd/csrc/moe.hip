@@ -299,27 +299,32 @@ template <typename F> hipError_t route_shape(int64_t E, F f) {
 
 // ---- balance loss ------------------------------------------------------------------------------
 
-// A token's probabilities, in place of its C scores a lane: softmax, or each expert's sigmoid divided by their sum (as
-// sigmoid_share). A token without any, and a lane past the row, has zeros. The exponentials are the hardware's, off by the
+// A token's probabilities, in place of its C scores a lane (-inf past the row): softmax, or each expert's sigmoid divided by their
+// sum (as sigmoid_share). A token without any, and a lane past the row, has zeros; a NaN makes its whole token NaN, through the
+// sum, as the maximum passes it over. The exponentials are the hardware's, off by the
 // rounding of their argument, |x| half steps (expf is a dozen instructions; 16384 x 128: 8.5 -> 7.1 us, the gradient 12.0 -> 11.2).
-template <int L, int C> __device__ __forceinline__ void balance_probs(int E, int lane, int sigmoid, float (&x)[C]) {
-  uint32_t m = 0u;
+// A kernel a score function: short straight code, as every launch fetches it anew (with a branch a score and score_key's maximum
+// the loss and the gradient together 22.6 us, so 20.8).
+template <int L, int C, bool SIGMOID> __device__ __forceinline__ void balance_probs(float (&x)[C]) {
+  float top = x[0];
 #pragma unroll
-  for (int j = 0; j < C; ++j) m = max(m, lane * C + j < E ? score_key(x[j]) : 0u);
-  const float top = key_score(group_max<L>(m));
-  const bool none = sigmoid ? top < -104.0f : top == -INFINITY;
-  const float shift = sigmoid ? fminf(top, 0.0f) : top;
+  for (int j = 1; j < C; ++j) top = fmaxf(top, x[j]);
+  top = __uint_as_float(group_reduce<L>(__float_as_uint(top), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+  const bool none = SIGMOID ? top < -104.0f : top == -INFINITY;
+  const float shift = none ? 0.0f : SIGMOID ? fminf(top, 0.0f) : top;
   float part = 0.0f;
 #pragma unroll
   for (int j = 0; j < C; ++j) {
-    const bool in = lane * C + j < E;
-    if (sigmoid) x[j] = in ? (x[j] < 0.0f ? __expf(x[j] - shift) / (1.0f + __expf(x[j])) : 1.0f / (1.0f + __expf(-x[j]))) : 0.0f;
-    else x[j] = in ? __expf(x[j] - shift) : 0.0f;
+    if constexpr (SIGMOID) x[j] = x[j] < 0.0f ? __expf(x[j] - shift) / (1.0f + __expf(x[j])) : 1.0f / (1.0f + __expf(-x[j]));
+    else x[j] = __expf(x[j] - shift);
     part += x[j];
   }
-  const float r = 1.0f / group_sum<L>(part);
+  const float total = group_sum<L>(part);
+  const float r = none && total == total ? 0.0f : 1.0f / total;
 #pragma unroll
-  for (int j = 0; j < C; ++j) x[j] = none ? 0.0f : x[j] * r;
+  for (int j = 0; j < C; ++j) x[j] *= r;
 }
 
 // The parts' sums added up, by one workgroup of 1024 threads: 2^sh >= E threads an expert's run of parts beside one another,
@@ -381,10 +386,10 @@ __global__ __launch_bounds__(1024) void balance_join_kernel(const float* __restr
 // finishes by itself. 16384 x 128: bound by its trips to memory, so kBalanceAtOnce tokens of a group are under way at once, and
 // the mask, read beside them, only chooses what is added (256 threads, a token at a time 15.6 us).
 constexpr int kBalanceThreads = 1024, kBalanceAtOnce = 2;
-template <typename T, int L, int C>
+template <typename T, int L, int C, bool SIGMOID>
 __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(const void* __restrict__ logits, const int* __restrict__ ids,
                                                                   const uint8_t* __restrict__ mask, int64_t tokens, int E,
-                                                                  int k, int sigmoid, int64_t chunk, float* part_p,
+                                                                  int k, int64_t chunk, float* part_p,
                                                                   int* part_c, int sh, int* __restrict__ counts,
                                                                   float* __restrict__ shares, float* __restrict__ loss) {
   constexpr int R = kBalanceThreads / L, W = kBalanceThreads / 64, U = kBalanceAtOnce;
@@ -402,12 +407,12 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(const void* __
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t t = t0 + u * R + tid / L;
-      load_scores<T, C>(logits, t, E, lane, t < end, 0.0f, x[u]);
+      load_scores<T, C>(logits, t, E, lane, t < end, -INFINITY, x[u]);
       live[u] = t < end && (mask == nullptr || mask[t] != 0);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      balance_probs<L, C>(E, lane, sigmoid, x[u]);
+      balance_probs<L, C, SIGMOID>(x[u]);
 #pragma unroll
       for (int j = 0; j < C; ++j) acc[j] += live[u] ? x[u][j] : 0.0f;
       seen += live[u] ? 1 : 0;
@@ -440,13 +445,13 @@ __global__ __launch_bounds__(kBalanceThreads) void balance_kernel(const void* __
 
 // The gradient: with a_e = dloss E counts_e / (n^2 k) and m = sum_e p_e a_e, p_e (a_e - m), of sigmoid scores times
 // 1 - q_e; on top of the chosen weights' (dweights NULL: none), both rounded once.
-template <typename T, int L, int C>
+template <typename T, int L, int C, bool SIGMOID>
 __global__ __launch_bounds__(kRouteThreads) void balance_bwd_kernel(const void* __restrict__ logits, const int* __restrict__ ids,
                                                                     const uint8_t* __restrict__ mask,
                                                                     const int* __restrict__ counts,
                                                                     const float* __restrict__ dloss,
                                                                     const float* __restrict__ dweights, int64_t tokens,
-                                                                    int E, int k, int sigmoid, int renorm,
+                                                                    int E, int k, int renorm,
                                                                     void* __restrict__ dlogits) {
   constexpr int R = kRouteThreads / L;
   const int lane = threadIdx.x & (L - 1);
@@ -462,17 +467,17 @@ __global__ __launch_bounds__(kRouteThreads) void balance_bwd_kernel(const void* 
     const int64_t t = t0 + threadIdx.x / L;
     const bool in = t < tokens, live = in && (mask == nullptr || mask[t] != 0);
     float x[C], d[C], rest[C];
-    load_scores<T, C>(logits, t, E, lane, in, 0.0f, x);   // (not `live`: the mask would be one more trip to memory first)
+    load_scores<T, C>(logits, t, E, lane, in, -INFINITY, x);   // (not `live`: the mask would be one more trip to memory first)
 #pragma unroll
-    for (int j = 0; j < C; ++j) rest[j] = sigmoid ? sigmoid_of(x[j]).rest : 1.0f;
-    balance_probs<L, C>(E, lane, sigmoid, x);
+    for (int j = 0; j < C; ++j) rest[j] = SIGMOID ? sigmoid_of(x[j]).rest : 1.0f;
+    balance_probs<L, C, SIGMOID>(x);
     float part = 0.0f;
 #pragma unroll
     for (int j = 0; j < C; ++j) part = __builtin_fmaf(x[j], a[j], part);
     const float m = group_sum<L>(part);
 #pragma unroll
     for (int j = 0; j < C; ++j) d[j] = live ? x[j] * rest[j] * (a[j] - m) : 0.0f;
-    if (dweights != nullptr) route_grad<T, L, C>(logits, ids, dweights, t, in, E, k, sigmoid, renorm, d);
+    if (dweights != nullptr) route_grad<T, L, C>(logits, ids, dweights, t, in, E, k, SIGMOID, renorm, d);
     if (in) store_scores<T, C>(dlogits, t, E, lane, d);
   }
 }
@@ -775,9 +780,10 @@ hipError_t run_moe_balance(DType dt, const void* logits, const int* ids, const u
   if (parts > 0) {
     const hipError_t e = by_type(dt, [&](auto v) {
       return route_shape(E, [&](auto l, auto c) {
-        hipLaunchKernelGGL((balance_kernel<decltype(v), decltype(l)::value, decltype(c)::value>), dim3(parts),
-                           dim3(kBalanceThreads), 0, s, logits, ids, mask, T, E, k, sigmoid, balance_chunk(T, E), part_p,
-                           part_c, sh, counts, shares, loss);
+        constexpr int L = decltype(l)::value, C = decltype(c)::value;
+        const auto kernel = sigmoid ? balance_kernel<decltype(v), L, C, true> : balance_kernel<decltype(v), L, C, false>;
+        hipLaunchKernelGGL(kernel, dim3(parts), dim3(kBalanceThreads), 0, s, logits, ids, mask, T, E, k, balance_chunk(T, E),
+                           part_p, part_c, sh, counts, shares, loss);
         return hipGetLastError();
       });
     });
@@ -793,8 +799,9 @@ hipError_t run_moe_balance_bwd(DType dt, const void* logits, const int* ids, con
   return by_type(dt, [&](auto v) {
     return route_shape(E, [&](auto l, auto c) {
       constexpr int L = decltype(l)::value, C = decltype(c)::value, R = kRouteThreads / L;
-      hipLaunchKernelGGL((balance_bwd_kernel<decltype(v), L, C>), dim3(item_grid(T, R)), dim3(kRouteThreads), 0, s, logits,
-                         ids, mask, counts, dloss, dweights, T, E, k, sigmoid, renorm, dlogits);
+      const auto kernel = sigmoid ? balance_bwd_kernel<decltype(v), L, C, true> : balance_bwd_kernel<decltype(v), L, C, false>;
+      hipLaunchKernelGGL(kernel, dim3(item_grid(T, R)), dim3(kRouteThreads), 0, s, logits, ids, mask, counts, dloss, dweights, T,
+                         E, k, renorm, dlogits);
       return hipGetLastError();
     });
   });
