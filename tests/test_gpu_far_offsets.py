@@ -8,6 +8,7 @@ import moe_reference as R
 import norm_reference as N
 from gpu_helpers import announce
 from test_gpu_moe import DEV, gen, normal, offsets_of
+from test_gpu_mx4 import check_product
 
 pytestmark = pytest.mark.gpu
 U8, BF = torch.uint8, torch.bfloat16
@@ -76,6 +77,11 @@ def test_product_of_many_rows():
     for i in range(0, reps, 1025):
         R.check(f"rows from {i * n}", y[i], ref, bound)
     assert (y == y[0]).all()
+
+
+def test_product_of_many_columns():
+    """Rows too long for offsets of 31 bits inside a large tile."""
+    check_product(257, 32, (1 << 21) + 8, "none", BF, residual=False)
 
 
 @pytest.mark.parametrize("rows", [2, 40])

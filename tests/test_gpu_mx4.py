@@ -214,6 +214,30 @@ def test_large_products_activations(act):
         check_product(3001, 96, 1544, act, dt, experts=4, offsets=offsets_of([1000, 0, 1500, 401]), residual=False)
 
 
+PARTS = [  # long K with few tiles: parts of K, on tiles of 64, 128 and 256
+    (40, 8224, 264, R.ACTS), (130, 16416, 136, ("none", "geglu")), (300, 12320, 264, ("relu", "swiglu")),
+    (775, 30752, 432, ("swiglu",)), (1772, 37536, 1160, ("swiglu",)),
+]
+
+
+@pytest.mark.parametrize("M,K,N,acts", PARTS)
+@pytest.mark.parametrize("dtype", list(R.DT))
+def test_products_in_parts(M, K, N, acts, dtype):
+    for i, act in enumerate(acts):
+        desc = gm.make_linear_desc(M, K, N, act=act, dtype=R.DT[dtype])
+        assert gm.mx4_linear_workspace_bytes(desc) >= 2 * M * N * 4
+        check_product(M, K, N, act, R.DT[dtype], bias=i % 3 != 1, residual=i % 2 == 0, seed=i)
+
+
+@pytest.mark.parametrize("counts,tail,K,N", [([2500, 0, 2701], 300, 288, 2312), ([4000, 513], 0, 544, 2056)])
+@pytest.mark.parametrize("dtype", list(R.DT))
+def test_many_rows_of_experts(counts, tail, K, N, dtype):
+    for act in ("none", "swiglu"):
+        for residual in (True, False):
+            check_product(sum(counts) + tail, K, N, act, R.DT[dtype], experts=len(counts), offsets=offsets_of(counts),
+                          residual=residual)
+
+
 EXPERTS = [  # rows an expert, rows behind them, K, N
     ([1], 0, 32, 8), ([0], 3, 64, 24), ([5], 0, 288, 136), ([0, 1, 0, 2], 0, 2080, 72), ([1, 0, 0, 16, 17, 3], 5, 160, 264),
     ([40, 0, 3], 9, 544, 40), ([130, 7, 0, 64, 129], 0, 288, 392), ([0, 0, 300, 0], 20, 96, 136),
