@@ -158,3 +158,27 @@ def test_balance():
     assert d.any() and is_again(d, d[:n])
     ref, size = N.balance_bwd(logits, out[0][0], k, mask, float(n), "softmax")
     R.check("dlogits", d[:n], ref, R.half_step(BF) * ref.abs() + 1e-5 * size + R.floor_of(BF))
+
+
+@pytest.mark.parametrize("M,K,N", [(3, (1 << 24) + 32, 40), (70, (1 << 24) + 96, 72), (300, (1 << 22) + 64, 264)])
+def test_product_of_long_rows(M, K, N):
+    """Rows nearly as long as they may be, of -1, 0 and 1 under scales of 1: every sum is a whole number below 2^24, so exact."""
+    announce(f"mx4 product {M} x {K} x {N}")
+    g = gen(6)
+    value = torch.tensor([0.0, 1.0, -1.0], device=DEV, dtype=torch.float64)
+    code = torch.tensor([0, 2, 10], device=DEV, dtype=U8)
+
+    def operand(rows):
+        pick = torch.randint(0, 3, (rows, K), device=DEV, generator=g, dtype=U8).int()
+        b = blocks(rows, K)
+        b[0].copy_(code[pick[:, ::2]] | code[pick[:, 1::2]] << 4)
+        b[1].zero_()
+        scales = torch.zeros(b[1].shape[0] * 8, dtype=U8, device=DEV)
+        scales[: K // 32] = 127
+        b[1][:, :rows] = scales.reshape(-1, 1, 8)
+        return b, value[pick]
+
+    (x, xv), (w, wv) = operand(M), operand(N)
+    y = torch.empty(M, N, device=DEV)
+    gm.mx4_linear_fwd(gm.make_linear_desc(M, K, N, dtype=torch.float32), *x, *w, y)
+    assert torch.equal(y.double(), xv @ wv.T)
