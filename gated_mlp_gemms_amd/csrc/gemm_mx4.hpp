@@ -485,7 +485,8 @@ __global__ __launch_bounds__(256, 1) void mx_kernel(const Mx4Gemm a) {
 
 template <typename IoT, int BM, int BN, int EPI> hipError_t launch_mx(const Mx4Gemm& a, hipStream_t s) {
   if constexpr (ElemTraits<IoT>::bytes == 2 && EPI != EPI_PARTIAL && BM == 256) {
-    // (offsets inside a tile's rows are 31 bits)
+    // (offsets inside a tile's rows are 31 bits; tiles of 128 x 128, two on a CU, are no faster so: 1024 x 4096 x 4096 17.9 us through
+    // LDS and 18.5, 512 x 4096 x 11008 22.5 and 22.5)
     if (a.g.res == nullptr && !(a.g.flags & 1) && a.g.ldc0 <= (1 << 21)) {
       hipLaunchKernelGGL((mx_kernel<IoT, BM, BN, EPI, true>), dim3(a.tiles), dim3(256), 0, s, a);
       return hipGetLastError();
