@@ -49,7 +49,6 @@ mlp_status check_product(const linear_desc* d) {
     return fail(MLP_ERR_UNSUPPORTED, "a leading dimension (K, N, or 2N gated) is 2^25 elements or more");
   if (d->M > kElems / P || d->M > kElems / d->K || E * P > kElems / d->K)
     return fail(MLP_ERR_UNSUPPORTED, "a matrix of the problem has more than 2^37 elements");
-  if ((d->M / 64 + E + 1) * ((P + 63) / 64) >= (int64_t)1 << 31) return fail(MLP_ERR_UNSUPPORTED, "more than 2^31 tiles");
   if (d->K % kMxBlock) return fail(MLP_ERR_ALIGNMENT, "K must be a multiple of %d (whole blocks)", kMxBlock);
   if (d->N % 8) return fail(MLP_ERR_ALIGNMENT, "N must be a multiple of 8");
   return MLP_OK;
@@ -73,22 +72,31 @@ const MxTile kMxTiles[] = {
 };
 const StepTime kMxWide = {0.25e-6, 0.40e-6, 0.50e-6, 0.60e-6, 5.2e-6};   // 64 x 128: 64 gated units
 
+// Tiles of a launch, of 256 threads each: 2^32 threads are more than one can have. (With 16 x 16 tiles of few rows an expert by a
+// very wide weight; larger tiles then take them.)
+constexpr int64_t kMostTiles = ((int64_t)1 << 24) - 1;
+
 struct MxPlan {
   bool skinny;       // few rows: run_mx4_skinny
   TileShape tile;
   int bm, bn;        // rows and output columns of a tile
   int splits, kps;   // parts of K, bytes of codes of one
+  int tiles;         // of the launch, those of every part; 0: no tile is large enough for kMostTiles
   double est;
 };
 
 MxPlan plan_product(const linear_desc* d) {
   const bool gated = is_gated(d->act);
   const int64_t M = d->M, E = d->experts, steps = mx_planes(d->K);
+  auto launched = [&](int64_t bm, int64_t bn, int64_t columns) {
+    return (E ? row_tiles(M, E, bm) : (M + bm - 1) / bm) * ((columns + bn - 1) / bn);
+  };
   MxPlan best{};
-  if (M <= (E ? kMxExpertRows * E : kMxSkinnyRows)) {
+  best.splits = 1;
+  if (M <= (E ? kMxExpertRows * E : kMxSkinnyRows) && launched(16, 16, d->N) <= kMostTiles) {
     best.skinny = true;
     best.bm = best.bn = 16;
-    best.splits = 1;
+    best.tiles = (int)launched(16, 16, d->N);
     return best;
   }
   best.est = 1e300;
@@ -101,21 +109,28 @@ MxPlan plan_product(const linear_desc* d) {
       const int bn = gated && !stacked && !wide ? t.bn / 2 : t.bn;
       const int64_t N = stacked ? 2 * d->N : d->N, tiles = rt * ((N + bn - 1) / bn);
       const int64_t kps = (steps + s - 1) / s;
-      if ((steps + kps - 1) / kps != s) continue;
+      if ((steps + kps - 1) / kps != s || launched(t.bm, bn, N) * s > kMostTiles) continue;
       double est = tiles_time(wide && !stacked ? kMxWide : t.st, t.slots, tiles * s, kps);
       // partial sums there and back, a launch. In 1, 2, 4, 8, 16 parts (us): 64 x 16384 x 512 on 64^2 21.7, 15.2, 11.6, 9.9, 10.1;
       // 256 x 16384 x 1024 20.6, 16.0, 13.8, 16.7, 21.9; 64 x 4096 x 4096 8.2, 9.3, 10.4, 14; 2048^3 on 128^2 12.2, 30.7, 40
       if (s > 1) est += (2.0 * s + 1.0) * (double)M * (double)N * 4.0 / 4.5e12 + 3.5e-6;
       if (est >= best.est * 0.98) continue;
-      best = {false, t.t, t.bm, bn, s, (int)(kps * (kMxPlane / 2)), est};
+      best = {false, t.t, t.bm, bn, s, (int)(kps * (kMxPlane / 2)), (int)(launched(t.bm, bn, N) * s), est};
     }
   }
   return best;
 }
 
-size_t partial_bytes(const linear_desc* d, const MxPlan& p) {
+// A valid descriptor's plan (without rows: none is needed), and its workspace.
+mlp_status make_plan(const linear_desc* d, MxPlan& p) {
+  MLP_TRY(check_product(d));
+  p = d->M == 0 ? MxPlan{} : plan_product(d);
+  if (d->M > 0 && p.tiles == 0) return fail(MLP_ERR_UNSUPPORTED, "the product's tiles are more than 2^32 threads");
+  return MLP_OK;
+}
+size_t workspace_of(const linear_desc* d, const MxPlan& p) {
   const int64_t P = is_gated(d->act) ? 2 * d->N : d->N;
-  return p.splits > 1 ? (size_t)p.splits * (size_t)d->M * (size_t)P * sizeof(float) : 0;
+  return p.splits > 1 ? round_up((size_t)p.splits * (size_t)d->M * (size_t)P * sizeof(float)) : kAlign;
 }
 
 }  // namespace
@@ -162,15 +177,16 @@ mlp_status mx4_dequantize(const void* codes, const void* scales, int dtype, int6
 }
 
 size_t mx4_linear_workspace_bytes(const linear_desc* d) {
-  if (check_product(d) != MLP_OK) return 0;
-  return std::max(kAlign, d->M == 0 ? 0 : round_up(partial_bytes(d, plan_product(d))));
+  MxPlan p;
+  return make_plan(d, p) == MLP_OK ? workspace_of(d, p) : 0;
 }
 
 mlp_status mx4_linear_fwd(const linear_desc* d, const void* x, const void* x_scales, const void* w,
                           const void* w_scales, const void* w_up, const void* w_up_scales, const void* bias,
                           const void* bias_up, const void* residual, const int32_t* offsets, void* y, void* preact,
                           void* ws, size_t ws_bytes, void* stream) {
-  MLP_TRY(check_product(d));
+  MxPlan p;
+  MLP_TRY(make_plan(d, p));
   const bool gated = is_gated(d->act);
   MLP_TRY(need_rows(x, d->M, "x"));
   MLP_TRY(need_rows(x_scales, d->M, "x_scales"));
@@ -193,7 +209,7 @@ mlp_status mx4_linear_fwd(const linear_desc* d, const void* x, const void* x_sca
   else MLP_TRY(need_null(offsets, "offsets", "unless desc->experts"));
   MLP_TRY(need_rows(y, d->M, "y"));
   if (preact) MLP_TRY(need_ptr(preact, "preact"));
-  const size_t need = mx4_linear_workspace_bytes(d);
+  const size_t need = workspace_of(d, p);
   if (ws_bytes < need)
     return fail(MLP_ERR_WORKSPACE, "workspace of %zu bytes is smaller than the %zu needed", ws_bytes, need);
   MLP_TRY(need_ptr(ws, "workspace"));
@@ -202,7 +218,6 @@ mlp_status mx4_linear_fwd(const linear_desc* d, const void* x, const void* x_sca
   hipStream_t s = stream_of(stream);
   const DType io = dtype_of(d->dtype);
   const int64_t M = d->M, N = d->N, K = d->K, P = gated ? 2 * N : N;
-  const MxPlan p = plan_product(d);
   Mx4Gemm a{};
   GemmArgs& g = a.g;
   g.alpha = 1.0f;
@@ -240,9 +255,7 @@ mlp_status mx4_linear_fwd(const linear_desc* d, const void* x, const void* x_sca
   a.ws_stride = mx_scale_bytes(N, K);
   a.bias_stride = N;
   a.splits = p.splits;
-  const int64_t tiles = (d->experts ? row_tiles(M, d->experts, p.bm) : (M + p.bm - 1) / p.bm) * g.tiles_n * p.splits;
-  if (tiles >= (int64_t)1 << 24) return fail(MLP_ERR_UNSUPPORTED, "more than 2^32 threads");   // (of 256 a tile: no launch has them)
-  a.tiles = (int)tiles;
+  a.tiles = p.tiles;
   if (p.splits > 1) {
     const GemmArgs join = g;
     g.N = (int)P;

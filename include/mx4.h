@@ -14,6 +14,10 @@
  *           blocks behind the last are 0, rows behind the last are not read as data.
  * A product's tile reads 256 values of its rows at a time, whose scales are one run of memory that way.
  * A batch of matrices is one after another. Buffers' addresses are 16-byte aligned.
+ *
+ * Size limits (MLP_ERR_UNSUPPORTED, before any HIP call): rows and M <= 2^29, columns, K and N (gated: 2 N) < 2^25,
+ * a batch <= 65535, MOE_MAX_EXPERTS experts, 2^37 elements a matrix (all experts' weights are one); and a product
+ * must fit a launch: its tiles, at most 256 x 256, are below 2^24 (beyond, only many experts of millions of columns).
  */
 #ifndef GATED_MLP_MX4_H
 #define GATED_MLP_MX4_H
@@ -51,7 +55,7 @@ mlp_status mx4_dequantize(const void* codes, const void* scales, int dtype, int6
  * (W^T)^T from dy's blocks along N and W^T's, dW [N, K] = dy^T (x^T)^T from the transposed blocks of both (rows that were
  * added as zeros add nothing). residual may be y, which adds to it.
  */
-size_t mx4_linear_workspace_bytes(const linear_desc* desc);   /* 0 for an invalid descriptor, else >= 256 */
+size_t mx4_linear_workspace_bytes(const linear_desc* desc);   /* 0 for what mx4_linear_fwd refuses, else >= 256 */
 mlp_status mx4_linear_fwd(const linear_desc* desc, const void* x, const void* x_scales, const void* w,
                           const void* w_scales, const void* w_up, const void* w_up_scales, const void* bias,
                           const void* bias_up, const void* residual, const int32_t* offsets, void* y, void* preact,
