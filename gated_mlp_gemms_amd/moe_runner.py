@@ -140,30 +140,32 @@ class MoeRunner:
                    offsets=self.offsets, preact=preact, workspace=self.ws)
         linear_fwd(self.down_desc, self.a, self.w2, self.ys, bias=self.b2, offsets=self.offsets, workspace=self.ws)
 
-    def _forward(self, preact):
+    def _forward(self, train):
         if self.norm is not None:
-            norm_fwd(self.stream, self.x, weight=self.norm_weight, bias=self.norm_bias, mean=self.mean, rstd=self.rstd,
-                     kind=self.norm)
+            norm_fwd(self.stream, self.x, weight=self.norm_weight, bias=self.norm_bias, mean=self.mean if train else None,
+                     rstd=self.rstd if train else None, kind=self.norm)
         if self.wide_router is not self.router:
             self.wide_router[: self.experts].copy_(self.router)
         linear_fwd(self.r_desc, self.x, self.wide_router, self.wide_logits, workspace=self.ws)
         if self.wide_logits is not self.logits:
             self.logits.copy_(self.wide_logits[:, : self.experts])
         moe_route(self.logits, self.ids, self.weights, score=self.score, renorm=self.renorm)
-        if self.balance:
+        if train and self.balance:
             moe_balance(self.logits, self.ids, self.counts, self.shares, self.loss, mask=self.mask, score=self.score,
                         workspace=self.ws)
         moe_sort(self.ids, self.experts, self.offsets, self.row_of, self.slot_of, workspace=self.ws)
         moe_gather(self.x, self.slot_of, self.offsets, self.xs)
-        self._experts(preact)
+        self._experts(self.preact if train else None)
         moe_combine(self.ys, self.weights, self.row_of, self.offsets, self.out, residual=self.residual)
         return self.out
 
     def forward(self):
-        return self._forward(self.preact)
+        return self._forward(True)
 
     def forward_infer(self):
-        return self._forward(None)
+        """The output alone: the balance loss with its loads, the norm's statistics and the pre-activation stay as
+        :meth:`forward` left them."""
+        return self._forward(False)
 
     def backward(self):
         """Every gradient of :meth:`forward` against ``dout`` (and ``balance`` times the balance loss); ``dx`` is the sum
