@@ -30,15 +30,15 @@ class MoeRunner:
     [experts, hidden, width]; w_down or w2 [experts, width, hidden]; optional b_gate, b_up or b1, b_down or b2; optional
     residual [tokens, width], added to the output in x's place: its gradient is dout, which dx then leaves out.
     ``train`` False holds no more than ``forward_infer`` needs.
-    ``norm`` "layer" or "rms": the layer works on norm(x) (tensors norm_weight, optional norm_bias [width]), x being the
-    residual stream. ``balance`` above 0: ``forward`` leaves the balance loss in ``loss`` [1] and the experts' loads in
+    ``norm`` "layer" or "rms": the layer works on norm(x) (tensors norm_weight, optional norm_bias [width]; ``eps`` the
+    norm's), x being the residual stream. ``balance`` above 0: ``forward`` leaves the balance loss in ``loss`` [1] and the experts' loads in
     ``counts`` and ``shares``, and the gradients are those of the layer's loss plus ``balance`` times it; optional
     mask [tokens] (bool): the tokens that it counts. ``mx4`` (``train`` False): the experts' weights are held as
     4-bit blocks, made here and by :meth:`quantize_weights`, and their inputs are rounded to them; width and hidden
     are multiples of 32."""
 
     def __init__(self, *, act, dtype, tokens, width, hidden, experts, choices, tensors, score="softmax", renorm=True,
-                 train=True, device="cuda", norm=None, balance=0.0, mx4=False):
+                 train=True, device="cuda", norm=None, balance=0.0, mx4=False, eps=1e-5):
         if norm is not None and "residual" in tensors:
             raise ValueError("with a norm the residual stream is x itself")
         if norm not in (None, "layer", "rms"):
@@ -53,7 +53,8 @@ class MoeRunner:
         n = T * k
         self.train, self.score, self.renorm, self.experts, self.dtype = train, score, renorm, E, dt
         self.x, self.router, self.residual = t["x"], t["router"], t.get("residual", t["x"])
-        self.norm, self.balance, self.mx4, self.mask = norm, float(balance) if train else 0.0, mx4, t.get("mask")
+        self.norm, self.eps, self.mx4 = norm, float(eps), mx4
+        self.balance, self.mask = float(balance) if train else 0.0, t.get("mask")
         self.w1, self.w_up, self.w2 = t["w_gate" if gated else "w1"], t.get("w_up"), t["w_down" if gated else "w2"]
         self.b1, self.b_up, self.b2 = t.get("b_gate" if gated else "b1"), t.get("b_up"), t.get("b_down" if gated else "b2")
 
@@ -143,7 +144,7 @@ class MoeRunner:
     def _forward(self, train):
         if self.norm is not None:
             norm_fwd(self.stream, self.x, weight=self.norm_weight, bias=self.norm_bias, mean=self.mean if train else None,
-                     rstd=self.rstd if train else None, kind=self.norm)
+                     rstd=self.rstd if train else None, kind=self.norm, eps=self.eps)
         if self.wide_router is not self.router:
             self.wide_router[: self.experts].copy_(self.router)
         linear_fwd(self.r_desc, self.x, self.wide_router, self.wide_logits, workspace=self.ws)
