@@ -167,7 +167,10 @@ __global__ __launch_bounds__(norm_threads<L>()) void norm_fwd_kernel(const NormF
 
 constexpr int kLongThreads = 1024;
 
-// Rows that registers do not hold: three passes over the row, the later ones from the caches.
+// Rows that registers do not hold: three passes over the row, the later ones from the caches. At most kLongGrid workgroups, which
+// then take several rows, as item_grid's do, but at a number of rows that memory holds and a test reaches: 2^16 rows are 8.6 GB
+// a tensor at least (131072 x 65544 bf16 with 2^16 and 2^20 workgroups 9.2-9.5 and 9.2-9.6 ms).
+constexpr int64_t kLongGrid = 1 << 16;
 template <typename T, typename W>
 __global__ __launch_bounds__(kLongThreads) void norm_fwd_long_kernel(const NormFwd a) {
   constexpr int N = Piece<T>::N, L = kLongThreads;
@@ -514,7 +517,7 @@ hipError_t run_norm_fwd(DType dt, bool wide, const void* x, const void* res, con
     using T = decltype(t);
     using W = decltype(v);
     if (pieces > kNormPieces) {
-      hipLaunchKernelGGL((norm_fwd_long_kernel<T, W>), dim3(item_grid(rows, 1)), dim3(kLongThreads), 0, s, a);
+      hipLaunchKernelGGL((norm_fwd_long_kernel<T, W>), dim3((unsigned)std::min(rows, kLongGrid)), dim3(kLongThreads), 0, s, a);
       return hipGetLastError();
     }
     auto launch = [&](auto shape) {
