@@ -176,7 +176,7 @@ hipError_t run_norm_fwd(DType dt, bool wide, const void* x, const void* res, con
                         int pieces, int64_t d, int layer, float eps, void* y, void* h, float* mean, float* rstd,
                         hipStream_t s);
 // part: fp32 [norm_parts][2][d], where dw or db is asked for.
-int norm_parts(int64_t rows, int pieces);
+int norm_parts(int64_t rows, int pieces, bool fp32);
 hipError_t run_norm_bwd(DType dt, bool wide, const void* dy, const void* h, const float* mean, const float* rstd,
                         const void* w, const void* dres, int64_t rows, int pieces, int64_t d, void* dx, void* dw,
                         void* db, int accumulate, float* part, hipStream_t s);

@@ -495,16 +495,20 @@ template <typename F> hipError_t norm_shape(int pieces, F f) {
 
 }  // namespace
 
-// Workgroups of a backward: a multiple of the CUs whose column sums are at most some 20 MB. Backward and join with 256, 512 and 1024
-// (us): 8192 rows of 4096 bf16 64 + 3, 57 + 3, 61 + 11; 4096 of 8192 63 + 4, 69 + 12, 76 + 21; 5003 of 1024 fp32 -, 20 + 3, 17 + 3.
-int norm_parts(int64_t rows, int pieces) {
+// Workgroups of a backward, a multiple of the 256 CUs that falls with the width, since each writes its column sums for the join to
+// read: 2^18 / pieces rounded up to it, at most 1024; 256 for 16-bit rows beyond 768 pieces, where a workgroup has 8 waves and a
+// piece's sums 64 bytes. Together the sums are at most 25 MB up to there and 34 MB at 2048 pieces; of fp32 rows half. Backward and join with
+// 256, 512 and 1024 (us): 8192 rows of 4096 bf16 64 + 3, 57 + 3, 61 + 11; 4096 of 8192 63 + 4, 69 + 12, 76 + 21; 5003 of 1024 fp32
+// -, 20 + 3, 17 + 3. Calls with 256 and 512: 8192 of 5120 bf16 (640 pieces) 122 and 97, 5003 of 6144 (768) 83 and 70, of 6152 75 and 80;
+// 7168: 512 rows 20 and 27, 2048 41 and 49, 8192 125 and 133; 8192 of 8152 132 and 140; 8192 of 3584 fp32 (896) 104 and 98.
+int norm_parts(int64_t rows, int pieces, bool fp32) {
   if (pieces > kNormBwdPieces) return (int)std::min<int64_t>(rows, 64);
   int r = 1;
   (void)norm_shape(pieces, [&](auto s) {
     r = decltype(s)::rows;
     return hipSuccess;
   });
-  const int64_t most = std::min<int64_t>(1024, ((1 << 18) / pieces + 255) / 256 * 256);
+  const int64_t most = !fp32 && pieces > 768 ? 256 : std::min<int64_t>(1024, ((1 << 18) / pieces + 255) / 256 * 256);
   return (int)std::min<int64_t>((rows + r - 1) / r, most);
 }
 
@@ -536,7 +540,7 @@ hipError_t run_norm_bwd(DType dt, bool wide, const void* dy, const void* h, cons
   const NormBwd a{static_cast<const u32x4*>(dy), static_cast<const u32x4*>(h), mean, rstd, w,
                   static_cast<const u32x4*>(dres), static_cast<u32x4*>(dx), sums ? part : nullptr, rows, pieces,
                   1.0f / (float)d};
-  const int parts = norm_parts(rows, pieces);
+  const int parts = norm_parts(rows, pieces, dt == DT_F32);
   return norm_types(dt, wide, [&](auto t, auto v) {
     using T = decltype(t);
     using W = decltype(v);

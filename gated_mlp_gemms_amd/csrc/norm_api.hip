@@ -67,7 +67,7 @@ mlp_status norm_fwd(const norm_desc* q, const void* x, const void* residual, con
 size_t norm_workspace_bytes(int64_t M, int64_t d) {
   if (check_size(M, d) != MLP_OK) return 0;
   // the parts of either element size (a row has d / 4 pieces at most, d / 8 at least)
-  const int parts = std::max(norm_parts(M, (int)((d + 3) / 4)), norm_parts(M, (int)((d + 7) / 8)));
+  const int parts = std::max(norm_parts(M, (int)((d + 3) / 4), true), norm_parts(M, (int)((d + 7) / 8), false));
   return std::max<size_t>(round_up((size_t)parts * 2 * (size_t)d * sizeof(float)), kAlign);
 }
 
