@@ -2,6 +2,8 @@
 // the weight's and bias' gradients. Bound by HBM: a row is read once, held in registers as it was loaded, and written once.
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "rows.hpp"
 
 namespace gmlp {
@@ -168,8 +170,8 @@ __global__ __launch_bounds__(norm_threads<L>()) void norm_fwd_kernel(const NormF
 constexpr int kLongThreads = 1024;
 
 // Rows that registers do not hold: three passes over the row, the later ones from the caches. At most kLongGrid workgroups, which
-// then take several rows, as item_grid's do, but at a number of rows that memory holds and a test reaches: 2^16 rows are 8.6 GB
-// a tensor at least (131072 x 65544 bf16 with 2^16 and 2^20 workgroups 9.2-9.5 and 9.2-9.6 ms).
+// then take several rows, as item_grid's do, but at a number of rows that memory holds and a test reaches (with 2^16 and 2^20 workgroups:
+// 131072 x 16392 bf16 1.84 and 1.89 ms, x 65544 9.2-9.5 and 9.2-9.6; 100000 x 32776 fp32 7.1 both).
 constexpr int64_t kLongGrid = 1 << 16;
 template <typename T, typename W>
 __global__ __launch_bounds__(kLongThreads) void norm_fwd_long_kernel(const NormFwd a) {
@@ -473,7 +475,14 @@ template <typename F> hipError_t norm_types(DType dt, bool wide, F f) {
 
 template <int L, int P> struct NormShape { static constexpr int lanes = L, per = P, rows = L < 256 ? 256 / L : 1; };
 
-constexpr int kNormPieces = 8192, kNormBwdPieces = 2048;   // the widest rows that registers hold
+// The widest rows that registers hold in the backward, and in the forward with 8 pieces a thread. There bf16 rows, and fp16 rows with
+// fp32 weights, would spill (190 bytes a thread): they are long rows. Forward held, and as a long row (us): fp32 4096 x 12288 85 and
+// 90, 4096 x 16384 120 and 135, 2048 x 32768 120 and 159; fp16 with its own weights 4096 x 16392 85 and 72, 4096 x 20000 90 and 87,
+// 1024 x 65536 61 and 85; bf16 4096 x 16392 239 and 65, 4096 x 20000 258 and 82, 1024 x 65536 119 and 85, 16 x 20000 10.4 and 5.5; fp16 with
+// fp32 weights 242 and 73, 260 and 92, 120 and 85, 10.7 and 5.6.
+constexpr int kNormBwdPieces = 2048, kNormPieces = 8192;
+template <typename T, typename W>
+constexpr int norm_held = std::is_same<T, bf16>::value || sizeof(W) != sizeof(T) ? kNormBwdPieces : kNormPieces;
 
 // f(NormShape) for rows of `pieces` pieces: few of them a thread, so that the backward's column sums (two fp32 an element)
 // leave room for several waves, and as few lanes idle as three pieces a thread allow. 8192 rows of 4096 bf16, residual, lanes x pieces
@@ -520,7 +529,7 @@ hipError_t run_norm_fwd(DType dt, bool wide, const void* x, const void* res, con
   return norm_types(dt, wide, [&](auto t, auto v) {
     using T = decltype(t);
     using W = decltype(v);
-    if (pieces > kNormPieces) {
+    if (pieces > norm_held<T, W>) {
       hipLaunchKernelGGL((norm_fwd_long_kernel<T, W>), dim3((unsigned)std::min(rows, kLongGrid)), dim3(kLongThreads), 0, s, a);
       return hipGetLastError();
     }
@@ -529,7 +538,10 @@ hipError_t run_norm_fwd(DType dt, bool wide, const void* x, const void* res, con
       hipLaunchKernelGGL((norm_fwd_kernel<T, W, L, P>), dim3(item_grid(rows, TH / L)), dim3(TH), 0, s, a);
       return hipGetLastError();
     };
-    return pieces > kNormBwdPieces ? launch(NormShape<1024, 8>{}) : norm_shape(pieces, launch);
+    if constexpr (norm_held<T, W> > kNormBwdPieces) {
+      if (pieces > kNormBwdPieces) return launch(NormShape<1024, 8>{});
+    }
+    return norm_shape(pieces, launch);
   });
 }
 

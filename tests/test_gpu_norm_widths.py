@@ -21,3 +21,16 @@ def test_column_sums_of_every_number_of_workgroups(M, pieces, dt):
     x, r, w, b = make(g, M, d, dt, True)
     h, mean, rstd = check_fwd(x, r, w, b if kind == "layer" else None, kind)
     check_bwd(normal(g, M, d, dtype=dt), h, mean, rstd, w, normal(g, M, d, dtype=dt), kind, True)
+
+
+@pytest.mark.parametrize("M", [1, 300])
+@pytest.mark.parametrize("pieces", [2047, 2048, 2049, 3001, 8191])
+@pytest.mark.parametrize("dt", list(R.DT.values()))
+def test_forward_of_wide_rows(M, pieces, dt):
+    d = pieces * (4 if dt == F32 else 8)
+    for kind in ("layer", "rms"):
+        announce(f"norm forward {M} x {d} {kind} {dt}")
+        for wide in ((True,) if dt == F32 else (False, True)):
+            x, r, w, b = make(gen(pieces + M), M, d, dt, wide)
+            check_fwd(x, r, w, b if kind == "layer" else None, kind)
+            check_fwd(x, None, None, None, kind)

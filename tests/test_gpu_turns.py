@@ -32,15 +32,17 @@ def assert_again(name, t, base):
     assert torch.equal(t[whole:], base[: t.shape[0] - whole]), name
 
 
-# 16-byte pieces a row, rows a workgroup, workgroups of a launch: every width that sums over several waves of a workgroup
-FORWARD = [(65, 2, 1 << 20), (193, 1, 1 << 20), (257, 2, 1 << 20), (385, 1, 1 << 20), (2049, 1, 1 << 20), (8193, 1, 1 << 16)]
+# 16-byte pieces a row, rows a workgroup, log2 of a launch's workgroups, type: every width that sums over several waves of a workgroup
+BF, F32 = torch.bfloat16, torch.float32
+FORWARD = [(65, 2, 20, BF), (193, 1, 20, BF), (257, 2, 20, BF), (385, 1, 20, BF), (2049, 1, 20, F32), (2049, 1, 16, BF),
+           (8193, 1, 16, F32)]
 
 
-@pytest.mark.parametrize("pieces,per,groups", FORWARD)
+@pytest.mark.parametrize("pieces,per,groups,dt", FORWARD)
 @pytest.mark.parametrize("kind", ["layer", "rms"])
-def test_norm_forward(pieces, per, groups, kind):
-    rows, d, dt = groups * per * (9 if pieces > 8192 else 5) // 4 + 37, pieces * 8, torch.bfloat16
-    announce(f"norm forward of {rows} x {d}, {kind}")
+def test_norm_forward(pieces, per, groups, dt, kind):
+    rows, d = (per * (9 if groups == 16 else 5) << groups) // 4 + 37, pieces * (4 if dt == F32 else 8)
+    announce(f"norm forward of {rows} x {d} {dt}, {kind}")
     g = gen(pieces)
     x, r, w = normal(g, 61, d, dtype=dt), normal(g, 61, d, dtype=dt), normal(g, d, dtype=dt)
     x *= torch.linspace(0.25, 4, 61, device=DEV)[:, None].to(dt)   # rows whose sums are far from one another's
