@@ -6,10 +6,12 @@
 // substep s of four the lane half h takes block 4 h + s, so a lane's four scales of a step are the four bytes of one word, which
 // the instruction picks from by number.
 //
-// Four waves, 2 x 2, one a SIMD. Large products are bound by power: with random operands the 4-bit MFMA alone runs at 6 PFLOP/s
-// of its 8.4 with constant ones, with its LDS reads at 4.9, and with the DMAs a 256 x 256 tile's step takes 2.1 us
-// (4.1 PFLOP/s; 1.5 us with constant operands). Half steps of 64 bytes in a ring of four were no faster (a DMA of half lines
-// takes 1.28 us a step by itself, of whole ones 1.05).
+// Four waves, 2 x 2, one a SIMD. A 256 x 256 tile's step, one on every CU, takes 1.8 us with random operands (4.8 PFLOP/s; 2.0
+// beyond 64 steps) and 1.4 with constant ones; the 4-bit MFMA alone runs at 6 PFLOP/s with random operands (power: 8.4 with constant
+// ones), with its LDS reads at 4.9. Beside its steps a tile takes 10 us to start and end, in which its CU multiplies nothing, and a
+// launch 4: 4096 x 4096 outputs, one round of 256 tiles, take 28 us at K = 2048, 42 at 4096, 72 at 8192, 129 at 16384 (2.5, 3.2,
+// 3.8 and 4.3 PFLOP/s). At K = 2048 constant operands take 26.5: what short K loses there is not power. Half steps of 64 bytes in a
+// ring of four were no faster (a DMA of half lines takes 1.28 us a step by itself, of whole ones 1.05).
 #pragma once
 
 #include "gemm_dma.hpp"

@@ -163,7 +163,9 @@ hipError_t run_mx4_linear_f32(int epi, TileShape tile, const Mx4Gemm& a, hipStre
 // Few rows: 16 rows of one weight by 16 columns a workgroup. Taken up to kMxSkinnyRows rows of one weight, and up to
 // kMxExpertRows an expert on average. Streamed and in tiles (us): 16 rows of 4096 x 11008 8.9 and 9.3, 32 14.8 and 9.3, 32 of
 // 1024 x 1024 4.2 and 5.5, 16 of 2048 x 5504 gate and up 6.0 and 8.1; 64 experts of 2048 x 1376 gate and up, 2 rows each 42 and 48, 4 41
-// and 45, 8 43 and 45, 16 48 and 45; 16 experts of 4096 x 1024, 16 rows each 11.3 and 9.5.
+// and 45, 8 43 and 45, 16 48 and 45; 16 experts of 4096 x 1024, 16 rows each 11.3 and 9.5. The host does not know each expert's rows. Of
+// the same gate and up, rows even, falling as 1 / rank, and all on four experts (whose weights are read anew for every 16 rows):
+// 512 of 64 experts 46 and 47, 48 and 45, 23 and 9; 256 of 64 40 and 45, 36 and 35, 15 and 9; 1024 of 128 85 and 87, 94 and 87, 45 and 13.
 constexpr int kMxSkinnyRows = 16, kMxExpertRows = 8;
 hipError_t run_mx4_skinny(DType io, int gated, const Mx4Gemm& a, hipStream_t s);
 // fp32 sums of a.splits parts of K, a.g.partial [splits][M][N]; B1: more rows of B from a.g.b_split on

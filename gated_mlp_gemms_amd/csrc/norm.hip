@@ -373,7 +373,8 @@ __global__ __launch_bounds__(norm_threads<L>()) void norm_bwd_kernel(const NormB
 }
 
 // Rows whose column sums registers do not hold: dx a workgroup a row in two passes, and the column sums by themselves, a
-// thread a piece of the width over every gridDim.y-th row.
+// thread a piece of the width over every gridDim.y-th row: dy and h are read three times, once from the caches. 4096 x 16384 fp32,
+// residual: 223 us for 1.07 GB, 104 for 0.54 and a join of 5, where 192 would carry each byte once.
 template <typename T, typename W>
 __global__ __launch_bounds__(kLongThreads) void norm_dx_long_kernel(const NormBwd a) {
   constexpr int N = Piece<T>::N, L = kLongThreads;

@@ -31,11 +31,11 @@ class MoeRunner:
     residual [tokens, width], added to the output in x's place: its gradient is dout, which dx then leaves out.
     ``train`` False holds no more than ``forward_infer`` needs.
     ``norm`` "layer" or "rms": the layer works on norm(x) (tensors norm_weight, optional norm_bias [width]; ``eps`` the
-    norm's), x being the residual stream. ``balance`` above 0: ``forward`` leaves the balance loss in ``loss`` [1] and the experts' loads in
-    ``counts`` and ``shares``, and the gradients are those of the layer's loss plus ``balance`` times it; optional
-    mask [tokens] (bool): the tokens that it counts. ``mx4`` (``train`` False): the experts' weights are held as
-    4-bit blocks, made here and by :meth:`quantize_weights`, and their inputs are rounded to them; width and hidden
-    are multiples of 32."""
+    norm's), x being the residual stream. ``balance`` above 0: ``forward`` leaves the balance loss in ``loss`` [1] and the
+    experts' loads in ``counts`` and ``shares``, and the gradients are those of the layer's loss plus ``balance`` times it; optional
+    mask [tokens] (bool): the tokens that it counts. ``mx4`` (``train`` False): the experts work on 4-bit
+    blocks of their weights, made here and by :meth:`quantize_weights` from the weights, which stay held beside them, and
+    their inputs are rounded to blocks; width and hidden are multiples of 32."""
 
     def __init__(self, *, act, dtype, tokens, width, hidden, experts, choices, tensors, score="softmax", renorm=True,
                  train=True, device="cuda", norm=None, balance=0.0, mx4=False, eps=1e-5):

@@ -10,7 +10,8 @@ of the two uint8 tensors that hold a matrix. A 4-bit layer, weights quantised on
     mx4_quantize(x, xq, xs)
     mx4_linear_fwd(desc, xq, xs, wq, ws, y)
 
-and its backward, with the transposed blocks that ``mx4_quantize`` writes next to the others::
+and, of one weight without an activation, its backward's products, with the transposed blocks that ``mx4_quantize`` writes
+next to the others (no bias' gradient; of experts ``dx`` only)::
 
     mx4_quantize(w, codes_t=wt, scales_t=wts)                # once: W^T, blocks along N
     mx4_quantize(x, codes_t=xt, scales_t=xts)

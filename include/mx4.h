@@ -51,9 +51,11 @@ mlp_status mx4_dequantize(const void* codes, const void* scales, int dtype, int6
 /*
  * linear_fwd (moe.h) on 4-bit operands: the same formula, on the values that x [M, K] and w (w_up iff gated)
  * [N, K] or [E, N, K] stand for; desc->dtype is that of bias, residual, y and preact. Products and sums in fp32,
- * rounded once. K a multiple of 32, N of 8. With blocks of the transposed matrices it is a layer's backward, too: dx [M, K] = dy
- * (W^T)^T from dy's blocks along N and W^T's, dW [N, K] = dy^T (x^T)^T from the transposed blocks of both (rows that were
- * added as zeros add nothing). residual may be y, which adds to it.
+ * rounded once. K a multiple of 32, N of 8. With blocks of the transposed matrices it gives the products of the backward of a layer
+ * without an activation, too: dx [M, K] = dy (W^T)^T from dy's blocks along N and W^T's (of experts [E, K, N]), and of one weight
+ * dW [N, K] = dy^T (x^T)^T from the transposed blocks of both (rows that were added as zeros add nothing; an expert's
+ * rows do not end where blocks do). Neither dy through an activation nor a bias' gradient is formed. residual may be y, which
+ * adds to it.
  */
 size_t mx4_linear_workspace_bytes(const linear_desc* desc);   /* 0 for what mx4_linear_fwd refuses, else >= 256 */
 mlp_status mx4_linear_fwd(const linear_desc* desc, const void* x, const void* x_scales, const void* w,
