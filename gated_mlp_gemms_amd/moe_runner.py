@@ -142,6 +142,7 @@ class MoeRunner:
         linear_fwd(self.down_desc, self.a, self.w2, self.ys, bias=self.b2, offsets=self.offsets, workspace=self.ws)
 
     def _forward(self, train):
+        preact = self.preact if train else None
         if self.norm is not None:
             norm_fwd(self.stream, self.x, weight=self.norm_weight, bias=self.norm_bias, mean=self.mean if train else None,
                      rstd=self.rstd if train else None, kind=self.norm, eps=self.eps)
@@ -156,7 +157,7 @@ class MoeRunner:
                         workspace=self.ws)
         moe_sort(self.ids, self.experts, self.offsets, self.row_of, self.slot_of, workspace=self.ws)
         moe_gather(self.x, self.slot_of, self.offsets, self.xs)
-        self._experts(self.preact if train else None)
+        self._experts(preact)
         moe_combine(self.ys, self.weights, self.row_of, self.offsets, self.out, residual=self.residual)
         return self.out
 

@@ -17,7 +17,8 @@
  *
  * Size limits (MLP_ERR_UNSUPPORTED, before any HIP call): rows and M <= 2^29, columns, K and N (gated: 2 N) < 2^25,
  * a batch <= 65535, MOE_MAX_EXPERTS experts, 2^37 elements a matrix (all experts' weights are one); and a product
- * must fit a launch: its tiles, at most 256 x 256, are below 2^24 (beyond, only many experts of millions of columns).
+ * must fit a launch: its tiles, of 256 x 256 at most (gated: 256 x 128), are fewer than 2^24 (only many experts with
+ * millions of columns have more).
  */
 #ifndef GATED_MLP_MX4_H
 #define GATED_MLP_MX4_H
